@@ -139,9 +139,9 @@ def lib():
 
 
 def declared_symbols(header: str | None = None):
-    """Names of the entry points include/ar.h declares."""
-    header = header or os.path.join(_build.INCLUDE, "ar.h")
-    text = open(header).read()
+    """Names of the entry points include/ar.h and ar_ops.h declare (or the given header)."""
+    headers = [header] if header else [os.path.join(_build.INCLUDE, f) for f in ("ar.h", "ar_ops.h")]
+    text = "".join(open(h).read() for h in headers)
     return sorted(set(re.findall(r"AR_API\s+[^;(]*?\b(ar_\w+)\s*\(", text)))
 
 

@@ -39,7 +39,7 @@ def sources():
 
 def _deps():
     return sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
-                        if f.endswith((".h", ".cuh"))] + [os.path.join(INCLUDE, "ar.h")]
+                        if f.endswith((".h", ".cuh"))] + [os.path.join(INCLUDE, f) for f in sorted(os.listdir(INCLUDE))]
 
 
 def up_to_date() -> bool:

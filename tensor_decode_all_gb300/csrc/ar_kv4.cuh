@@ -1,0 +1,82 @@
+// ar_kv4.cuh -- the 4-bit cache's tile layout and small helpers of the
+// operators of include/ar_ops.h.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "ar_ops.h"
+
+namespace tda {
+
+constexpr int kTileTokens = 16;   // tokens of a tile
+constexpr int kGroup = 32;        // channels that share a scale
+
+__host__ __device__ constexpr int tile_bytes(int D) { return 18 * D; }
+__host__ __device__ constexpr int tile_v(int D) { return 8 * D; }
+__host__ __device__ constexpr int tile_ks(int D) { return 16 * D; }
+__host__ __device__ constexpr int tile_vs(int D) { return 17 * D; }
+
+// The 32-bit word that holds token r's K channels 32*j + 8*t .. + 7 (nibble i: channel + i).
+__host__ __device__ constexpr int k_word(int G, int r, int t, int j) { return (r * 4 + t) * G + j; }
+// The word whose half r % 2 holds token r's V channels 32*j + 4*g .. + 3.
+__host__ __device__ constexpr int v_word(int G, int r, int g, int j) {
+    return ((r >> 3) * 32 + g * 4 + ((r & 7) >> 1)) * G + j;
+}
+
+template <typename T> struct Elem;
+template <> struct Elem<__half> {
+    static __device__ float to_float(__half x) { return __half2float(x); }
+    static __device__ __half from_float(float x) { return __float2half_rn(x); }
+};
+template <> struct Elem<__nv_bfloat16> {
+    static __device__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+    static __device__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
+};
+
+__device__ __forceinline__ float bf16_bits(uint32_t bits) { return __uint_as_float(bits << 16); }
+
+// Eight 16-bit elements: one 16-byte access where the address allows it.
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, bool vec, float (&x)[8]) {
+    union { uint4 v; T e[8]; } u;
+    if (vec) {
+        u.v = *reinterpret_cast<const uint4 *>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u.e[i] = p[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = Elem<T>::to_float(u.e[i]);
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T *p, bool vec, const float (&x)[8]) {
+    union { uint4 v; T e[8]; } u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u.e[i] = Elem<T>::from_float(x[i]);
+    if (vec) {
+        *reinterpret_cast<uint4 *>(p) = u.v;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = u.e[i];
+    }
+}
+
+// Whether rows at p with these strides (elements of 2 bytes) all start on 16 bytes.
+inline bool rows_aligned(const void *p, int64_t a, int64_t b) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && a % 8 == 0 && b % 8 == 0;
+}
+
+inline bool misaligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+// The launch's own error, not one left by an earlier call of the program.
+inline int launch_status(cudaError_t e) {
+    if (e == cudaSuccess) return AR_OK;
+    (void)cudaGetLastError();
+    return AR_ECUDA;
+}
+
+}  // namespace tda

@@ -1,0 +1,164 @@
+// ar_kv_plan.cu -- ar_kv_plan: block tables and slot maps from the requests' lengths.
+//
+// Two running sums over the requests (new tokens, new pages) give every new
+// token and page its place; each token then finds its request by bisection.
+// Every block makes the whole sums for itself in shared memory (at most 8192
+// requests, a few passes of one block) and writes its share of the tokens; the
+// blocks are one cluster, whose barrier stands between the reads of lens and
+// *free_used and their writes, so that both may be updated in place.
+#include "ar_kv4.cuh"
+
+namespace {
+
+using namespace tda;
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanRequests = 8192;
+
+struct Sums {
+    long long tokens, pages;
+};
+
+__device__ __forceinline__ Sums warp_scan(Sums x) {
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const long long a = __shfl_up_sync(~0u, x.tokens, d), b = __shfl_up_sync(~0u, x.pages, d);
+        if ((threadIdx.x & 31) >= d) {
+            x.tokens += a;
+            x.pages += b;
+        }
+    }
+    return x;
+}
+
+__device__ __forceinline__ int pages_of(int64_t tokens, int page) { return (int)((tokens + page - 1) / page); }
+
+// The last b with start[b] <= i, of n (start is non-decreasing, start[0] = 0 <= i).
+__device__ __forceinline__ int find(const int *start, int n, int i) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (start[mid] <= i) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ar_kv_plan_args a) {
+    extern __shared__ int sh[];
+    int *len = sh, *token0 = sh + a.requests, *page0 = token0 + a.requests;
+    __shared__ Sums warp_sums[kPlanThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int used = a.free_used[0];
+    Sums carry = {0, 0};
+    int bad = used < 0 ? 1 : 0;   // bit 0: AR_EINVAL, bit 1: AR_ETOOBIG
+    for (int base = 0; base < a.requests; base += kPlanThreads) {
+        const int b = base + threadIdx.x;
+        const bool in = b < a.requests;
+        const int n = in ? a.lens[b] : 0, m = in ? a.new_tokens[b] : 0;
+        Sums x = {0, 0};
+        if (n < 0 || m < 0 || (int64_t)n + m > 0x7fffffff) {
+            bad |= 1;
+        } else {
+            const int had = pages_of(n, a.page), all = pages_of((int64_t)n + m, a.page);
+            x = {m, all - had};
+            if (all > a.table_width) bad |= 2;
+            else if (m > 0 && n % a.page && a.table[(int64_t)b * a.table_stride + n / a.page] < 0) bad |= 1;
+        }
+        const Sums own = x;
+        x = warp_scan(x);
+        if (lane == 31) warp_sums[warp] = x;
+        __syncthreads();
+        if (warp == 0) warp_sums[lane] = warp_scan(warp_sums[lane]);
+        __syncthreads();
+        Sums before = carry;
+        if (warp > 0) {
+            before.tokens += warp_sums[warp - 1].tokens;
+            before.pages += warp_sums[warp - 1].pages;
+        }
+        if (in) {
+            // kept within 32 bits: past them the plan is refused and these are not read
+            len[b] = n;
+            token0[b] = (int)min(before.tokens + x.tokens - own.tokens, 0x7fffffffll);
+            page0[b] = (int)min(before.pages + x.pages - own.pages, 0x7fffffffll);
+        }
+        carry.tokens += warp_sums[kPlanThreads / 32 - 1].tokens;
+        carry.pages += warp_sums[kPlanThreads / 32 - 1].pages;
+        __syncthreads();
+    }
+    if (carry.tokens > a.max_tokens) bad |= 2;
+    if (carry.tokens > 0x7fffffff || (long long)used + carry.pages > 0x7fffffff) bad |= 1;
+    const bool invalid = __syncthreads_or(bad & 1), big = __syncthreads_or(bad & 2);
+    const int status = invalid ? AR_EINVAL : big ? AR_ETOOBIG : (long long)used + carry.pages > a.free_count ? AR_ENOMEM : AR_OK;
+    const int tokens = status ? 0 : (int)carry.tokens, pages = status ? 0 : (int)carry.pages;
+
+    // Every block of the cluster has read what follows may overwrite.
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+
+    const int first = blockIdx.x * kPlanThreads + threadIdx.x, stride = gridDim.x * kPlanThreads;
+    for (int b = first; b < a.requests; b += stride) {
+        const int end = b + 1 < a.requests ? token0[b + 1] : tokens;
+        a.lens_out[b] = len[b] + (status ? 0 : end - token0[b]);
+        a.cu[b] = status ? 0 : token0[b];
+    }
+    for (int i = first; i < pages; i += stride) {
+        const int b = find(page0, a.requests, i);
+        a.table[(int64_t)b * a.table_stride + pages_of(len[b], a.page) + i - page0[b]] = a.free_pages[used + i];
+    }
+    for (int i = first; i < a.max_tokens; i += stride) {
+        int64_t slot = -1;
+        int b = -1, p = -1;
+        if (i < tokens) {
+            b = find(token0, a.requests, i);
+            p = len[b] + i - token0[b];
+            const int col = p / a.page, had = pages_of(len[b], a.page);
+            const int64_t id = col < had ? a.table[(int64_t)b * a.table_stride + col] : a.free_pages[used + page0[b] + col - had];
+            slot = id * a.page + p % a.page;
+        }
+        a.slots[i] = slot;
+        a.request[i] = b;
+        a.position[i] = p;
+    }
+    if (first == 0) {
+        a.cu[a.requests] = tokens;
+        a.free_used_out[0] = used + pages;
+        a.status[0] = status;
+    }
+}
+
+}  // namespace
+
+extern "C" AR_API int ar_kv_plan(const ar_kv_plan_args *args, ar_stream_t stream) {
+    if (!args) return AR_EINVAL;
+    const ar_kv_plan_args &a = *args;
+    if (a.requests < 0 || a.table_width < 0 || a.page < kTileTokens || a.page % kTileTokens || a.max_tokens < 0 ||
+        a.free_count < 0 || a.table_stride < a.table_width)
+        return AR_EINVAL;
+    if (a.requests > kPlanRequests) return AR_ETOOBIG;
+    if (!a.free_used || !a.free_used_out || !a.status || !a.cu) return AR_EINVAL;
+    if (a.requests > 0 && (!a.lens || !a.new_tokens || !a.lens_out || (!a.table && a.table_width > 0))) return AR_EINVAL;
+    if (a.max_tokens > 0 && (!a.slots || !a.request || !a.position)) return AR_EINVAL;
+    if (a.free_count > 0 && !a.free_pages) return AR_EINVAL;
+    for (const void *p : {(const void *)a.lens, (const void *)a.new_tokens, (const void *)a.table, (const void *)a.free_pages,
+                          (const void *)a.free_used, (const void *)a.lens_out, (const void *)a.cu, (const void *)a.request,
+                          (const void *)a.position, (const void *)a.free_used_out, (const void *)a.status})
+        if (misaligned(p, 4)) return AR_EINVAL;
+    if (misaligned(a.slots, 8)) return AR_EINVAL;
+    // One block while its threads have about one token each, else a cluster of 8.
+    const int blocks = a.max_tokens > 2 * kPlanThreads ? 8 : 1;
+    const size_t smem = (size_t)a.requests * 3 * sizeof(int);
+    if (cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanRequests * 12) != cudaSuccess)
+        return launch_status(cudaErrorUnknown);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)blocks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return launch_status(cudaLaunchKernelEx(&cfg, plan_kernel, a));
+}
