@@ -138,7 +138,8 @@ AR_API int ar_kv4_load(const ar_kv4_rows_args *args, ar_stream_t stream);
  * stays inside the buffers; outputs of such requests are undefined), and AR_ETIMEOUT
  * after a copy into shared memory that did not arrive.
  * Results do not depend on the order in which blocks run.
- * Errors: AR_EINVAL, AR_ETOOBIG (requests > 8192), AR_ECUDA.
+ * Errors: AR_EINVAL, AR_ETOOBIG (requests > 8192, tokens * query heads of a kv
+ * head > 2^30, or a window > 2^30 shorter than the table), AR_ECUDA.
  */
 typedef struct ar_kv4_attend_args {
     const void *q;          /* [tokens][q_heads][head_dim] by its strides, channels contiguous */
