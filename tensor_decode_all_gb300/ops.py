@@ -282,18 +282,23 @@ def kv4_load(pool, slots, dtype=None, *, out=None, stream=None):
 
 # ---------------------------------------------------------------- attention
 
+def _capturing(stream, dev):
+    with _stream(stream, dev)[1]:
+        return _torch.cuda.is_current_stream_capturing()
+
+
 _workspaces = {}
 _workspace_lock = threading.Lock()
 
 
 class Kv4Workspace:
     """Working memory of kv4_attend on one device: one for calls that may overlap on the GPU.  Calls
-    without one share a workspace of their stream's, which lives as long as the process."""
+    without one share a workspace of their stream's (see kv4_workspace), which lives as long as the process."""
 
     def __init__(self, device=None, stream=None):
         torch = _torch or _T()
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-        if torch.cuda.is_current_stream_capturing():
+        if _capturing(stream, dev):
             raise RuntimeError("a kv4_attend workspace cannot be made while a CUDA graph is captured: "
                                "make it (or call kv4_attend once on this stream) before")
         raw, where = _stream(stream, dev)
@@ -316,7 +321,10 @@ class Kv4Workspace:
 
 
 def kv4_workspace(device=None, stream=None) -> Kv4Workspace:
-    """The workspace that kv4_attend uses on this stream when it is given none."""
+    """The workspace that kv4_attend uses on this stream when it is given none.
+
+    Calls that are being captured share one of their device's, made with the first workspace on it:
+    graphs that may run at the same time need one each (``workspace=``)."""
     torch = _torch or _T()
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     raw = _stream(stream, dev)[0]
@@ -325,6 +333,12 @@ def kv4_workspace(device=None, stream=None) -> Kv4Workspace:
         with _workspace_lock:
             ws = _workspaces.get((dev.index, raw))
             if ws is None:
+                if _capturing(stream, dev):
+                    ws = _workspaces.get((dev.index, "capture"))
+                    return ws if ws is not None else Kv4Workspace(dev, stream)    # which says why it cannot
+                if (dev.index, "capture") not in _workspaces:
+                    _workspaces[dev.index, "capture"] = Kv4Workspace(dev, stream)
+                    (torch.cuda.ExternalStream(raw, device=dev) if raw else torch.cuda.default_stream(dev)).synchronize()
                 ws = _workspaces[dev.index, raw] = Kv4Workspace(dev, stream)
     return ws
 
