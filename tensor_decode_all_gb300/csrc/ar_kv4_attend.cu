@@ -1,9 +1,11 @@
 // ar_kv4_attend.cu -- ar_kv4_attend: attention over the 4-bit paged cache.
 //
-// A block of four warps takes rows of one request and kv head (8 NT query rows:
-// new tokens x heads of the group) over a run of the request's tokens; runs of
-// all requests are cut evenly over the blocks of one resident grid, and what a
-// cut separates is joined by the last block to arrive.
+// A warp takes 8 or 16 query rows (new tokens x heads) of one request and kv
+// head over a run of the request's tokens, with its own ring of stages in shared
+// memory and no other warp to wait for.  The runs cut the chunks of all
+// requests, heads and row blocks, laid end to end, into equal shares, one to a
+// warp of a resident grid; where a cut separates a row's tokens the partial results go to
+// the workspace, and a second, small kernel joins them in order.
 //
 // The products are S^T = K Q^T and O^T = V^T P^T (mma.m16n8k16, fp16 operands,
 // binary32 sums), with the tokens (channels) as the 16 rows and the query rows
@@ -18,7 +20,8 @@
 // it still a normal number, whatever the scales.
 //
 // Each warp reads its tokens on its own: a ring of stages in shared memory,
-// filled by bulk copies (a tile is 18 D contiguous bytes) one stage or more ahead.
+// filled by bulk copies (a tile is 18 D contiguous bytes) a stage ahead, the
+// next segment's first stages before the last one's results are written.
 #include <type_traits>
 
 #include "ar_kv4.cuh"
@@ -27,31 +30,41 @@ namespace {
 
 using namespace tda;
 
-constexpr int kWarps = 4;
-constexpr int kThreads4 = kWarps * 32;
 constexpr int kMaxRequests = 8192;
-constexpr int kMaxGrid = 1024;            // blocks a workspace has room for
+constexpr int kWarps = 4;                 // warps of a block; each works alone
 constexpr float kNoScore = -3.0e38f;      // below every score; finite, so that differences are numbers
 constexpr int kHead = 8;                  // weights stand near 2^kHead ...
 constexpr int kLead = 6;                  // ... and may pass it by 2^kLead before the reference moves
 
-// Workspace: [0] status; from 4096: counters, one to a block; from 16384: two partial results to a block.
-constexpr size_t kCounterAt = 4096, kPartAt = 16384;
-constexpr size_t kWorkspaceBytes = kPartAt + (16u << 20);
+// Workspace: status, a record for each warp, and two partial results to a warp.
+struct Record {
+    int parts;                      // of the segment that begins in the warp and ends in another; 0: there is none
+    int rows, kv, row0, first;      // as in Segment
+    int unused[3];
+};
+constexpr int kMaxWarps = 2048;
+constexpr size_t kRecordAt = 256, kPartAt = kRecordAt + kMaxWarps * sizeof(Record);
+constexpr size_t kWorkspaceBytes = kPartAt + (24u << 20);
+static_assert(kPartAt % 256 == 0, "partial results start on a line");
 
 struct Attend {
     ar_kv4_attend_args a;
     int group;        // query heads of a kv head
     int vec_q, vec_o;
-    int min_chunks;   // least chunks worth a block of their own
+    int min_chunks;   // least share of a warp
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], const uint32_t b0, const uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, float c0, float c1,
+                                         float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    mma16816(d, a, b0, b1, d[0], d[1], d[2], d[3]);
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -94,6 +107,19 @@ __device__ __forceinline__ void nibbles_to_half(uint32_t w, uint32_t (&h)[4]) {
     }
 }
 
+// The 8 nibbles of w as fp16 pairs in the same order, the pairs 0 and 2 as
+// 256 + u and 1 and 3 as 16 + u: a nibble in the upper bits of a mantissa is a
+// whole number above a power of two.  What is too much, kOver0 or kOver1 of each, is
+// taken out of the sums (see the products with q).
+constexpr float kOver0 = 256 + 8, kOver1 = 16 + 8;
+__device__ __forceinline__ void nibbles_over(uint32_t w, uint32_t (&h)[4]) {
+    const uint32_t lo = w << 2, hi = w >> 6, k256 = 0x5c005c00u, k16 = 0x4c004c00u;
+    asm("lop3.b32 %0, %1, 0x003c003c, %2, 0xea;" : "=r"(h[0]) : "r"(lo), "r"(k256));
+    asm("lop3.b32 %0, %1, 0x03c003c0, %2, 0xea;" : "=r"(h[1]) : "r"(lo), "r"(k16));
+    asm("lop3.b32 %0, %1, 0x003c003c, %2, 0xea;" : "=r"(h[2]) : "r"(hi), "r"(k256));
+    asm("lop3.b32 %0, %1, 0x03c003c0, %2, 0xea;" : "=r"(h[3]) : "r"(hi), "r"(k16));
+}
+
 // N words from shared memory in the widest accesses (the address is a multiple of 4 N, up to 16).
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
@@ -111,26 +137,22 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
     }
 }
 
-template <int D_, int NT_, int CT_, int S_>
+template <int D_, int NT_, int CT_, int S_, int Blocks_>
 struct Shape {
     static constexpr int D = D_;              // head dim
     static constexpr int NT = NT_;            // 8-row tiles of query rows
     static constexpr int CT = CT_;            // tiles of a chunk, the unit of work and a stage of the ring
     static constexpr int S = S_;              // stages
+    static constexpr int Blocks = Blocks_;    // of an SM, for which registers are kept
     static constexpr int G = D / kGroup;
     static constexpr int Tokens = CT * kTileTokens;
     static constexpr int Rows = 8 * NT;
-    static constexpr bool QShared = NT > 2;   // q operands in shared memory, for want of registers
+    // One row tile: the constants that nibbles stand on come out of K's sums; with more of them subtracting before
+    // the products costs less, each nibble serving all (and needs no registers for what to take out).
+    static constexpr bool Over = NT == 1;
     static constexpr int Stage = CT * tile_bytes(D);
-    static constexpr int Ring = kWarps * S * Stage;
-    static constexpr int OStride = D + 4;     // floats of a row in the exchange: conflict-free for 16-byte stores
-    static constexpr int Exchange = kWarps * Rows * (OStride + 2) * 4;
-    static constexpr int QBytes = QShared ? D / 16 * NT * 32 * 8 : 0;
-    static constexpr int Data = Ring > Exchange ? Ring : Exchange;
-    static constexpr int Smem = Data + QBytes;
+    static constexpr int Smem = kWarps * S * Stage;
     static constexpr size_t PartFloats = (size_t)Rows * (D + 2);   // rows, then their references and sums
-    static constexpr size_t Fit = (kWorkspaceBytes - kPartAt) / (2 * PartFloats * 4);
-    static constexpr int MaxGrid = Fit < kMaxGrid ? (int)Fit : kMaxGrid;
 };
 
 // What a request asks for.
@@ -143,19 +165,18 @@ template <class C>
 __device__ __forceinline__ Request request_of(const Attend &c, int b) {
     const ar_kv4_attend_args &a = c.a;
     Request r;
-    int *status = static_cast<int *>(a.workspace);
     r.len = a.lens[b];
     r.first = a.cu ? a.cu[b] : b;
     const int end = a.cu ? a.cu[b + 1] : b + 1;
     const long long room = (long long)a.table_width * a.page;
     if (r.len < 0 || r.len > room || r.first < 0 || end < r.first || end > a.tokens) {
-        atomicCAS(status, 0, AR_EINVAL);
+        atomicCAS(static_cast<int *>(a.workspace), 0, AR_EINVAL);
         r.len = min(max(r.len, 0), (int)min(room, 0x7fffffffll));
         r.first = min(max(r.first, 0), a.tokens);
     }
     r.count = max(min(end, a.tokens) - r.first, 0);
-    r.blocks = (int)(((long long)r.count * c.group + C::Rows - 1) / C::Rows);
-    const int all = max((r.len + C::Tokens - 1) / C::Tokens, 1);
+    r.blocks = (r.count * c.group + C::Rows - 1) / C::Rows;
+    const int all = max((int)(((long long)r.len + C::Tokens - 1) / C::Tokens), 1);
     r.chunks = all;
     if (a.window) {
         const int sink = (int)min((long long)all, ((long long)a.sinks + C::Tokens - 1) / C::Tokens);
@@ -169,37 +190,79 @@ __device__ __forceinline__ Request request_of(const Attend &c, int b) {
     return r;
 }
 
-// Wait for a stage's copies, with a limit (about a second, and a millisecond
-// once one has run out), after which the status says so and the caller goes on
-// with what is there.
-__device__ __forceinline__ void wait_stage(uint32_t bar, uint32_t parity, bool &late, int *status) {
-    for (int i = 0; i < (late ? 1 << 10 : 1 << 20); ++i) {
+// A segment: a run of the chunks of one row block of one kv head of a request.
+struct Segment {
+    int rows, kv, row0, first;      // query rows, kv head, first row (token x group), first row of q of the request
+    int pos0, pos_lo, pos_hi;       // position of the request's first new token, of the rows' first and last
+    int c0, chunks;                 // chunks c0 .. c0 + chunks - 1 of those that its rows see
+    int sink_chunks, low_chunk;     // chunk i is i below sink_chunks, i + low_chunk - sink_chunks from there on
+    int request;
+    bool whole, begins;             // all of its row block; its beginning
+};
+
+__device__ __forceinline__ int chunk_at(const Segment &s, int i) {
+    return i < s.sink_chunks ? i : s.low_chunk + i - s.sink_chunks;
+}
+
+__device__ __forceinline__ long long now_ns() {
+    long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+
+// Wait for the phase of that parity to end, with a limit (four seconds) after
+// which the status says so and the answer is false.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int *status) {
+    long long begun = 0;
+    for (;;) {
         uint32_t done;
-        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000; selp.u32 %0, 1, 0, p; }"
-                     : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-        if (done) return;
+        for (int i = 0; i < 64; ++i) {
+            asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                         : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+            if (done) return true;
+        }
+        const long long t = now_ns();
+        if (begun == 0) begun = t;
+        if (t - begun > 4000000000ll) break;
     }
-    late = true;
     atomicCAS(status, 0, AR_ETIMEOUT);
+    return false;
+}
+
+// A row's result: divided by its sum, rounded; 0 and -infinity where nothing was seen.
+template <typename T>
+__device__ __forceinline__ void store_row(const Attend &c, long long token, int head, int channel, float4 v, float m, float sum) {
+    const ar_kv4_attend_args &a = c.a;
+    const float inv = sum > 0 ? __fdiv_rn(1.0f, sum) : sum == sum ? 0.0f : sum;
+    T *dst = static_cast<T *>(a.out) + token * a.out_token_stride + (long long)head * a.out_head_stride + channel;
+    union { uint2 u; T e[4]; } w;
+    w.e[0] = Elem<T>::from_float(v.x * inv); w.e[1] = Elem<T>::from_float(v.y * inv);
+    w.e[2] = Elem<T>::from_float(v.z * inv); w.e[3] = Elem<T>::from_float(v.w * inv);
+    if (c.vec_o) {
+        *reinterpret_cast<uint2 *>(dst) = w.u;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i] = w.e[i];
+    }
+    if (channel == 0 && a.lse)
+        a.lse[token * a.q_heads + head] = sum > 0 ? (m + log2f(sum)) * 0.6931471805599453f : sum == sum ? -INFINITY : sum;
 }
 
 template <typename T, class C>
-__global__ void __launch_bounds__(kThreads4) attend_kernel(const __grid_constant__ Attend c) {
-    constexpr int D = C::D, NT = C::NT, CT = C::CT, S = C::S, G = C::G, Rows = C::Rows;
+__global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __grid_constant__ Attend c) {
+    constexpr int D = C::D, NT = C::NT, CT = C::CT, S = C::S, G = C::G;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) unsigned long long bars[kWarps * S];
-    __shared__ long long sums[kWarps];
-    __shared__ int start_b, is_last;
-    __shared__ long long start_off;
+    __shared__ long long sums[kWarps], start_off[kWarps];
+    __shared__ int start_b[kWarps];
     const ar_kv4_attend_args &a = c.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     int *status = static_cast<int *>(a.workspace);
 
-    // Running sum over the requests' chunks: every block finds its share by itself.
-    long long u0, u1;
-    long long per;
+    // Running sum over the requests' chunks: every warp finds its share by itself.
+    long long u0, u1, per;
     {
-        const int each = (a.requests + kThreads4 - 1) / kThreads4;
+        const int each = (a.requests + kWarps * 32 - 1) / (kWarps * 32);
         const int b0 = min((int)threadIdx.x * each, a.requests), b1 = min(b0 + each, a.requests);
         long long own = 0;
         for (int b = b0; b < b1; ++b) {
@@ -223,120 +286,152 @@ __global__ void __launch_bounds__(kThreads4) attend_kernel(const __grid_constant
             if (w < warp) run += sums[w];
             total += sums[w];
         }
-        per = max((total + gridDim.x - 1) / gridDim.x, (long long)c.min_chunks);
-        u0 = min(per * blockIdx.x, total);
-        u1 = min(u0 + per, total);
-        if (u0 >= u1) return;
-        long long at = run - own;
-        if (at <= u0 && u0 < run) {
-            for (int b = b0; b < b1; ++b) {
-                const Request r = request_of<C>(c, b);
-                const long long units = (long long)r.blocks * r.chunks * a.kv_heads;
-                if (u0 < at + units) {
-                    start_b = b;
-                    start_off = u0 - at;
-                    break;
+        const long long warps = (long long)gridDim.x * kWarps;
+        per = max((total + warps - 1) / warps, (long long)c.min_chunks);
+        // (the block's first share tells whether there is any)
+        const long long first = per * kWarps * blockIdx.x;
+        if (first < total) {
+            long long at = run - own;
+            if (at < first + per * kWarps && run > first) {
+                for (int b = b0; b < b1; ++b) {
+                    const Request r = request_of<C>(c, b);
+                    const long long units = (long long)r.blocks * r.chunks * a.kv_heads;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) {
+                        const long long u = first + per * w;
+                        if (at <= u && u < at + units) {
+                            start_b[w] = b;
+                            start_off[w] = u - at;
+                        }
+                    }
+                    at += units;
                 }
-                at += units;
             }
         }
+        u0 = min(first + per * warp, total);
+        u1 = min(u0 + per, total);
         __syncthreads();
     }
-    int b = start_b;
-    long long off = start_off;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int self = blockIdx.x * kWarps + warp;
+    Record *record = reinterpret_cast<Record *>(static_cast<uint8_t *>(a.workspace) + kRecordAt) + self;
+    if (lane == 0) record->parts = 0;
+    if (u0 >= u1) return;
+
+    int b = start_b[warp];
+    long long off = start_off[warp], u = u0;
     uint8_t *ring = smem + warp * S * C::Stage;
     const uint32_t ring_addr = smem_addr(ring), bar_addr = smem_addr(&bars[warp * S]);
     bool late = false;
-    uint32_t filled = 0, used = 0;   // stages filled and used by this warp, over all its segments
+    uint32_t filled = 0, used = 0;   // stages filled and used, over all segments
+    Request r = request_of<C>(c, b);
 
-    for (long long u = u0; u < u1;) {
-        const Request r = request_of<C>(c, b);
-        const long long units = (long long)r.blocks * r.chunks * a.kv_heads;
-        if (off >= units) {
-            if (++b >= a.requests) break;   // only if the lengths changed meanwhile
+    auto next_segment = [&](Segment &s) -> bool {
+        if (u >= u1) return false;
+        while (off >= (long long)r.blocks * r.chunks * a.kv_heads) {
+            if (++b >= a.requests) return false;   // only if the lengths changed meanwhile
             off = 0;
-            continue;
+            r = request_of<C>(c, b);
         }
-        // The segment: one kv head and row block, chunks c0 .. c0 + take of it.
-        const int seg = (int)(off / r.chunks), c0 = (int)(off % r.chunks);
-        const int take = (int)min((long long)(r.chunks - c0), u1 - u);
-        const int kv = seg / r.blocks, row0 = seg % r.blocks * Rows;
-        const int rows = min(Rows, r.count * c.group - row0);
-        const int pos0 = r.len - r.count;                                // position of the first new token
-        const int pos_lo = pos0 + row0 / c.group, pos_hi = pos0 + (row0 + rows - 1) / c.group;
-        const int low = a.window ? max(pos_lo - a.window + 1, 0) : 0;   // first token in a window
-        const int low_chunk = low / C::Tokens;
-        const int sink_chunks = a.window ? (int)min((long long)low_chunk, ((long long)a.sinks + C::Tokens - 1) / C::Tokens) : 0;
-        const int chunks = pos_hi < 0 ? 0 : sink_chunks + pos_hi / C::Tokens - low_chunk + 1;
-        const int cb = min(c0 + take, chunks);
-        const int mine = cb - c0 > warp ? (cb - c0 - warp + kWarps - 1) / kWarps : 0;   // chunks c0 + warp + 4 k of it
-
-        // -- the producer's side: page ids of 32 / CT chunks at a time, a batch ahead
-        const int last_tile = pos_hi < 0 ? -1 : pos_hi / kTileTokens;
-        const int32_t *table = a.table + (long long)b * a.table_stride;
-        constexpr int kBatch = 32 / CT;
-        auto chunk_id = [&](int k) {
-            const int i = c0 + warp + kWarps * k;
-            return i < sink_chunks ? i : low_chunk + i - sink_chunks;
-        };
-        auto page_ids = [&](int k) -> int {
-            k += lane / CT;
-            if (k >= mine) return 0;
-            const int tile = chunk_id(k) * CT + lane % CT;
-            return tile <= last_tile ? table[tile * kTileTokens / a.page] : 0;
-        };
-        int ids = page_ids(0), ids_next = page_ids(kBatch);
-        int sent = 0;
-        auto send = [&]() {
-            if (sent >= mine) return;
-            if (sent && sent % kBatch == 0) {
-                ids = ids_next;
-                ids_next = page_ids(sent + kBatch);
+        const int index = off >> 32 ? (int)(off / r.chunks) : (int)((unsigned)off / (unsigned)r.chunks), from = (int)(off - (long long)index * r.chunks);
+        const int take = (int)min((long long)(r.chunks - from), u1 - u);
+        s.kv = index / r.blocks;
+        s.row0 = (index - s.kv * r.blocks) * C::Rows;
+        s.rows = min(C::Rows, r.count * c.group - s.row0);
+        s.first = r.first;
+        s.request = b;
+        s.pos0 = r.len - r.count;
+        s.pos_lo = s.pos0 + s.row0 / c.group;
+        s.pos_hi = s.pos0 + (s.row0 + s.rows - 1) / c.group;
+        s.low_chunk = a.window ? max(s.pos_lo - a.window + 1, 0) / C::Tokens : 0;
+        s.sink_chunks = a.window ? (int)min((long long)s.low_chunk, ((long long)a.sinks + C::Tokens - 1) / C::Tokens) : 0;
+        const int seen = s.pos_hi < 0 ? 0 : s.sink_chunks + s.pos_hi / C::Tokens - s.low_chunk + 1;
+        s.c0 = from;
+        s.chunks = max(min(from + take, seen) - from, 0);
+        s.whole = take == r.chunks;
+        s.begins = from == 0;
+        if (lane == 0 && u + take >= u1) {
+            // the last segment: whether it goes on in other warps
+            const long long last = u - from + r.chunks - 1;
+            const int parts = s.begins && !s.whole ? (int)((last >> 32 ? last / per : (unsigned)last / (unsigned)per) - self) + 1 : 0;
+            if (parts) {
+                record->rows = s.rows; record->kv = s.kv; record->row0 = s.row0; record->first = s.first;
             }
-            const int stage = filled % S;
-            const int tile = chunk_id(sent) * CT + lane;
-            int id = __shfl_sync(~0u, ids, sent % kBatch * CT + lane % CT);
-            const bool get = lane < CT && tile <= last_tile;
-            const unsigned n = __popc(__ballot_sync(~0u, get));
-            if (lane == 0)
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar_addr + 8 * stage),
-                             "r"(n * (unsigned)tile_bytes(D)) : "memory");
-            __syncwarp();
-            if (get) {
-                if (id < 0 || id >= a.pages) {
-                    atomicCAS(status, 0, AR_EINVAL);
-                    id = 0;
-                }
-                const uint8_t *src = static_cast<const uint8_t *>(a.pool) +
-                                     (((long long)id * a.kv_heads + kv) * (a.page / kTileTokens) + tile % (a.page / kTileTokens)) *
-                                         tile_bytes(D);
-                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                                 ring_addr + stage * C::Stage + lane * tile_bytes(D)),
-                             "l"(src), "r"((unsigned)tile_bytes(D)), "r"(bar_addr + 8 * stage)
-                             : "memory");
-            }
-            ++sent;
-            ++filled;
-        };
-        for (int i = 0; i < S; ++i) send();
+            record->parts = parts;
+        }
+        u += take;
+        off += take;
+        return true;
+    };
 
+    // The copies: lane l has the address of tile l % CT of the segment's chunk l / CT of a batch, and reads the page
+    // ids of the batch after.
+    constexpr int kBatch = 32 / CT;
+    const int tiles_page = a.page / kTileTokens;
+    int batch_tile = 0, batch_id = 0, last_tile = -1, sent = 0;
+    const uint8_t *src = nullptr;
+    unsigned have = 0;     // lanes whose tile exists
+    auto read_ids = [&](const Segment &s, int k) {
+        k += lane / CT;
+        batch_tile = k < s.chunks ? chunk_at(s, s.c0 + k) * CT + lane % CT : last_tile + 1;
+        batch_id = batch_tile <= last_tile ? a.table[(long long)s.request * a.table_stride + batch_tile / tiles_page] : 0;
+    };
+    auto next_batch = [&](const Segment &s, int k) {
+        const bool get = batch_tile <= last_tile;
+        have = __ballot_sync(~0u, get);
+        int id = batch_id;
+        if (get && (id < 0 || id >= a.pages)) {
+            atomicCAS(status, 0, AR_EINVAL);
+            id = 0;
+        }
+        src = static_cast<const uint8_t *>(a.pool) +
+              (((long long)id * a.kv_heads + s.kv) * tiles_page + batch_tile % tiles_page) * tile_bytes(D);
+        read_ids(s, k + kBatch);
+    };
+    auto send = [&](const Segment &s) {
+        if (sent >= s.chunks) return;
+        const int in = sent % kBatch * CT;    // first lane of the chunk
+        if (in == 0) next_batch(s, sent);
+        const uint32_t stage = filled % S, bar = bar_addr + 8 * stage, n = __popc((have >> in) & ((1u << CT) - 1));
+        if (lane == in)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n * tile_bytes(D)) : "memory");
+        __syncwarp();
+        if ((unsigned)(lane - in) < n)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             ring_addr + stage * C::Stage + (lane - in) * tile_bytes(D)),
+                         "l"(src), "r"((unsigned)tile_bytes(D)), "r"(bar)
+                         : "memory");
+        ++sent;
+        ++filled;
+    };
+    // The first stage at once; the others once q is on its way, so that every warp's first data come early.
+    auto begin = [&](const Segment &s) {
+        last_tile = s.pos_hi < 0 ? -1 : s.pos_hi / kTileTokens;
+        sent = 0;
+        read_ids(s, 0);
+        send(s);
+    };
+
+    Segment seg;
+    bool more = next_segment(seg);
+    if (more) begin(seg);
+    while (more) {
         // -- q: column g of tile n is row row0 + 8 n + g; fp16 of q / 2^e, e the row's own for bfloat16
-        uint32_t qf[C::QShared ? 1 : NT][D / 16][2];
-        uint2 *q_shared = reinterpret_cast<uint2 *>(smem + C::Data);
-        float mult[NT][2];            // what a sum of products is worth, in base 2: columns 2 t and 2 t + 1
-        int pos[NT][2];               // their positions
+        uint2 qf[NT][D / 16];
+        float less[C::Over ? NT : 1][G][2];   // minus what nibbles_over puts on top of a group's products
+        float mult[NT][2];                    // what a sum of products is worth, in base 2: columns 2 t and 2 t + 1
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int row = row0 + 8 * n + g;
-            const bool in = row < row0 + rows;
+            const int row = seg.row0 + 8 * n + g;
+            const bool in = 8 * n + g < seg.rows;
             float x[G][8];
             uint32_t top = 0;
-            const T *src = static_cast<const T *>(a.q) + (long long)(r.first + (in ? row / c.group : 0)) * a.q_token_stride +
-                           (long long)(kv * c.group + (in ? row % c.group : 0)) * a.q_head_stride + 8 * t;
+            const T *qs = static_cast<const T *>(a.q) + (long long)(seg.first + (in ? row / c.group : 0)) * a.q_token_stride +
+                          (long long)(seg.kv * c.group + (in ? row % c.group : 0)) * a.q_head_stride + 8 * t;
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 if (in) {
-                    load8(src + 32 * j, c.vec_q != 0, x[j]);
+                    load8(qs + 32 * j, c.vec_q != 0, x[j]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[j][i] = 0;
@@ -345,7 +440,7 @@ __global__ void __launch_bounds__(kThreads4) attend_kernel(const __grid_constant
                 for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[j][i]) & 0x7fffffffu);
             }
             float unit = 1, worth = a.scale * 1.4426950408889634f;
-            if constexpr (sizeof(T) == 2 && !std::is_same<T, __half>::value) {
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
                 top = max(top, __shfl_xor_sync(~0u, top, 1));
                 top = max(top, __shfl_xor_sync(~0u, top, 2));
                 // 2^e <= top, and 2^-e a normal number; zeros, infinities and NaN stay as they are
@@ -358,29 +453,36 @@ __global__ void __launch_bounds__(kThreads4) attend_kernel(const __grid_constant
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 uint32_t h[4];
+                float over = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = pack_half(x[j][i] * unit, x[j][i + 4] * unit);
-                if constexpr (C::QShared) {
-                    if (warp == n % kWarps) {
-                        q_shared[((2 * j) * NT + n) * 32 + lane] = make_uint2(h[0], h[1]);
-                        q_shared[((2 * j + 1) * NT + n) * 32 + lane] = make_uint2(h[2], h[3]);
+                for (int i = 0; i < 4; ++i) {
+                    h[i] = pack_half(x[j][i] * unit, x[j][i + 4] * unit);
+                    if constexpr (C::Over) {
+                        // of the operands as they are, rounded
+                        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+                        over = fmaf(i & 1 ? kOver1 : kOver0, v.x + v.y, over);
                     }
-                } else {
-                    qf[n][2 * j][0] = h[0]; qf[n][2 * j][1] = h[1];
-                    qf[n][2 * j + 1][0] = h[2]; qf[n][2 * j + 1][1] = h[3];
+                }
+                qf[n][2 * j] = make_uint2(h[0], h[1]);
+                qf[n][2 * j + 1] = make_uint2(h[2], h[3]);
+                if constexpr (C::Over) {
+                    over += __shfl_xor_sync(~0u, over, 1);
+                    over += __shfl_xor_sync(~0u, over, 2);
+                    less[n][j][0] = -__shfl_sync(~0u, over, 8 * t);
+                    less[n][j][1] = -__shfl_sync(~0u, over, 8 * t + 4);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                mult[n][i] = __shfl_sync(~0u, worth, (2 * t + i) * 4);
-                pos[n][i] = min(pos0 + (row0 + 8 * n + 2 * t + i) / c.group, pos_hi);
-            }
+            for (int i = 0; i < 2; ++i) mult[n][i] = __shfl_sync(~0u, worth, (2 * t + i) * 4);
         }
-        if constexpr (C::QShared) __syncthreads();
+
+#pragma unroll 1
+        for (int i = 1; i < S; ++i) send(seg);
 
         float o[D / 16][NT][4];
         float ref[NT][2], l[NT][2];
         int vexp = -80;                      // exponent of the largest V scale so far, at least -80
+        float most = kHead + kLead + 80, vnext = __uint_as_float((uint32_t)(128 - 80) << 23);   // what moves the reference: a score, a scale
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -391,16 +493,9 @@ __global__ void __launch_bounds__(kThreads4) attend_kernel(const __grid_constant
             l[n][0] = l[n][1] = 0;
         }
 
-        for (int k = 0; k < mine; ++k) {
-            const int stage = used % S;
-            wait_stage(bar_addr + 8 * stage, (used / S) & 1, late, status);
-            const uint8_t *data = ring + stage * C::Stage;
-            const int tok0 = chunk_id(k) * C::Tokens;
-            // Whether every row sees every token of the chunk.
-            const bool full = tok0 + C::Tokens - 1 <= pos_lo &&
-                              (!a.window || tok0 > pos_hi - a.window || tok0 <= a.sinks - C::Tokens);
-
-            // scores
+        // One chunk.  Full: every row sees every token of it.
+        auto chunk = [&](auto is_full, const uint8_t *data, int tok0) {
+            constexpr bool Full = decltype(is_full)::value;
             float x[CT][NT][4];
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
@@ -413,22 +508,25 @@ __global__ void __launch_bounds__(kThreads4) attend_kernel(const __grid_constant
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
                     uint32_t h0[4], h1[4];
-                    nibbles_to_half(w0[j], h0);
-                    nibbles_to_half(w1[j], h1);
+                    if constexpr (C::Over) {
+                        nibbles_over(w0[j], h0);
+                        nibbles_over(w1[j], h1);
+                    } else {
+                        nibbles_to_half(w0[j], h0);
+                        nibbles_to_half(w1[j], h1);
+                    }
                     const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
                     const float s0 = __uint_as_float(j & 1 ? sc0[j / 2] & 0xffff0000u : sc0[j / 2] << 16);
                     const float s1 = __uint_as_float(j & 1 ? sc1[j / 2] & 0xffff0000u : sc1[j / 2] << 16);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        float acc[4] = {0, 0, 0, 0};
-                        if constexpr (C::QShared) {
-                            const uint2 q0 = q_shared[((2 * j) * NT + n) * 32 + lane], q1 = q_shared[((2 * j + 1) * NT + n) * 32 + lane];
-                            mma16816(acc, a0, q0.x, q0.y);
-                            mma16816(acc, a1, q1.x, q1.y);
-                        } else {
-                            mma16816(acc, a0, qf[n][2 * j][0], qf[n][2 * j][1]);
-                            mma16816(acc, a1, qf[n][2 * j + 1][0], qf[n][2 * j + 1][1]);
-                        }
+                        float acc[4];
+                        const uint2 q0 = qf[n][2 * j], q1 = qf[n][2 * j + 1];
+                        if constexpr (C::Over)
+                            mma16816(acc, a0, q0.x, q0.y, less[n][j][0], less[n][j][1], less[n][j][0], less[n][j][1]);
+                        else
+                            mma16816(acc, a0, q0.x, q0.y, 0.0f, 0.0f, 0.0f, 0.0f);
+                        mma16816(acc, a1, q1.x, q1.y);
                         if (j == 0) {
                             x[ct][n][0] = acc[0] * s0; x[ct][n][1] = acc[1] * s0;
                             x[ct][n][2] = acc[2] * s1; x[ct][n][3] = acc[3] * s1;
@@ -439,39 +537,57 @@ __global__ void __launch_bounds__(kThreads4) attend_kernel(const __grid_constant
                     }
                 }
             }
-            // V scales: the largest exponent among tokens that some row sees
-            int vmax = 0;
+            // V scales: the largest among tokens that some row sees, infinities and NaN left out
+            float vtop = 0;
 #pragma unroll
             for (int i = 0; i < CT * D / 128; ++i) {
                 const int wd = i * 32 + lane, ct = wd / (D / 4), in = wd % (D / 4);
                 uint32_t w = *reinterpret_cast<const uint32_t *>(data + ct * tile_bytes(D) + tile_vs(D) + in * 4);
-                if (!full) {
+                if constexpr (!Full) {
                     const int tok = tok0 + ct * kTileTokens + in / (G / 2);
-                    if (tok > pos_hi || (a.window && tok <= pos_lo - a.window && tok >= a.sinks)) w = 0;
+                    if (tok > seg.pos_hi || (a.window && tok <= seg.pos_lo - a.window && tok >= a.sinks)) w = 0;
                 }
-                const int e0 = (w >> 7) & 255, e1 = (w >> 23) & 255;
-                vmax = max(vmax, max(e0 == 255 ? 0 : e0, e1 == 255 ? 0 : e1));
+                vtop = fmaxf(vtop, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w))));
             }
-            bool move = vmax - 127 > vexp;
-            // relative to the reference; what a row does not see is -infinity
-            const float most = (float)(kHead + kLead - vexp);
+            // scores under the reference; what a row does not see is -infinity
+            if constexpr (!Full) {
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = seg.row0 + 8 * n + 2 * t + (i & 1), p = min(seg.pos0 + row / c.group, seg.pos_hi);
+                            const int tok = tok0 + ct * kTileTokens + g + (i & 2) * 4;
+                            const bool see = tok <= p && (!a.window || tok > p - a.window || tok < a.sinks);
+                            x[ct][n][i] = see ? x[ct][n][i] * mult[n][i & 1] : -INFINITY;
+                        }
+            }
+            float y[CT][NT][4];
+            float above = kNoScore;
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        x[ct][n][i] *= mult[n][i & 1];
-                        if (!full) {
-                            const int tok = tok0 + ct * kTileTokens + g + (i & 2) * 4, p = pos[n][i & 1];
-                            const bool see = tok <= p && (!a.window || tok > p - a.window || tok < a.sinks);
-                            x[ct][n][i] = see ? x[ct][n][i] : -INFINITY;
-                        }
-                        move |= x[ct][n][i] - ref[n][i & 1] > most;
+                        y[ct][n][i] = Full ? fmaf(x[ct][n][i], mult[n][i & 1], -ref[n][i & 1]) : x[ct][n][i] - ref[n][i & 1];
+                        above = fmaxf(above, y[ct][n][i]);
                     }
-            if (__any_sync(~0u, move)) {
-                vmax = __reduce_max_sync(~0u, vmax);
-                vexp = max(vexp, vmax - 127);
+            if (__any_sync(~0u, vtop >= vnext || above > most)) {
+                if (!(vtop < INFINITY)) {
+                    // an infinite scale spoils its own group; the others keep theirs
+                    vtop = 0;
+#pragma unroll 1
+                    for (int i = 0; i < CT * D / 64; ++i) {
+                        const int half = (i / 2 * 32 + lane) * 2 + i % 2, ct = half / (D / 2), in = half % (D / 2), tok = tok0 + ct * kTileTokens + in / G;
+                        const float v = fabsf(bf16_bits(*reinterpret_cast<const uint16_t *>(data + ct * tile_bytes(D) + tile_vs(D) + in * 2)));
+                        if (v < INFINITY && tok <= seg.pos_hi && (!a.window || tok > seg.pos_lo - a.window || tok < a.sinks)) vtop = fmaxf(vtop, v);
+                    }
+                }
+                vexp = max(vexp, (int)(__reduce_max_sync(~0u, __float_as_uint(vtop)) >> 23) - 127);
+                most = (float)(kHead + kLead - vexp);
+                vnext = __uint_as_float((uint32_t)(vexp + 128) << 23);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -479,6 +595,13 @@ __global__ void __launch_bounds__(kThreads4) attend_kernel(const __grid_constant
                         float top = kNoScore;
 #pragma unroll
                         for (int ct = 0; ct < CT; ++ct) top = fmaxf(top, fmaxf(x[ct][n][i], x[ct][n][i + 2]));
+                        if constexpr (Full) {
+                            // (a product with a negative scale turns the order around)
+                            float low = -kNoScore;
+#pragma unroll
+                            for (int ct = 0; ct < CT; ++ct) low = fminf(low, fminf(x[ct][n][i], x[ct][n][i + 2]));
+                            top = fmaxf(top * mult[n][i], low * mult[n][i]);
+                        }
 #pragma unroll
                         for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
                         // the reference never falls: a lower one would let earlier weights overflow
@@ -491,6 +614,11 @@ __global__ void __launch_bounds__(kThreads4) attend_kernel(const __grid_constant
                             o[m][n][i] *= keep;
                             o[m][n][i + 2] *= keep;
                         }
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                            for (int h = i; h < 4; h += 2)
+                                y[ct][n][h] = Full ? fmaf(x[ct][n][h], mult[n][i], -now) : x[ct][n][h] - now;
                     }
             }
             // weights, and the sum over V
@@ -505,9 +633,9 @@ __global__ void __launch_bounds__(kThreads4) attend_kernel(const __grid_constant
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[ct][n][i] = exp2_approx(x[ct][n][i] - ref[n][i & 1]);
-                    l[n][0] += x[ct][n][0] + x[ct][n][2];
-                    l[n][1] += x[ct][n][1] + x[ct][n][3];
+                    for (int i = 0; i < 4; ++i) y[ct][n][i] = exp2_approx(y[ct][n][i]);
+                    l[n][0] += y[ct][n][0] + y[ct][n][2];
+                    l[n][1] += y[ct][n][1] + y[ct][n][3];
                 }
 #pragma unroll
                 for (int j = 0; j < G; ++j) {
@@ -519,11 +647,11 @@ __global__ void __launch_bounds__(kThreads4) attend_kernel(const __grid_constant
                     const float s1 = __uint_as_float(j & 1 ? sc1[j / 2] & 0xffff0000u : sc1[j / 2] << 16);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        float p[4] = {x[ct][n][0] * s0, x[ct][n][1] * s0, x[ct][n][2] * s1, x[ct][n][3] * s1};
-                        if (!full) {
-                            // a scale that no row of ours may see can be anything
+                        float p[4] = {y[ct][n][0] * s0, y[ct][n][1] * s0, y[ct][n][2] * s1, y[ct][n][3] * s1};
+                        if constexpr (!Full) {
+                            // a scale that a row does not see can be anything
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) p[i] = x[ct][n][i] == 0 ? 0 : p[i];
+                            for (int i = 0; i < 4; ++i) p[i] = y[ct][n][i] == 0 ? 0 : p[i];
                         }
                         const uint32_t b0 = transpose8x8(pack_half(p[0], p[1])), b1 = transpose8x8(pack_half(p[2], p[3]));
                         mma16816(o[2 * j][n], a0, b0, b1);
@@ -531,118 +659,113 @@ __global__ void __launch_bounds__(kThreads4) attend_kernel(const __grid_constant
                     }
                 }
             }
+        };
+
+        for (int k = 0; k < seg.chunks; ++k) {
+            const uint32_t stage = used % S;
+            if (!late) late = !bar_wait(bar_addr + 8 * stage, (used / S) & 1, status);
+            const uint8_t *data = ring + stage * C::Stage;
+            const int tok0 = chunk_at(seg, seg.c0 + k) * C::Tokens;
+            if (tok0 + C::Tokens - 1 <= seg.pos_lo && (!a.window || tok0 > seg.pos_hi - a.window || tok0 <= a.sinks - C::Tokens))
+                chunk(std::true_type(), data, tok0);
+            else
+                chunk(std::false_type(), data, tok0);
             ++used;
             __syncwarp();      // every lane has read the stage
-            send();
+            send(seg);
         }
 
-        // -- join the warps: each one's reference, sum and rows through shared memory
-        __syncthreads();
-        float *xo = reinterpret_cast<float *>(smem), *xm = xo + kWarps * Rows * C::OStride;
+        const Segment now = seg;
+        more = next_segment(seg);
+        if (more) begin(seg);
+
+        // -- results: to their rows, or one part of them to the workspace
+        float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kPartAt) +
+                      (2 * (size_t)self + (now.begins ? 1 : 0)) * C::PartFloats;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
 #pragma unroll
                 for (int d = 4; d < 32; d *= 2) l[n][i] += __shfl_xor_sync(~0u, l[n][i], d);
-                const int col = 8 * n + 2 * t + i;
-                if (g == 0) {
-                    xm[(warp * Rows + col) * 2] = ref[n][i];
-                    xm[(warp * Rows + col) * 2 + 1] = l[n][i];
-                }
+                const int col = 8 * n + 2 * t + i, row = now.row0 + col;
+                if (col < now.rows) {
+                    const long long token = now.first + row / c.group;
+                    const int head = now.kv * c.group + row % c.group;
 #pragma unroll
-                for (int j = 0; j < G; ++j)
-                    *reinterpret_cast<float4 *>(&xo[(warp * Rows + col) * C::OStride + 32 * j + 4 * g]) =
-                        make_float4(o[2 * j][n][i], o[2 * j][n][i + 2], o[2 * j + 1][n][i], o[2 * j + 1][n][i + 2]);
-            }
-        }
-        __syncthreads();
-        // The segment's other blocks, if any.
-        const long long s0 = u - c0;
-        const int first = (int)(s0 / per), parts = (int)((s0 + r.chunks - 1) / per) - first + 1;
-        float *part_base = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kPartAt);
-        float *part = part_base + (2 * (size_t)blockIdx.x + (first == (int)blockIdx.x ? 1 : 0)) * C::PartFloats;
-        auto finish = [&](int col, int quad, float4 v, float m, float sum) {
-            const int row = row0 + col;
-            const float inv = sum > 0 ? __fdiv_rn(1.0f, sum) : sum == sum ? 0.0f : sum;
-            const long long token = r.first + row / c.group;
-            const int head = kv * c.group + row % c.group;
-            T *dst = static_cast<T *>(a.out) + token * a.out_token_stride + (long long)head * a.out_head_stride + 4 * quad;
-            union { uint2 u; T e[4]; } w;
-            w.e[0] = Elem<T>::from_float(v.x * inv); w.e[1] = Elem<T>::from_float(v.y * inv);
-            w.e[2] = Elem<T>::from_float(v.z * inv); w.e[3] = Elem<T>::from_float(v.w * inv);
-            if (c.vec_o) {
-                *reinterpret_cast<uint2 *>(dst) = w.u;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dst[i] = w.e[i];
-            }
-            if (quad == 0 && a.lse)
-                a.lse[token * a.q_heads + head] =
-                    sum > 0 ? (m + log2f(sum)) * 0.6931471805599453f : sum == sum ? -INFINITY : sum;
-        };
-        for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads4) {
-            const int col = i / (D / 4), quad = i % (D / 4);
-            float m = kNoScore;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, xm[(w * Rows + col) * 2]);
-            float4 v = make_float4(0, 0, 0, 0);
-            float sum = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = exp2_approx(xm[(w * Rows + col) * 2] - m);
-                const float4 y = *reinterpret_cast<const float4 *>(&xo[(w * Rows + col) * C::OStride + 4 * quad]);
-                sum = fmaf(xm[(w * Rows + col) * 2 + 1], f, sum);
-                v.x = fmaf(y.x, f, v.x); v.y = fmaf(y.y, f, v.y); v.z = fmaf(y.z, f, v.z); v.w = fmaf(y.w, f, v.w);
-            }
-            if (parts == 1) {
-                finish(col, quad, v, m, sum);
-            } else {
-                *reinterpret_cast<float4 *>(part + col * D + 4 * quad) = v;
-                if (quad == 0) {
-                    part[Rows * D + 2 * col] = m;
-                    part[Rows * D + 2 * col + 1] = sum;
-                }
-            }
-        }
-        if (parts > 1) {
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                unsigned *counter = reinterpret_cast<unsigned *>(static_cast<uint8_t *>(a.workspace) + kCounterAt) + first;
-                is_last = atomicAdd(counter, 1) == (unsigned)parts - 1;
-                if (is_last) *counter = 0;   // for the next call
-                __threadfence();
-            }
-            __syncthreads();
-            if (is_last) {
-                // in the order of the parts, whoever came last
-                auto at = [&](int i) { return part_base + (i == 0 ? 2 * (size_t)first + 1 : 2 * (size_t)(first + i)) * C::PartFloats; };
-                for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads4) {
-                    const int col = i / (D / 4), quad = i % (D / 4);
-                    float m = kNoScore, sum = 0;
-                    float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-                    for (int k = 0; k < parts; ++k) {
-                        const float *p = at(k);
-                        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(p + Rows * D + 2 * col));
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p + col * D + 4 * quad));
-                        const float m2 = fmaxf(m, ml.x), f0 = exp2_approx(m - m2), f1 = exp2_approx(ml.x - m2);
-                        m = m2;
-                        sum = fmaf(sum, f0, ml.y * f1);
-                        v.x = fmaf(v.x, f0, y.x * f1); v.y = fmaf(v.y, f0, y.y * f1);
-                        v.z = fmaf(v.z, f0, y.z * f1); v.w = fmaf(v.w, f0, y.w * f1);
+                    for (int j = 0; j < G; ++j) {
+                        const float4 v = make_float4(o[2 * j][n][i], o[2 * j][n][i + 2], o[2 * j + 1][n][i], o[2 * j + 1][n][i + 2]);
+                        const int channel = 32 * j + 4 * g;
+                        if (now.whole) store_row<T>(c, token, head, channel, v, ref[n][i], l[n][i]);
+                        else *reinterpret_cast<float4 *>(part + col * D + channel) = v;
                     }
-                    finish(col, quad, v, m, sum);
+                    if (!now.whole && g == 0) *reinterpret_cast<float2 *>(part + C::Rows * D + 2 * col) = make_float2(ref[n][i], l[n][i]);
                 }
             }
         }
-        __syncthreads();   // the ring is free for the next segment's copies
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        u += take;
-        off += take;
     }
 }
+
+// Joins the parts of the segment that begins in a warp, in their order.  A
+// block to a warp's record and, by Spread, to one of its rows: then groups of D / 4
+// threads share out the parts, for where a few rows have many.
+constexpr int kJoinThreads = 256;
+
+template <typename T, class C, bool Spread>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Attend c) {
+    constexpr int D = C::D, Quads = D / 4, Groups = Spread ? kJoinThreads / Quads : 1;
+    __shared__ float4 rows[Groups][Quads];
+    __shared__ float2 facts[Groups];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint8_t *ws = static_cast<const uint8_t *>(c.a.workspace);
+    const Record r = reinterpret_cast<const Record *>(ws + kRecordAt)[blockIdx.x];
+    if (r.parts == 0 || (Spread && (int)blockIdx.y >= r.rows)) return;
+    // part 0 lies in its warp's second place, the others in their warps' first
+    const float *base = reinterpret_cast<const float *>(ws + kPartAt) + (2 * (size_t)blockIdx.x + 1) * C::PartFloats;
+    const int group = Spread ? threadIdx.x / Quads : 0;
+    for (int i = Spread ? blockIdx.y * Quads + threadIdx.x % Quads : threadIdx.x; i < r.rows * Quads; i += kJoinThreads) {
+        const int col = i / Quads, quad = i % Quads;
+        float m = kNoScore, sum = 0;
+        float4 v = make_float4(0, 0, 0, 0);
+        auto add = [&](float2 ml, float4 y) {
+            const float m2 = fmaxf(m, ml.x), f0 = exp2_approx(m - m2), f1 = exp2_approx(ml.x - m2);
+            m = m2;
+            sum = fmaf(sum, f0, ml.y * f1);
+            v.x = fmaf(v.x, f0, y.x * f1); v.y = fmaf(v.y, f0, y.y * f1);
+            v.z = fmaf(v.z, f0, y.z * f1); v.w = fmaf(v.w, f0, y.w * f1);
+        };
+        constexpr int kAtOnce = 8;
+        for (int k = group; k < r.parts; k += kAtOnce * Groups) {
+            float2 ml[kAtOnce];
+            float4 y[kAtOnce];
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e) {
+                const int part = k + e * Groups;
+                const float *p = part ? base + (2 * (size_t)part - 1) * C::PartFloats : base;
+                if (part < r.parts) {
+                    ml[e] = __ldcg(reinterpret_cast<const float2 *>(p + C::Rows * D + 2 * col));
+                    y[e] = __ldcg(reinterpret_cast<const float4 *>(p + col * D + 4 * quad));
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e)
+                if (k + e * Groups < r.parts) add(ml[e], y[e]);
+        }
+        if constexpr (Spread) {
+            rows[group][quad] = v;
+            if (quad == 0) facts[group] = make_float2(m, sum);
+            __syncthreads();
+            if (group > 0) return;
+#pragma unroll
+            for (int k = 1; k < Groups; ++k) add(facts[k], rows[k][quad]);
+        }
+        const int row = r.row0 + col;
+        store_row<T>(c, (long long)r.first + row / c.group, r.kv * c.group + row % c.group, 4 * quad, v, m, sum);
+        if constexpr (Spread) return;
+    }
+}
+
+constexpr int kSpreadSegments = 64;
 
 template <typename T, class C>
 int start(const Attend &c, cudaStream_t s) {
@@ -655,35 +778,45 @@ int start(const Attend &c, cudaStream_t s) {
     if (grid == 0) {
         int per_sm = 0, sms = 0;
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads4, C::Smem) != cudaSuccess || per_sm < 1 ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kWarps * 32, C::Smem) != cudaSuccess || per_sm < 1 ||
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return launch_status(cudaErrorUnknown);
-        grid = min(per_sm * sms, C::MaxGrid);
+        const int fit = (int)((kWorkspaceBytes - kPartAt) / (2 * kWarps * C::PartFloats * 4));
+        grid = min(per_sm * sms, min(fit, kMaxWarps / kWarps));
         *(volatile int *)&resident[dev] = grid;
     }
     // No more blocks than the longest contexts the table can hold would fill.
-    const long long chunks = ((long long)c.a.table_width * c.a.page + C::Tokens - 1) / C::Tokens;
+    const long long chunks = max(((long long)c.a.table_width * c.a.page + C::Tokens - 1) / C::Tokens, 1ll);
     const long long blocks = ((long long)c.a.tokens * c.group + C::Rows - 1) / C::Rows + c.a.requests;
-    const long long most = (blocks * max(chunks, 1ll) * c.a.kv_heads + c.min_chunks - 1) / c.min_chunks;
+    const long long share = (long long)c.min_chunks * kWarps, most = (blocks * chunks * c.a.kv_heads + share - 1) / share;
+    grid = (int)min((long long)grid, most);
     void *args[] = {const_cast<Attend *>(&c)};
-    return launch_status(cudaLaunchKernel(kernel, dim3((unsigned)min((long long)grid, most)), dim3(kThreads4), args, C::Smem, s));
+    cudaError_t e = cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3(kWarps * 32), args, C::Smem, s);
+    // The joining kernel comes to the GPU beside the end of the first, and waits for it.
+    if (e == cudaSuccess && chunks > c.min_chunks) {
+        const bool spread = (long long)c.a.requests * c.a.kv_heads <= kSpreadSegments;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(grid * kWarps), spread ? C::Rows : 1);
+        cfg.blockDim = dim3(kJoinThreads);
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = spread ? cudaLaunchKernelEx(&cfg, join_kernel<T, C, true>, c) : cudaLaunchKernelEx(&cfg, join_kernel<T, C, false>, c);
+    }
+    return launch_status(e);
 }
 
 template <typename T>
 int start(const Attend &c, cudaStream_t s) {
     const long long rows = (long long)max(c.a.max_new, 1) * c.group;
     switch (c.a.head_dim) {
-        case 64:
-            if (rows <= 8) return start<T, Shape<64, 1, 2, 4>>(c, s);
-            if (rows <= 16) return start<T, Shape<64, 2, 2, 4>>(c, s);
-            return start<T, Shape<64, 4, 2, 4>>(c, s);
-        case 128:
-            if (rows <= 8) return start<T, Shape<128, 1, 2, 3>>(c, s);
-            if (rows <= 16) return start<T, Shape<128, 2, 2, 3>>(c, s);
-            return start<T, Shape<128, 4, 1, 4>>(c, s);
-        default:
-            if (rows <= 8) return start<T, Shape<256, 1, 1, 3>>(c, s);
-            return start<T, Shape<256, 2, 1, 3>>(c, s);
+        case 64: return rows <= 8 ? start<T, Shape<64, 1, 4, 3, 3>>(c, s) : start<T, Shape<64, 2, 4, 3, 3>>(c, s);
+        case 128: return rows <= 8 ? start<T, Shape<128, 1, 4, 2, 3>>(c, s) : start<T, Shape<128, 2, 2, 4, 2>>(c, s);
+        default: return start<T, Shape<256, 1, 1, 5, 2>>(c, s);
     }
 }
 
@@ -728,10 +861,11 @@ AR_API int ar_kv4_attend(const ar_kv4_attend_args *args, ar_stream_t stream) {
     // A window or sinks that cover the table limit nothing; smaller ones and the rows stay where sums fit 32 bits.
     const long long room = (long long)a.table_width * a.page;
     if (a.window >= room || a.sinks >= room) c.a.window = 0;
-    if ((long long)a.tokens * c.group > 1 << 30 || c.a.window > 1 << 30) return AR_ETOOBIG;
+    if ((long long)a.tokens * c.group > 1 << 30 || c.a.window > 1 << 30 || (long long)a.tokens * a.q_heads > 0x7fffffff)
+        return AR_ETOOBIG;
     c.vec_q = rows_aligned(a.q, a.q_token_stride, a.q_head_stride);
     c.vec_o = rows_aligned(a.out, a.out_token_stride, a.out_head_stride);
-    c.min_chunks = kWarps;
+    c.min_chunks = 1;
     return a.dtype == AR_F16 ? start<__half>(c, stream) : start<__nv_bfloat16>(c, stream);
 }
 
