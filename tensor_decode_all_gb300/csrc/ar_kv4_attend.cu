@@ -34,6 +34,7 @@ constexpr int kMaxRequests = 8192;
 constexpr int kWarps = 4;                 // warps of a block; each works alone
 constexpr float kNoScore = -3.0e38f;      // below every score; finite, so that differences are numbers
 constexpr int kHead = 8;                  // weights stand near 2^kHead ...
+constexpr int kStart = 2;                 // chunks that beginning a segment is worth
 constexpr int kLead = 6;                  // ... and may pass it by 2^kLead before the reference moves
 
 // Workspace: status, a record for each warp, and two partial results to a warp.
@@ -159,6 +160,9 @@ struct Shape {
 struct Request {
     int len, first, count;   // tokens, first row of q, rows
     int blocks, chunks;      // row blocks; chunks of a row block (an upper bound where there are several)
+    // A row block's length in the row of shares: a segment costs as much as kStart chunks beside its own.
+    __device__ long long length() const { return chunks + kStart; }
+    __device__ long long total(int kv_heads) const { return blocks * length() * kv_heads; }
 };
 
 template <class C>
@@ -196,12 +200,12 @@ struct Segment {
     int pos0, pos_lo, pos_hi;       // position of the request's first new token, of the rows' first and last
     int c0, chunks;                 // chunks c0 .. c0 + chunks - 1 of those that its rows see
     int sink_chunks, low_chunk;     // chunk i is i below sink_chunks, i + low_chunk - sink_chunks from there on
-    int request;
-    bool whole, begins;             // all of its row block; its beginning
+    int request, end_tile;          // its tiles that hold tokens end there
+    int whole, begins;              // all of its row block; its beginning
 };
 
-__device__ __forceinline__ int chunk_at(const Segment &s, int i) {
-    return i < s.sink_chunks ? i : s.low_chunk + i - s.sink_chunks;
+__device__ __forceinline__ int chunk_at(int i, int sink_chunks, int low_chunk) {
+    return i < sink_chunks ? i : low_chunk + i - sink_chunks;
 }
 
 __device__ __forceinline__ long long now_ns() {
@@ -253,8 +257,9 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
     constexpr int D = C::D, NT = C::NT, CT = C::CT, S = C::S, G = C::G;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) unsigned long long bars[kWarps * S];
-    __shared__ long long sums[kWarps], start_off[kWarps];
+    __shared__ long long sums[kWarps], start_off[kWarps], start_u[kWarps];   // where each warp's walk stands
     __shared__ int start_b[kWarps];
+    __shared__ Segment segments[kWarps][2];
     const ar_kv4_attend_args &a = c.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     int *status = static_cast<int *>(a.workspace);
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
         long long own = 0;
         for (int b = b0; b < b1; ++b) {
             const Request r = request_of<C>(c, b);
-            own += (long long)r.blocks * r.chunks * a.kv_heads;
+            own += r.total(a.kv_heads);
         }
         long long run = own;
 #pragma unroll
@@ -295,13 +300,14 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
             if (at < first + per * kWarps && run > first) {
                 for (int b = b0; b < b1; ++b) {
                     const Request r = request_of<C>(c, b);
-                    const long long units = (long long)r.blocks * r.chunks * a.kv_heads;
+                    const long long units = r.total(a.kv_heads);
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) {
                         const long long u = first + per * w;
                         if (at <= u && u < at + units) {
                             start_b[w] = b;
                             start_off[w] = u - at;
+                            start_u[w] = u;
                         }
                     }
                     at += units;
@@ -318,80 +324,96 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
     if (lane == 0) record->parts = 0;
     if (u0 >= u1) return;
 
-    int b = start_b[warp];
-    long long off = start_off[warp], u = u0;
+    // ---- the copies' side: walks the segments, at most one ahead of the products
     uint8_t *ring = smem + warp * S * C::Stage;
     const uint32_t ring_addr = smem_addr(ring), bar_addr = smem_addr(&bars[warp * S]);
+    const int tiles_page = a.page / kTileTokens;
+    constexpr int kBatch = 32 / CT;
     bool late = false;
-    uint32_t filled = 0, used = 0;   // stages filled and used, over all segments
-    Request r = request_of<C>(c, b);
-
-    auto next_segment = [&](Segment &s) -> bool {
-        if (u >= u1) return false;
-        while (off >= (long long)r.blocks * r.chunks * a.kv_heads) {
-            if (++b >= a.requests) return false;   // only if the lengths changed meanwhile
-            off = 0;
-            r = request_of<C>(c, b);
-        }
-        const int index = off >> 32 ? (int)(off / r.chunks) : (int)((unsigned)off / (unsigned)r.chunks), from = (int)(off - (long long)index * r.chunks);
-        const int take = (int)min((long long)(r.chunks - from), u1 - u);
-        s.kv = index / r.blocks;
-        s.row0 = (index - s.kv * r.blocks) * C::Rows;
-        s.rows = min(C::Rows, r.count * c.group - s.row0);
-        s.first = r.first;
-        s.request = b;
-        s.pos0 = r.len - r.count;
-        s.pos_lo = s.pos0 + s.row0 / c.group;
-        s.pos_hi = s.pos0 + (s.row0 + s.rows - 1) / c.group;
-        s.low_chunk = a.window ? max(s.pos_lo - a.window + 1, 0) / C::Tokens : 0;
-        s.sink_chunks = a.window ? (int)min((long long)s.low_chunk, ((long long)a.sinks + C::Tokens - 1) / C::Tokens) : 0;
-        const int seen = s.pos_hi < 0 ? 0 : s.sink_chunks + s.pos_hi / C::Tokens - s.low_chunk + 1;
-        s.c0 = from;
-        s.chunks = max(min(from + take, seen) - from, 0);
-        s.whole = take == r.chunks;
-        s.begins = from == 0;
-        if (lane == 0 && u + take >= u1) {
-            // the last segment: whether it goes on in other warps
-            const long long last = u - from + r.chunks - 1;
-            const int parts = s.begins && !s.whole ? (int)((last >> 32 ? last / per : (unsigned)last / (unsigned)per) - self) + 1 : 0;
-            if (parts) {
-                record->rows = s.rows; record->kv = s.kv; record->row0 = s.row0; record->first = s.first;
+    uint32_t filled = 0, used = 0;       // stages filled and used, over all segments
+    int walked = 0;                      // segments walked to
+    // Of the segment walked to last: its chunks and how many of them are sent.  Lane l has the address of tile l % CT of
+    // its chunk l / CT of a batch, and reads the page ids of the batch after.
+    int p_chunks = 0, sent = 0, batch_tile = 0, batch_id = 0;
+    const uint8_t *src = nullptr;
+    unsigned have = 0;                   // lanes whose tile exists
+    auto read_ids = [&](int k) {
+        const Segment &s = segments[warp][(walked - 1) & 1];
+        k += lane / CT;
+        batch_tile = k < p_chunks ? chunk_at(s.c0 + k, s.sink_chunks, s.low_chunk) * CT + lane % CT : s.end_tile;
+        batch_id = batch_tile < s.end_tile ? a.table[(long long)s.request * a.table_stride + batch_tile / tiles_page] : 0;
+    };
+    auto walk = [&]() -> bool {
+        __syncwarp();                    // every lane is done with the segment whose place this takes
+        int b = start_b[warp];
+        long long off = start_off[warp], u = start_u[warp];
+        Segment s;
+        for (;;) {
+            if (u >= u1 || b >= a.requests) return false;     // (the latter only if the lengths changed meanwhile)
+            const Request r = request_of<C>(c, b);
+            if (off >= r.total(a.kv_heads)) {
+                ++b;
+                off = 0;
+                continue;
             }
-            record->parts = parts;
+            const int length = (int)r.length();
+            const int index = off >> 32 ? (int)(off / length) : (int)((unsigned)off / (unsigned)length);
+            const int from = (int)(off - (long long)index * length), take = (int)min((long long)(length - from), u1 - u);
+            const long long last = u - from + length - 1;
+            u += take;
+            off += take;
+            if (from + take <= kStart) continue;              // no chunk of it
+            s.kv = index / r.blocks;
+            s.row0 = (index - s.kv * r.blocks) * C::Rows;
+            s.rows = min(C::Rows, r.count * c.group - s.row0);
+            s.first = r.first;
+            s.request = b;
+            s.pos0 = r.len - r.count;
+            s.pos_lo = s.pos0 + s.row0 / c.group;
+            s.pos_hi = s.pos0 + (s.row0 + s.rows - 1) / c.group;
+            s.end_tile = s.pos_hi < 0 ? 0 : s.pos_hi / kTileTokens + 1;
+            s.low_chunk = a.window ? max(s.pos_lo - a.window + 1, 0) / C::Tokens : 0;
+            s.sink_chunks = a.window ? (int)min((long long)s.low_chunk, ((long long)a.sinks + C::Tokens - 1) / C::Tokens) : 0;
+            const int seen = s.pos_hi < 0 ? 0 : s.sink_chunks + s.pos_hi / C::Tokens - s.low_chunk + 1;
+            s.c0 = max(from - kStart, 0);
+            s.chunks = max(min(from + take - kStart, seen) - s.c0, 0);
+            s.begins = from <= kStart;
+            s.whole = s.begins && from + take == length;
+            if (lane == 0 && s.begins && !s.whole) {
+                // it goes on in other warps
+                record->rows = s.rows; record->kv = s.kv; record->row0 = s.row0; record->first = s.first;
+                record->parts = (int)((last >> 32 ? last / per : (unsigned)last / (unsigned)per) - self) + 1;
+            }
+            break;
         }
-        u += take;
-        off += take;
+        if (lane == 0) {
+            segments[warp][walked & 1] = s;
+            start_b[warp] = b;
+            start_off[warp] = off;
+            start_u[warp] = u;
+        }
+        __syncwarp();
+        ++walked;
+        p_chunks = s.chunks;
+        sent = 0;
+        read_ids(0);
         return true;
     };
-
-    // The copies: lane l has the address of tile l % CT of the segment's chunk l / CT of a batch, and reads the page
-    // ids of the batch after.
-    constexpr int kBatch = 32 / CT;
-    const int tiles_page = a.page / kTileTokens;
-    int batch_tile = 0, batch_id = 0, last_tile = -1, sent = 0;
-    const uint8_t *src = nullptr;
-    unsigned have = 0;     // lanes whose tile exists
-    auto read_ids = [&](const Segment &s, int k) {
-        k += lane / CT;
-        batch_tile = k < s.chunks ? chunk_at(s, s.c0 + k) * CT + lane % CT : last_tile + 1;
-        batch_id = batch_tile <= last_tile ? a.table[(long long)s.request * a.table_stride + batch_tile / tiles_page] : 0;
-    };
-    auto next_batch = [&](const Segment &s, int k) {
-        const bool get = batch_tile <= last_tile;
-        have = __ballot_sync(~0u, get);
-        int id = batch_id;
-        if (get && (id < 0 || id >= a.pages)) {
-            atomicCAS(status, 0, AR_EINVAL);
-            id = 0;
-        }
-        src = static_cast<const uint8_t *>(a.pool) +
-              (((long long)id * a.kv_heads + s.kv) * tiles_page + batch_tile % tiles_page) * tile_bytes(D);
-        read_ids(s, k + kBatch);
-    };
-    auto send = [&](const Segment &s) {
-        if (sent >= s.chunks) return;
+    auto send = [&]() {
         const int in = sent % kBatch * CT;    // first lane of the chunk
-        if (in == 0) next_batch(s, sent);
+        if (in == 0) {
+            const Segment &s = segments[warp][(walked - 1) & 1];
+            const bool get = batch_tile < s.end_tile;
+            have = __ballot_sync(~0u, get);
+            int id = batch_id;
+            if (get && (id < 0 || id >= a.pages)) {
+                atomicCAS(status, 0, AR_EINVAL);
+                id = 0;
+            }
+            src = static_cast<const uint8_t *>(a.pool) +
+                  (((long long)id * a.kv_heads + s.kv) * tiles_page + batch_tile % tiles_page) * tile_bytes(D);
+            read_ids(sent + kBatch);
+        }
         const uint32_t stage = filled % S, bar = bar_addr + 8 * stage, n = __popc((have >> in) & ((1u << CT) - 1));
         if (lane == in)
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n * tile_bytes(D)) : "memory");
@@ -404,40 +426,292 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
         ++sent;
         ++filled;
     };
-    // The first stage at once; the others once q is on its way, so that every warp's first data come early.
-    auto begin = [&](const Segment &s) {
-        last_tile = s.pos_hi < 0 ? -1 : s.pos_hi / kTileTokens;
-        sent = 0;
-        read_ids(s, 0);
-        send(s);
-    };
 
-    Segment seg;
-    bool more = next_segment(seg);
-    if (more) begin(seg);
-    while (more) {
-        // -- q: column g of tile n is row row0 + 8 n + g; fp16 of q / 2^e, e the row's own for bfloat16
-        uint2 qf[NT][D / 16];
-        float less[C::Over ? NT : 1][G][2];   // minus what nibbles_over puts on top of a group's products
-        float mult[NT][2];                    // what a sum of products is worth, in base 2: columns 2 t and 2 t + 1
+    // q of a segment: column g of tile n is row row0 + 8 n + g; lane t has channels 32 j + 8 t .. + 7
+    uint4 raw[NT][G];
+    auto read_q = [&](const Segment &s) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int row = seg.row0 + 8 * n + g;
-            const bool in = 8 * n + g < seg.rows;
-            float x[G][8];
-            uint32_t top = 0;
-            const T *qs = static_cast<const T *>(a.q) + (long long)(seg.first + (in ? row / c.group : 0)) * a.q_token_stride +
-                          (long long)(seg.kv * c.group + (in ? row % c.group : 0)) * a.q_head_stride + 8 * t;
+            const int row = s.row0 + 8 * n + g;
+            const bool in = 8 * n + g < s.rows;
+            const T *qs = static_cast<const T *>(a.q) + (long long)(s.first + (in ? row / c.group : 0)) * a.q_token_stride +
+                          (long long)(s.kv * c.group + (in ? row % c.group : 0)) * a.q_head_stride + 8 * t;
 #pragma unroll
             for (int j = 0; j < G; ++j) {
+                union { uint4 v; T e[8]; } x;
+                x.v = make_uint4(0, 0, 0, 0);
                 if (in) {
-                    load8(qs + 32 * j, c.vec_q != 0, x[j]);
-                } else {
+                    if (c.vec_q) {
+                        x.v = *reinterpret_cast<const uint4 *>(qs + 32 * j);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[j][i] = 0;
+                        for (int i = 0; i < 8; ++i) x.e[i] = qs[32 * j + i];
+                    }
                 }
+                raw[n][j] = x.v;
+            }
+        }
+    };
+
+    // ---- the products' side
+    uint2 qf[NT][D / 16];
+    float less[C::Over ? NT : 1][G][2];   // minus what nibbles_over puts on top of a group's products
+    float mult[NT][2];                    // what a sum of products is worth, in base 2: columns 2 t and 2 t + 1
+    float o[D / 16][NT][4];
+    float ref[NT][2], l[NT][2];
+    int vexp = 0;                         // exponent of the largest V scale so far, at least -80
+    float most = 0, vnext = 0;            // what moves the reference: a score, a scale
+    int at = -1, next = 0, end = 0;       // the segment multiplied, its next chunk and its end
+    int full0 = 0, full1 = 0, full2 = 0;  // every row sees all of its chunks below full0, and from full1 to full2
+    auto seg = [&]() -> const Segment & { return segments[warp][at & 1]; };
+
+    // One chunk.  Full: every row sees every token of it.
+    auto chunk = [&](auto is_full, const uint8_t *data, int tok0) {
+        constexpr bool Full = decltype(is_full)::value;
+        float x[CT][NT][4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[j][i]) & 0x7fffffffu);
+        for (int ct = 0; ct < CT; ++ct) {
+            const uint8_t *tile = data + ct * tile_bytes(D);
+            uint32_t w0[G], w1[G], sc0[G / 2], sc1[G / 2];
+            load_words(tile + lane * G * 4, w0);
+            load_words(tile + (32 + lane) * G * 4, w1);
+            load_words(tile + tile_ks(D) + g * G * 2, sc0);
+            load_words(tile + tile_ks(D) + (g + 8) * G * 2, sc1);
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                uint32_t h0[4], h1[4];
+                if constexpr (C::Over) {
+                    nibbles_over(w0[j], h0);
+                    nibbles_over(w1[j], h1);
+                } else {
+                    nibbles_to_half(w0[j], h0);
+                    nibbles_to_half(w1[j], h1);
+                }
+                const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
+                const float s0 = __uint_as_float(j & 1 ? sc0[j / 2] & 0xffff0000u : sc0[j / 2] << 16);
+                const float s1 = __uint_as_float(j & 1 ? sc1[j / 2] & 0xffff0000u : sc1[j / 2] << 16);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float acc[4];
+                    const uint2 q0 = qf[n][2 * j], q1 = qf[n][2 * j + 1];
+                    if constexpr (C::Over)
+                        mma16816(acc, a0, q0.x, q0.y, less[n][j][0], less[n][j][1], less[n][j][0], less[n][j][1]);
+                    else
+                        mma16816(acc, a0, q0.x, q0.y, 0.0f, 0.0f, 0.0f, 0.0f);
+                    mma16816(acc, a1, q1.x, q1.y);
+                    if (j == 0) {
+                        x[ct][n][0] = acc[0] * s0; x[ct][n][1] = acc[1] * s0;
+                        x[ct][n][2] = acc[2] * s1; x[ct][n][3] = acc[3] * s1;
+                    } else {
+                        x[ct][n][0] = fmaf(acc[0], s0, x[ct][n][0]); x[ct][n][1] = fmaf(acc[1], s0, x[ct][n][1]);
+                        x[ct][n][2] = fmaf(acc[2], s1, x[ct][n][2]); x[ct][n][3] = fmaf(acc[3], s1, x[ct][n][3]);
+                    }
+                }
+            }
+        }
+        // V scales: the largest among tokens that some row sees, infinities and NaN left out
+        float vtop = 0;
+#pragma unroll
+        for (int i = 0; i < CT * D / 128; ++i) {
+            const int wd = i * 32 + lane, ct = wd / (D / 4), in = wd % (D / 4);
+            uint32_t w = *reinterpret_cast<const uint32_t *>(data + ct * tile_bytes(D) + tile_vs(D) + in * 4);
+            if constexpr (!Full) {
+                const int tok = tok0 + ct * kTileTokens + in / (G / 2);
+                if (tok > seg().pos_hi || (a.window && tok <= seg().pos_lo - a.window && tok >= a.sinks)) w = 0;
+            }
+            vtop = fmaxf(vtop, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w))));
+        }
+        // scores under the reference; what a row does not see is -infinity
+        if constexpr (!Full) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = seg().row0 + 8 * n + 2 * t + (i & 1), p = min(seg().pos0 + row / c.group, seg().pos_hi);
+                        const int tok = tok0 + ct * kTileTokens + g + (i & 2) * 4;
+                        const bool see = tok <= p && (!a.window || tok > p - a.window || tok < a.sinks);
+                        x[ct][n][i] = see ? x[ct][n][i] * mult[n][i & 1] : -INFINITY;
+                    }
+        }
+        float y[CT][NT][4];
+        float above = kNoScore;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    y[ct][n][i] = Full ? fmaf(x[ct][n][i], mult[n][i & 1], -ref[n][i & 1]) : x[ct][n][i] - ref[n][i & 1];
+                    above = fmaxf(above, y[ct][n][i]);
+                }
+        if (__any_sync(~0u, vtop >= vnext || above > most)) {
+            if (!(vtop < INFINITY)) {
+                // an infinite scale spoils its own group; the others keep theirs
+                vtop = 0;
+#pragma unroll 1
+                for (int i = 0; i < CT * D / 64; ++i) {
+                    const int half = (i / 2 * 32 + lane) * 2 + i % 2, ct = half / (D / 2), in = half % (D / 2), tok = tok0 + ct * kTileTokens + in / G;
+                    const float v = fabsf(bf16_bits(*reinterpret_cast<const uint16_t *>(data + ct * tile_bytes(D) + tile_vs(D) + in * 2)));
+                    const bool see = Full || (tok <= seg().pos_hi && (!a.window || tok > seg().pos_lo - a.window || tok < a.sinks));
+                        if (see && v < INFINITY) vtop = fmaxf(vtop, v);
+                }
+            }
+            vexp = max(vexp, (int)(__reduce_max_sync(~0u, __float_as_uint(vtop)) >> 23) - 127);
+            most = (float)(kHead + kLead - vexp);
+            vnext = __uint_as_float((uint32_t)(vexp + 128) << 23);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float top = kNoScore;
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) top = fmaxf(top, fmaxf(x[ct][n][i], x[ct][n][i + 2]));
+                    if constexpr (Full) {
+                        // (a product with a negative scale turns the order around)
+                        float low = -kNoScore;
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) low = fminf(low, fminf(x[ct][n][i], x[ct][n][i + 2]));
+                        top = fmaxf(top * mult[n][i], low * mult[n][i]);
+                    }
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                    // the reference never falls: a lower one would let earlier weights overflow
+                    const float now = top > kNoScore ? fmaxf(ref[n][i], top + (float)(vexp - kHead)) : ref[n][i];
+                    const float keep = exp2_approx(ref[n][i] - now);
+                    ref[n][i] = now;
+                    l[n][i] *= keep;
+#pragma unroll
+                    for (int m = 0; m < D / 16; ++m) {
+                        o[m][n][i] *= keep;
+                        o[m][n][i + 2] *= keep;
+                    }
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                        for (int h = i; h < 4; h += 2)
+                            y[ct][n][h] = Full ? fmaf(x[ct][n][h], mult[n][i], -now) : x[ct][n][h] - now;
+                }
+        }
+        // weights, and the sum over V
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            const uint8_t *tile = data + ct * tile_bytes(D);
+            uint32_t w0[G], w1[G], sc0[G / 2], sc1[G / 2];
+            load_words(tile + tile_v(D) + lane * G * 4, w0);
+            load_words(tile + tile_v(D) + (32 + lane) * G * 4, w1);
+            load_words(tile + tile_vs(D) + g * G * 2, sc0);
+            load_words(tile + tile_vs(D) + (g + 8) * G * 2, sc1);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) y[ct][n][i] = exp2_approx(y[ct][n][i]);
+                l[n][0] += y[ct][n][0] + y[ct][n][2];
+                l[n][1] += y[ct][n][1] + y[ct][n][3];
+            }
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                uint32_t h0[4], h1[4];
+                nibbles_to_half(w0[j], h0);
+                nibbles_to_half(w1[j], h1);
+                const uint32_t a0[4] = {h0[0], h0[1], h1[0], h1[1]}, a1[4] = {h0[2], h0[3], h1[2], h1[3]};
+                const float s0 = __uint_as_float(j & 1 ? sc0[j / 2] & 0xffff0000u : sc0[j / 2] << 16);
+                const float s1 = __uint_as_float(j & 1 ? sc1[j / 2] & 0xffff0000u : sc1[j / 2] << 16);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float p[4] = {y[ct][n][0] * s0, y[ct][n][1] * s0, y[ct][n][2] * s1, y[ct][n][3] * s1};
+                    if constexpr (!Full) {
+                        // a scale that a row does not see can be anything
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) p[i] = y[ct][n][i] == 0 ? 0 : p[i];
+                    }
+                    const uint32_t b0 = transpose8x8(pack_half(p[0], p[1])), b1 = transpose8x8(pack_half(p[2], p[3]));
+                    mma16816(o[2 * j][n], a0, b0, b1);
+                    mma16816(o[2 * j + 1][n], a1, b0, b1);
+                }
+            }
+        }
+    };
+
+
+    for (;;) {
+        // Fill the free stages, going on into the next segment; at the start one, so that every warp's first data come early.
+#pragma unroll 1
+        while (filled - used < (at < 0 ? 1 : S)) {
+            if (sent < p_chunks) send();
+            else if (walked - 1 > at || !walk()) break;
+        }
+#pragma unroll 1
+        while (next < end) {
+            const uint32_t stage = used % S;
+            if (!late) late = !bar_wait(bar_addr + 8 * stage, (used / S) & 1, status);
+            const uint8_t *data = ring + stage * C::Stage;
+            if (next < full0 || (next >= full1 && next < full2))
+                chunk(std::true_type(), data, 0);
+            else
+                chunk(std::false_type(), data, chunk_at(next, seg().sink_chunks, seg().low_chunk) * C::Tokens);
+            ++next;
+            ++used;
+            __syncwarp();      // every lane has read the stage
+            if (sent >= p_chunks) break;
+            send();
+        }
+        if (next < end) continue;
+
+        // The segment's end.  The next one's q comes while the results go.
+        const bool more = at + 1 < walked;
+        if (more) read_q(segments[warp][(at + 1) & 1]);
+        if (at >= 0) {
+            const Segment &seg = segments[warp][at & 1];
+            // -- results: to their rows, or one part of them to the workspace
+            float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kPartAt) +
+                          (2 * (size_t)self + (seg.begins ? 1 : 0)) * C::PartFloats;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) l[n][i] += __shfl_xor_sync(~0u, l[n][i], d);
+                    const int col = 8 * n + 2 * t + i, row = seg.row0 + col;
+                    if (col < seg.rows) {
+                        const long long token = seg.first + row / c.group;
+                        const int head = seg.kv * c.group + row % c.group;
+#pragma unroll
+                        for (int j = 0; j < G; ++j) {
+                            const float4 v = make_float4(o[2 * j][n][i], o[2 * j][n][i + 2], o[2 * j + 1][n][i], o[2 * j + 1][n][i + 2]);
+                            const int channel = 32 * j + 4 * g;
+                            if (seg.whole) store_row<T>(c, token, head, channel, v, ref[n][i], l[n][i]);
+                            else *reinterpret_cast<float4 *>(part + col * D + channel) = v;
+                        }
+                        if (!seg.whole && g == 0) *reinterpret_cast<float2 *>(part + C::Rows * D + 2 * col) = make_float2(ref[n][i], l[n][i]);
+                    }
+                }
+            }
+        }
+        if (!more) break;
+        ++at;
+        next = seg().c0;
+        end = next + seg().chunks;
+        full0 = a.window ? min(seg().sink_chunks, a.sinks / C::Tokens) : 0;
+        full1 = seg().pos_hi < a.window || !a.window ? seg().sink_chunks - seg().low_chunk
+                                                     : seg().sink_chunks - seg().low_chunk + (seg().pos_hi - a.window) / C::Tokens + 1;
+        full2 = seg().pos_lo < 0 ? 0 : seg().sink_chunks - seg().low_chunk + (int)(((long long)seg().pos_lo + 1) / C::Tokens);
+
+        // -- operands of q: fp16 of q / 2^e, e the row's own for bfloat16
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float x[G][8];
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                union { uint4 v; T e[8]; } w;
+                w.v = raw[n][j];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[j][i] = Elem<T>::to_float(w.e[i]);
+                    top = max(top, __float_as_uint(x[j][i]) & 0x7fffffffu);
+                }
             }
             float unit = 1, worth = a.scale * 1.4426950408889634f;
             if constexpr (std::is_same<T, __nv_bfloat16>::value) {
@@ -476,13 +750,9 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
             for (int i = 0; i < 2; ++i) mult[n][i] = __shfl_sync(~0u, worth, (2 * t + i) * 4);
         }
 
-#pragma unroll 1
-        for (int i = 1; i < S; ++i) send(seg);
-
-        float o[D / 16][NT][4];
-        float ref[NT][2], l[NT][2];
-        int vexp = -80;                      // exponent of the largest V scale so far, at least -80
-        float most = kHead + kLead + 80, vnext = __uint_as_float((uint32_t)(128 - 80) << 23);   // what moves the reference: a score, a scale
+        vexp = -80;
+        most = kHead + kLead + 80;
+        vnext = __uint_as_float((uint32_t)(128 - 80) << 23);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -492,226 +762,14 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
             ref[n][0] = ref[n][1] = kNoScore;
             l[n][0] = l[n][1] = 0;
         }
-
-        // One chunk.  Full: every row sees every token of it.
-        auto chunk = [&](auto is_full, const uint8_t *data, int tok0) {
-            constexpr bool Full = decltype(is_full)::value;
-            float x[CT][NT][4];
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const uint8_t *tile = data + ct * tile_bytes(D);
-                uint32_t w0[G], w1[G], sc0[G / 2], sc1[G / 2];
-                load_words(tile + lane * G * 4, w0);
-                load_words(tile + (32 + lane) * G * 4, w1);
-                load_words(tile + tile_ks(D) + g * G * 2, sc0);
-                load_words(tile + tile_ks(D) + (g + 8) * G * 2, sc1);
-#pragma unroll
-                for (int j = 0; j < G; ++j) {
-                    uint32_t h0[4], h1[4];
-                    if constexpr (C::Over) {
-                        nibbles_over(w0[j], h0);
-                        nibbles_over(w1[j], h1);
-                    } else {
-                        nibbles_to_half(w0[j], h0);
-                        nibbles_to_half(w1[j], h1);
-                    }
-                    const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
-                    const float s0 = __uint_as_float(j & 1 ? sc0[j / 2] & 0xffff0000u : sc0[j / 2] << 16);
-                    const float s1 = __uint_as_float(j & 1 ? sc1[j / 2] & 0xffff0000u : sc1[j / 2] << 16);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float acc[4];
-                        const uint2 q0 = qf[n][2 * j], q1 = qf[n][2 * j + 1];
-                        if constexpr (C::Over)
-                            mma16816(acc, a0, q0.x, q0.y, less[n][j][0], less[n][j][1], less[n][j][0], less[n][j][1]);
-                        else
-                            mma16816(acc, a0, q0.x, q0.y, 0.0f, 0.0f, 0.0f, 0.0f);
-                        mma16816(acc, a1, q1.x, q1.y);
-                        if (j == 0) {
-                            x[ct][n][0] = acc[0] * s0; x[ct][n][1] = acc[1] * s0;
-                            x[ct][n][2] = acc[2] * s1; x[ct][n][3] = acc[3] * s1;
-                        } else {
-                            x[ct][n][0] = fmaf(acc[0], s0, x[ct][n][0]); x[ct][n][1] = fmaf(acc[1], s0, x[ct][n][1]);
-                            x[ct][n][2] = fmaf(acc[2], s1, x[ct][n][2]); x[ct][n][3] = fmaf(acc[3], s1, x[ct][n][3]);
-                        }
-                    }
-                }
-            }
-            // V scales: the largest among tokens that some row sees, infinities and NaN left out
-            float vtop = 0;
-#pragma unroll
-            for (int i = 0; i < CT * D / 128; ++i) {
-                const int wd = i * 32 + lane, ct = wd / (D / 4), in = wd % (D / 4);
-                uint32_t w = *reinterpret_cast<const uint32_t *>(data + ct * tile_bytes(D) + tile_vs(D) + in * 4);
-                if constexpr (!Full) {
-                    const int tok = tok0 + ct * kTileTokens + in / (G / 2);
-                    if (tok > seg.pos_hi || (a.window && tok <= seg.pos_lo - a.window && tok >= a.sinks)) w = 0;
-                }
-                vtop = fmaxf(vtop, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w))));
-            }
-            // scores under the reference; what a row does not see is -infinity
-            if constexpr (!Full) {
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = seg.row0 + 8 * n + 2 * t + (i & 1), p = min(seg.pos0 + row / c.group, seg.pos_hi);
-                            const int tok = tok0 + ct * kTileTokens + g + (i & 2) * 4;
-                            const bool see = tok <= p && (!a.window || tok > p - a.window || tok < a.sinks);
-                            x[ct][n][i] = see ? x[ct][n][i] * mult[n][i & 1] : -INFINITY;
-                        }
-            }
-            float y[CT][NT][4];
-            float above = kNoScore;
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        y[ct][n][i] = Full ? fmaf(x[ct][n][i], mult[n][i & 1], -ref[n][i & 1]) : x[ct][n][i] - ref[n][i & 1];
-                        above = fmaxf(above, y[ct][n][i]);
-                    }
-            if (__any_sync(~0u, vtop >= vnext || above > most)) {
-                if (!(vtop < INFINITY)) {
-                    // an infinite scale spoils its own group; the others keep theirs
-                    vtop = 0;
-#pragma unroll 1
-                    for (int i = 0; i < CT * D / 64; ++i) {
-                        const int half = (i / 2 * 32 + lane) * 2 + i % 2, ct = half / (D / 2), in = half % (D / 2), tok = tok0 + ct * kTileTokens + in / G;
-                        const float v = fabsf(bf16_bits(*reinterpret_cast<const uint16_t *>(data + ct * tile_bytes(D) + tile_vs(D) + in * 2)));
-                        if (v < INFINITY && tok <= seg.pos_hi && (!a.window || tok > seg.pos_lo - a.window || tok < a.sinks)) vtop = fmaxf(vtop, v);
-                    }
-                }
-                vexp = max(vexp, (int)(__reduce_max_sync(~0u, __float_as_uint(vtop)) >> 23) - 127);
-                most = (float)(kHead + kLead - vexp);
-                vnext = __uint_as_float((uint32_t)(vexp + 128) << 23);
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float top = kNoScore;
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) top = fmaxf(top, fmaxf(x[ct][n][i], x[ct][n][i + 2]));
-                        if constexpr (Full) {
-                            // (a product with a negative scale turns the order around)
-                            float low = -kNoScore;
-#pragma unroll
-                            for (int ct = 0; ct < CT; ++ct) low = fminf(low, fminf(x[ct][n][i], x[ct][n][i + 2]));
-                            top = fmaxf(top * mult[n][i], low * mult[n][i]);
-                        }
-#pragma unroll
-                        for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-                        // the reference never falls: a lower one would let earlier weights overflow
-                        const float now = top > kNoScore ? fmaxf(ref[n][i], top + (float)(vexp - kHead)) : ref[n][i];
-                        const float keep = exp2_approx(ref[n][i] - now);
-                        ref[n][i] = now;
-                        l[n][i] *= keep;
-#pragma unroll
-                        for (int m = 0; m < D / 16; ++m) {
-                            o[m][n][i] *= keep;
-                            o[m][n][i + 2] *= keep;
-                        }
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                            for (int h = i; h < 4; h += 2)
-                                y[ct][n][h] = Full ? fmaf(x[ct][n][h], mult[n][i], -now) : x[ct][n][h] - now;
-                    }
-            }
-            // weights, and the sum over V
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const uint8_t *tile = data + ct * tile_bytes(D);
-                uint32_t w0[G], w1[G], sc0[G / 2], sc1[G / 2];
-                load_words(tile + tile_v(D) + lane * G * 4, w0);
-                load_words(tile + tile_v(D) + (32 + lane) * G * 4, w1);
-                load_words(tile + tile_vs(D) + g * G * 2, sc0);
-                load_words(tile + tile_vs(D) + (g + 8) * G * 2, sc1);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) y[ct][n][i] = exp2_approx(y[ct][n][i]);
-                    l[n][0] += y[ct][n][0] + y[ct][n][2];
-                    l[n][1] += y[ct][n][1] + y[ct][n][3];
-                }
-#pragma unroll
-                for (int j = 0; j < G; ++j) {
-                    uint32_t h0[4], h1[4];
-                    nibbles_to_half(w0[j], h0);
-                    nibbles_to_half(w1[j], h1);
-                    const uint32_t a0[4] = {h0[0], h0[1], h1[0], h1[1]}, a1[4] = {h0[2], h0[3], h1[2], h1[3]};
-                    const float s0 = __uint_as_float(j & 1 ? sc0[j / 2] & 0xffff0000u : sc0[j / 2] << 16);
-                    const float s1 = __uint_as_float(j & 1 ? sc1[j / 2] & 0xffff0000u : sc1[j / 2] << 16);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float p[4] = {y[ct][n][0] * s0, y[ct][n][1] * s0, y[ct][n][2] * s1, y[ct][n][3] * s1};
-                        if constexpr (!Full) {
-                            // a scale that a row does not see can be anything
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) p[i] = y[ct][n][i] == 0 ? 0 : p[i];
-                        }
-                        const uint32_t b0 = transpose8x8(pack_half(p[0], p[1])), b1 = transpose8x8(pack_half(p[2], p[3]));
-                        mma16816(o[2 * j][n], a0, b0, b1);
-                        mma16816(o[2 * j + 1][n], a1, b0, b1);
-                    }
-                }
-            }
-        };
-
-        for (int k = 0; k < seg.chunks; ++k) {
-            const uint32_t stage = used % S;
-            if (!late) late = !bar_wait(bar_addr + 8 * stage, (used / S) & 1, status);
-            const uint8_t *data = ring + stage * C::Stage;
-            const int tok0 = chunk_at(seg, seg.c0 + k) * C::Tokens;
-            if (tok0 + C::Tokens - 1 <= seg.pos_lo && (!a.window || tok0 > seg.pos_hi - a.window || tok0 <= a.sinks - C::Tokens))
-                chunk(std::true_type(), data, tok0);
-            else
-                chunk(std::false_type(), data, tok0);
-            ++used;
-            __syncwarp();      // every lane has read the stage
-            send(seg);
-        }
-
-        const Segment now = seg;
-        more = next_segment(seg);
-        if (more) begin(seg);
-
-        // -- results: to their rows, or one part of them to the workspace
-        float *part = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kPartAt) +
-                      (2 * (size_t)self + (now.begins ? 1 : 0)) * C::PartFloats;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int d = 4; d < 32; d *= 2) l[n][i] += __shfl_xor_sync(~0u, l[n][i], d);
-                const int col = 8 * n + 2 * t + i, row = now.row0 + col;
-                if (col < now.rows) {
-                    const long long token = now.first + row / c.group;
-                    const int head = now.kv * c.group + row % c.group;
-#pragma unroll
-                    for (int j = 0; j < G; ++j) {
-                        const float4 v = make_float4(o[2 * j][n][i], o[2 * j][n][i + 2], o[2 * j + 1][n][i], o[2 * j + 1][n][i + 2]);
-                        const int channel = 32 * j + 4 * g;
-                        if (now.whole) store_row<T>(c, token, head, channel, v, ref[n][i], l[n][i]);
-                        else *reinterpret_cast<float4 *>(part + col * D + channel) = v;
-                    }
-                    if (!now.whole && g == 0) *reinterpret_cast<float2 *>(part + C::Rows * D + 2 * col) = make_float2(ref[n][i], l[n][i]);
-                }
-            }
-        }
     }
 }
 
 // Joins the parts of the segment that begins in a warp, in their order.  A
 // block to a warp's record and, by Spread, to one of its rows: then groups of D / 4
 // threads share out the parts, for where a few rows have many.
-constexpr int kJoinThreads = 256;
 
-template <typename T, class C, bool Spread>
+template <typename T, class C, bool Spread, int kJoinThreads = Spread ? 256 : 128>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Attend c) {
     constexpr int D = C::D, Quads = D / 4, Groups = Spread ? kJoinThreads / Quads : 1;
     __shared__ float4 rows[Groups][Quads];
@@ -789,16 +847,16 @@ int start(const Attend &c, cudaStream_t s) {
     // No more blocks than the longest contexts the table can hold would fill.
     const long long chunks = max(((long long)c.a.table_width * c.a.page + C::Tokens - 1) / C::Tokens, 1ll);
     const long long blocks = ((long long)c.a.tokens * c.group + C::Rows - 1) / C::Rows + c.a.requests;
-    const long long share = (long long)c.min_chunks * kWarps, most = (blocks * chunks * c.a.kv_heads + share - 1) / share;
+    const long long share = (long long)c.min_chunks * kWarps, most = (blocks * (chunks + kStart) * c.a.kv_heads + share - 1) / share;
     grid = (int)min((long long)grid, most);
     void *args[] = {const_cast<Attend *>(&c)};
     cudaError_t e = cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3(kWarps * 32), args, C::Smem, s);
     // The joining kernel comes to the GPU beside the end of the first, and waits for it.
-    if (e == cudaSuccess && chunks > c.min_chunks) {
+    if (e == cudaSuccess && chunks > 1) {     // one chunk is never split
         const bool spread = (long long)c.a.requests * c.a.kv_heads <= kSpreadSegments;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(grid * kWarps), spread ? C::Rows : 1);
-        cfg.blockDim = dim3(kJoinThreads);
+        cfg.blockDim = dim3(spread ? 256 : 128);
         cfg.stream = s;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
