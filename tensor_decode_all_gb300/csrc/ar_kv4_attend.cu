@@ -138,11 +138,12 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
     }
 }
 
-template <int D_, int NT_, int CT_, int S_, int Blocks_>
+template <int D_, int NT_, int CT_, int CI_, int S_, int Blocks_>
 struct Shape {
     static constexpr int D = D_;              // head dim
     static constexpr int NT = NT_;            // 8-row tiles of query rows
     static constexpr int CT = CT_;            // tiles of a chunk, the unit of work and a stage of the ring
+    static constexpr int CI = CI_;            // tiles multiplied together: enough to hide latencies, few enough for the instruction cache
     static constexpr int S = S_;              // stages
     static constexpr int Blocks = Blocks_;    // of an SM, for which registers are kept
     static constexpr int G = D / kGroup;
@@ -254,7 +255,7 @@ __device__ __forceinline__ void store_row(const Attend &c, long long token, int 
 
 template <typename T, class C>
 __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __grid_constant__ Attend c) {
-    constexpr int D = C::D, NT = C::NT, CT = C::CT, S = C::S, G = C::G;
+    constexpr int D = C::D, NT = C::NT, CT = C::CT, CI = C::CI, S = C::S, G = C::G;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) unsigned long long bars[kWarps * S];
     __shared__ long long sums[kWarps], start_off[kWarps], start_u[kWarps];   // where each warp's walk stands
@@ -465,12 +466,12 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
     int full0 = 0, full1 = 0, full2 = 0;  // every row sees all of its chunks below full0, and from full1 to full2
     auto seg = [&]() -> const Segment & { return segments[warp][at & 1]; };
 
-    // One chunk.  Full: every row sees every token of it.
-    auto chunk = [&](auto is_full, const uint8_t *data, int tok0) {
+    // CI tiles of a chunk.  Full: every row sees every token of it.
+    auto multiply = [&](auto is_full, const uint8_t *data, int tok0) {
         constexpr bool Full = decltype(is_full)::value;
-        float x[CT][NT][4];
+        float x[CI][NT][4];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
+        for (int ct = 0; ct < CI; ++ct) {
             const uint8_t *tile = data + ct * tile_bytes(D);
             uint32_t w0[G], w1[G], sc0[G / 2], sc1[G / 2];
             load_words(tile + lane * G * 4, w0);
@@ -512,7 +513,7 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
         // V scales: the largest among tokens that some row sees, infinities and NaN left out
         float vtop = 0;
 #pragma unroll
-        for (int i = 0; i < CT * D / 128; ++i) {
+        for (int i = 0; i < CI * D / 128; ++i) {
             const int wd = i * 32 + lane, ct = wd / (D / 4), in = wd % (D / 4);
             uint32_t w = *reinterpret_cast<const uint32_t *>(data + ct * tile_bytes(D) + tile_vs(D) + in * 4);
             if constexpr (!Full) {
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
         // scores under the reference; what a row does not see is -infinity
         if constexpr (!Full) {
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
+            for (int ct = 0; ct < CI; ++ct)
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -535,10 +536,10 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
                         x[ct][n][i] = see ? x[ct][n][i] * mult[n][i & 1] : -INFINITY;
                     }
         }
-        float y[CT][NT][4];
+        float y[CI][NT][4];
         float above = kNoScore;
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
+        for (int ct = 0; ct < CI; ++ct)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -551,7 +552,7 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
                 // an infinite scale spoils its own group; the others keep theirs
                 vtop = 0;
 #pragma unroll 1
-                for (int i = 0; i < CT * D / 64; ++i) {
+                for (int i = 0; i < CI * D / 64; ++i) {
                     const int half = (i / 2 * 32 + lane) * 2 + i % 2, ct = half / (D / 2), in = half % (D / 2), tok = tok0 + ct * kTileTokens + in / G;
                     const float v = fabsf(bf16_bits(*reinterpret_cast<const uint16_t *>(data + ct * tile_bytes(D) + tile_vs(D) + in * 2)));
                     const bool see = Full || (tok <= seg().pos_hi && (!a.window || tok > seg().pos_lo - a.window || tok < a.sinks));
@@ -567,12 +568,12 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
                 for (int i = 0; i < 2; ++i) {
                     float top = kNoScore;
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) top = fmaxf(top, fmaxf(x[ct][n][i], x[ct][n][i + 2]));
+                    for (int ct = 0; ct < CI; ++ct) top = fmaxf(top, fmaxf(x[ct][n][i], x[ct][n][i + 2]));
                     if constexpr (Full) {
                         // (a product with a negative scale turns the order around)
                         float low = -kNoScore;
 #pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) low = fminf(low, fminf(x[ct][n][i], x[ct][n][i + 2]));
+                        for (int ct = 0; ct < CI; ++ct) low = fminf(low, fminf(x[ct][n][i], x[ct][n][i + 2]));
                         top = fmaxf(top * mult[n][i], low * mult[n][i]);
                     }
 #pragma unroll
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
                         o[m][n][i + 2] *= keep;
                     }
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
+                    for (int ct = 0; ct < CI; ++ct)
 #pragma unroll
                         for (int h = i; h < 4; h += 2)
                             y[ct][n][h] = Full ? fmaf(x[ct][n][h], mult[n][i], -now) : x[ct][n][h] - now;
@@ -596,7 +597,7 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
         }
         // weights, and the sum over V
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
+        for (int ct = 0; ct < CI; ++ct) {
             const uint8_t *tile = data + ct * tile_bytes(D);
             uint32_t w0[G], w1[G], sc0[G / 2], sc1[G / 2];
             load_words(tile + tile_v(D) + lane * G * 4, w0);
@@ -647,10 +648,14 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
             const uint32_t stage = used % S;
             if (!late) late = !bar_wait(bar_addr + 8 * stage, (used / S) & 1, status);
             const uint8_t *data = ring + stage * C::Stage;
-            if (next < full0 || (next >= full1 && next < full2))
-                chunk(std::true_type(), data, 0);
-            else
-                chunk(std::false_type(), data, chunk_at(next, seg().sink_chunks, seg().low_chunk) * C::Tokens);
+            if (next < full0 || (next >= full1 && next < full2)) {
+#pragma unroll 1
+                for (int i = 0; i < CT; i += CI) multiply(std::true_type(), data + i * tile_bytes(D), 0);
+            } else {
+                const int tok0 = chunk_at(next, seg().sink_chunks, seg().low_chunk) * C::Tokens;
+#pragma unroll 1
+                for (int i = 0; i < CT; i += CI) multiply(std::false_type(), data + i * tile_bytes(D), tok0 + i * kTileTokens);
+            }
             ++next;
             ++used;
             __syncwarp();      // every lane has read the stage
@@ -872,9 +877,9 @@ template <typename T>
 int start(const Attend &c, cudaStream_t s) {
     const long long rows = (long long)max(c.a.max_new, 1) * c.group;
     switch (c.a.head_dim) {
-        case 64: return rows <= 8 ? start<T, Shape<64, 1, 4, 3, 3>>(c, s) : start<T, Shape<64, 2, 4, 3, 3>>(c, s);
-        case 128: return rows <= 8 ? start<T, Shape<128, 1, 4, 2, 3>>(c, s) : start<T, Shape<128, 2, 2, 4, 2>>(c, s);
-        default: return start<T, Shape<256, 1, 1, 5, 2>>(c, s);
+        case 64: return rows <= 8 ? start<T, Shape<64, 1, 4, 2, 3, 3>>(c, s) : start<T, Shape<64, 2, 4, 2, 3, 3>>(c, s);
+        case 128: return rows <= 8 ? start<T, Shape<128, 1, 4, 2, 2, 3>>(c, s) : start<T, Shape<128, 2, 2, 1, 4, 2>>(c, s);
+        default: return start<T, Shape<256, 1, 1, 1, 5, 2>>(c, s);
     }
 }
 
