@@ -146,8 +146,14 @@ extern "C" AR_API int ar_kv_plan(const ar_kv_plan_args *args, ar_stream_t stream
     // One block while its threads have about one token each, else a cluster of 8.
     const int blocks = a.max_tokens > 2 * kPlanThreads ? 8 : 1;
     const size_t smem = (size_t)a.requests * 3 * sizeof(int);
-    if (cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanRequests * 12) != cudaSuccess)
-        return launch_status(cudaErrorUnknown);
+    static bool ready[64] = {};      // the attribute is set once a device; racing threads set the same
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return launch_status(cudaErrorUnknown);
+    if (!*(volatile bool *)&ready[dev]) {
+        if (cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPlanRequests * 12) != cudaSuccess)
+            return launch_status(cudaErrorUnknown);
+        *(volatile bool *)&ready[dev] = true;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(kPlanThreads);

@@ -1,8 +1,10 @@
 // ar_norm_fp8.cu -- ar_add_norm_fp8: residual, RMS norm and e4m3 output with scales.
 //
-// One block takes a row: h = x + residual goes to shared memory while its
-// squares are summed, then y = h * rsqrt(mean + eps) * weight is taken group by
-// group, a warp each, for the group's maximum and its quotients.
+// One pass: a block takes a row and keeps h = x + residual in registers.  Since
+// y = h * w * inv with inv = 1 / sqrt(mean + eps) common to the row, the largest |y|
+// of a group is inv times its largest |h * w|: the sum of squares and the maxima
+// come out of one round through shared memory.  Rows that do not lie on 16 bytes
+// and groups that a warp's lanes do not divide take a kernel that goes through shared memory.
 #include <cuda_fp8.h>
 
 #include "ar_kv4.cuh"
@@ -13,6 +15,7 @@ using namespace tda;
 
 constexpr int kNormThreads = 256;
 constexpr int kNormDim = 32768;
+constexpr int kFewRows = 304;             // two blocks to a multiprocessor
 
 __device__ __forceinline__ float block_sum(float v, float *buf) {
 #pragma unroll
@@ -28,6 +31,88 @@ __device__ __forceinline__ float block_sum(float v, float *buf) {
 // The larger of two magnitudes; a NaN wins.
 __device__ __forceinline__ float top_of(float a, float b) {
     return __uint_as_float(max(__float_as_uint(a) & 0x7fffffffu, __float_as_uint(b) & 0x7fffffffu));
+}
+
+// Vectors of 8 channels, V to a thread: vector i * blockDim.x + threadIdx.x.  Lanes: threads that share a group (a
+// power of two up to 32; 0: the row is one group).
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) norm_rows_kernel(const ar_add_norm_fp8_args a, int lanes) {
+    __shared__ float2 buf[32];
+    const int64_t row = blockIdx.x;
+    const int vecs = a.dim / 8, warps = (blockDim.x + 31) / 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + row * a.x_stride);
+    const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.residual) + row * a.residual_stride);
+    const uint4 *w = static_cast<const uint4 *>(a.weight);
+    union Vec { uint4 v; T e[8]; };
+    Vec xv[V], rv[V], wv[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int at = i * blockDim.x + threadIdx.x;
+        xv[i].v = rv[i].v = wv[i].v = make_uint4(0, 0, 0, 0);
+        if (at < vecs) {
+            xv[i].v = __ldcs(x + at);
+            if (a.residual) rv[i].v = __ldcs(r + at);
+            wv[i].v = __ldg(w + at);
+        }
+    }
+    float h[V][8], top[V], sum = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        top[i] = 0;
+        Vec out;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float v = Elem<T>::to_float(xv[i].e[e]) + (a.residual ? Elem<T>::to_float(rv[i].e[e]) : 0.0f);
+            out.e[e] = Elem<T>::from_float(v);
+            sum = fmaf(v, v, sum);
+            h[i][e] = v * Elem<T>::to_float(wv[i].e[e]);
+            top[i] = top_of(top[i], h[i][e]);
+        }
+        const int at = i * blockDim.x + threadIdx.x;
+        if (a.residual_out && at < vecs)
+            reinterpret_cast<uint4 *>(static_cast<T *>(a.residual_out) + row * a.residual_out_stride)[at] = out.v;
+    }
+    float most = 0;
+    if (lanes == 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) most = top_of(most, top[i]);
+    }
+#pragma unroll
+    for (int d = 16; d; d /= 2) {
+        sum += __shfl_xor_sync(~0u, sum, d);
+        if (lanes == 0) {
+            most = top_of(most, __shfl_xor_sync(~0u, most, d));
+        } else if (d < lanes) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) top[i] = top_of(top[i], __shfl_xor_sync(~0u, top[i], d));
+        }
+    }
+    if (lane == 0) buf[warp] = make_float2(sum, most);
+    __syncthreads();
+    // every warp adds the warps' sums for itself, in the same order
+    const float2 part = lane < warps ? buf[lane] : make_float2(0, 0);
+    sum = part.x;
+    most = part.y;
+#pragma unroll
+    for (int d = 16; d; d /= 2) {
+        sum += __shfl_xor_sync(~0u, sum, d);
+        most = top_of(most, __shfl_xor_sync(~0u, most, d));
+    }
+    const float inv = rsqrtf(__fdiv_rn(sum, (float)a.dim) + a.eps);
+    uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + row * a.dim);
+    const int groups = lanes ? (vecs + lanes - 1) / lanes : 1;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int at = i * blockDim.x + threadIdx.x;
+        const float y = (lanes ? top[i] : most) * inv, scale = y == 0 ? 1.0f : __fdiv_rn(y, 448.0f), q = __fdiv_rn(inv, scale);
+        if (at >= vecs) break;
+        uint32_t b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            b[e] = __nv_cvt_float2_to_fp8x2(make_float2(h[i][2 * e] * q, h[i][2 * e + 1] * q), __NV_SATFINITE, __NV_E4M3);
+        __stcs(out + at, make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16));
+        if (lanes ? at % lanes == 0 : at == 0) a.scales[row * groups + (lanes ? at / lanes : 0)] = scale;
+    }
 }
 
 template <typename T>
@@ -83,12 +168,37 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const ar_add_norm_fp
     }
 }
 
+bool aligned16(const void *p, int64_t stride) { return !misaligned(p, 16) && stride % 8 == 0; }
+
 template <typename T>
 cudaError_t start(const ar_add_norm_fp8_args &a, cudaStream_t s) {
-    const size_t smem = (size_t)a.dim * 4;
-    const cudaError_t e = cudaFuncSetAttribute(norm_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormDim * 4);
+    // Threads that share a group of the vector kernel; -1: it cannot take the call.
+    int lanes = -1;
+    if (a.dim % 8 == 0 && aligned16(a.x, a.x_stride) && aligned16(a.residual, a.residual_stride) && aligned16(a.weight, 0) &&
+        aligned16(a.residual_out, a.residual_out_stride) && !misaligned(a.out, 8)) {
+        if (a.group == 0 || a.group == a.dim) lanes = 0;
+        else if (a.group == 8 || a.group == 16 || a.group == 32 || a.group == 64 || a.group == 128 || a.group == 256) lanes = a.group / 8;
+    }
+    if (lanes >= 0) {
+        // Few rows: a vector a thread, for the shortest way through a row.  Many: two, for more loads in flight from
+        // fewer warps (measured below at the launch sizes of a step and of a chunk).
+        const int vecs = a.dim / 8;
+        const int v = vecs > 2048 ? 4 : vecs > 1024 || (a.rows > kFewRows && vecs >= 128) ? 2 : 1;
+        const int threads = ((vecs + v - 1) / v + 31) / 32 * 32;
+        if (v == 1) norm_rows_kernel<T, 1><<<(unsigned)a.rows, threads, 0, s>>>(a, lanes);
+        else if (v == 2) norm_rows_kernel<T, 2><<<(unsigned)a.rows, threads, 0, s>>>(a, lanes);
+        else norm_rows_kernel<T, 4><<<(unsigned)a.rows, threads, 0, s>>>(a, lanes);
+        return cudaGetLastError();
+    }
+    static bool ready[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !*(volatile bool *)&ready[dev])) {
+        e = cudaFuncSetAttribute(norm_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormDim * 4);
+        if (e == cudaSuccess && dev < 64) *(volatile bool *)&ready[dev] = true;
+    }
     if (e != cudaSuccess) return e;
-    norm_kernel<T><<<(unsigned)a.rows, kNormThreads, smem, s>>>(a);
+    norm_kernel<T><<<(unsigned)a.rows, kNormThreads, (size_t)a.dim * 4, s>>>(a);
     return cudaGetLastError();
 }
 
