@@ -2,7 +2,7 @@
 // in the paged cache, and back.
 //
 // append, per group of 32 channels:  scale = bf16(max|x| / 7),  n = rint(x / scale).
-// The division by 7 and by the scale are IEEE ones, so that a plain
+// Both quotients are rounded as IEEE division rounds them, so that a plain
 // implementation in binary32 writes the same bytes.
 #include "ar_kv4.cuh"
 
@@ -50,20 +50,26 @@ __device__ __forceinline__ void get_words(const uint32_t *p, uint32_t (&w)[G]) {
     }
 }
 
-// N consecutive elements (4 or 8), one access where the rows lie on 16 bytes.
+// N consecutive elements (4 or 8) as pairs, one access where the rows lie on 16 bytes.
 template <typename T, int N>
-__device__ __forceinline__ void get_row(const T *p, bool vec, float (&x)[N]) {
-    union { uint4 v; uint2 u; T e[8]; } w;
+__device__ __forceinline__ void get_row(const T *p, bool vec, uint32_t (&x)[N / 2]) {
     if (!vec) {
+        const unsigned short *e = reinterpret_cast<const unsigned short *>(p);
 #pragma unroll
-        for (int i = 0; i < N; ++i) w.e[i] = p[i];
+        for (int i = 0; i < N / 2; ++i) x[i] = e[2 * i] | (uint32_t)e[2 * i + 1] << 16;
     } else if constexpr (N == 8) {
-        w.v = __ldcs(reinterpret_cast<const uint4 *>(p));
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(p));
+        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
     } else {
-        w.u = __ldcs(reinterpret_cast<const uint2 *>(p));
+        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+        x[0] = v.x; x[1] = v.y;
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = Elem<T>::to_float(w.e[i]);
+}
+
+// Both elements of a pair.
+__device__ __forceinline__ float2 pair_of(uint32_t w, __half) { return __half22float2(*reinterpret_cast<__half2 *>(&w)); }
+__device__ __forceinline__ float2 pair_of(uint32_t w, __nv_bfloat16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 template <typename T, int N>
@@ -82,26 +88,50 @@ __device__ __forceinline__ void put_row(T *p, bool vec, const float (&x)[N]) {
 }
 
 // A group's scale and N of its channels as nibbles; Lanes threads (First to First * Lanes / 2 apart) hold the group.
-template <int N, int Lanes, int First>
-__device__ __forceinline__ uint32_t quantise(const float (&x)[N], __nv_bfloat16 &scale) {
-    // The largest magnitude as bits, so that a NaN (above every number) wins.
+template <typename T, int N, int Lanes, int First>
+__device__ __forceinline__ uint32_t quantise(const uint32_t (&pairs)[N / 2], __nv_bfloat16 &scale) {
+    // The largest magnitude by its bits, so that a NaN (above every number) wins.
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    for (int i = 0; i < N / 2; ++i) top = __vmaxu2(top, pairs[i] & 0x7fff7fffu);
 #pragma unroll
-    for (int d = First; d < First * Lanes; d *= 2) top = max(top, __shfl_xor_sync(~0u, top, d));
-    scale = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 7.0f));
+    for (int d = First; d < First * Lanes; d *= 2) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, d));
+    const float2 tops = pair_of(max(top & 0xffffu, top >> 16), T());
+    float x[N];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const float2 v = pair_of(pairs[i], T());
+        x[2 * i] = v.x;
+        x[2 * i + 1] = v.y;
+    }
+    scale = __float2bfloat16_rn(__fdiv_rn(tops.x, 7.0f));
     const float s = __bfloat162float(scale);
     uint32_t w = 0;
+    if (s >= 0x1p-100f && s <= 0x1p100f) {
+        // x / s rounded as IEEE division rounds it, from the rounded 1 / s and one exact remainder (P. Markstein,
+        // "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).  |x / s| < 7.02, so the
+        // sum with 1.5 * 2^23 rounds it half to even into the low bits.
+        const float r = __frcp_rn(s);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float f = rintf(__fdiv_rn(x[i], s));
-        // fmax and fmin turn NaN into a bound, so NaN (and 0 / 0) is asked for first
-        const uint32_t n = (uint32_t)(f == f ? (int)fminf(fmaxf(f, -7.0f), 7.0f) + 8 : 8);
-        w |= n << (4 * i);
+        for (int i = 0; i < N; ++i) {
+            const float q = x[i] * r, n = fmaf(fmaf(-q, s, x[i]), r, q) + (12582912.0f + 8.0f);
+            w |= (__float_as_uint(n) & 15u) << (4 * i);
+        }
+    } else {
+        // zeros, the type's ends, infinities and NaN
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float f = rintf(__fdiv_rn(x[i], s));
+            // fmax and fmin turn NaN into a bound, so NaN (and 0 / 0) is asked for first
+            const uint32_t n = (uint32_t)(f == f ? (int)fminf(fmaxf(f, -7.0f), 7.0f) + 8 : 8);
+            w |= n << (4 * i);
+        }
     }
     return w;
 }
+
+// Nibble i of w as u - 8: under the exponent of 2^23 it is a whole number, and one subtraction is exact.
+__device__ __forceinline__ float nibble(uint32_t w, int i) { return __uint_as_float((w >> (4 * i) & 15u) | 0x4b000000u) - (8388608.0f + 8.0f); }
 
 constexpr int kRowThreads = 128;
 
@@ -141,14 +171,15 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(Rows a) {
         const int r8 = w.lane / 4, t = w.lane % 4;
         const int64_t token = w.token0 + r8, slot = slot_at(a, token);
         const bool in = slot >= 0;
-        const T *src = static_cast<const T *>(a.k) + (in ? token : 0) * a.k_token + w.head * a.k_head + 8 * t;
+        // (the row does not wait for its slot)
+        const T *src = static_cast<const T *>(a.k) + (token < a.tokens ? token : 0) * a.k_token + w.head * a.k_head + 8 * t;
         uint32_t words[G];
         __nv_bfloat16 scales[G];
-        float x[G][8];
+        uint32_t x[G][4];
 #pragma unroll
-        for (int j = 0; j < G; ++j) get_row(src + 32 * j, a.vec != 0, x[j]);
+        for (int j = 0; j < G; ++j) get_row<T, 8>(src + 32 * j, a.vec != 0, x[j]);
 #pragma unroll
-        for (int j = 0; j < G; ++j) words[j] = quantise<8, 4, 1>(x[j], scales[j]);
+        for (int j = 0; j < G; ++j) words[j] = quantise<T, 8, 4, 1>(x[j], scales[j]);
         if (!in) return;
         uint8_t *tile = tile_of<D>(a, slot, w.head);
         const int r = (int)(slot % kTileTokens);
@@ -160,47 +191,56 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(Rows a) {
         return;
     }
     const int g = w.lane / 4, t = w.lane % 4;
-    // Two tokens whose slots are 2 p and 2 p + 1 share words: the one at the even slot writes both, wherever in the 8 it
-    // stands.  Of a run, that is one of every lane's two; other tokens write their halves of the words.
-#pragma unroll 1
+    // Two tokens whose slots are 2 p and 2 p + 1 share words.  Where both are this warp's, next to each other, the lane of the
+    // first writes whole words: tokens 2 t and 2 t + 1 of a lane in a run that begins at an even slot, 2 t + 1 and the next
+    // lane's first in one that begins at an odd slot.  Other tokens write their halves of the words.
+    int64_t slot[3];
+    uint32_t words[3][G];
+    __nv_bfloat16 scales[3][G];
+    uint32_t x[2][G][2];
+#pragma unroll
     for (int c = 0; c < 2; ++c) {
-        const int64_t token = w.token0 + 2 * t + c, slot = slot_at(a, token);
-        const bool even = slot >= 0 && slot % 2 == 0;
-        const bool pair = even && slot_at(a, token + 1) == slot + 1;
-        const bool follows = slot >= 0 && !even && slot_at(a, token - 1) == slot - 1;
-        const bool in = slot >= 0 && !follows;
-        if (!__any_sync(~0u, in)) continue;
-        uint32_t words[2][G];
-        __nv_bfloat16 scales[2][G];
+        const int64_t token = w.token0 + 2 * t + c;
+        slot[c] = slot_at(a, token);
+        const T *src = static_cast<const T *>(a.v) + (token < a.tokens ? token : 0) * a.v_token + w.head * a.v_head + 4 * g;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const T *src = static_cast<const T *>(a.v) + (in ? token + (pair ? p : 0) : 0) * a.v_token + w.head * a.v_head + 4 * g;
-            float x[G][4];
+        for (int j = 0; j < G; ++j) get_row<T, 4>(src + 32 * j, a.vec != 0, x[c][j]);
+    }
 #pragma unroll
-            for (int j = 0; j < G; ++j) get_row(src + 32 * j, a.vec != 0, x[j]);
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int j = 0; j < G; ++j) words[p][j] = quantise<4, 8, 4>(x[j], scales[p][j]);
-        }
-        if (!in) continue;
-        uint8_t *tile = tile_of<D>(a, slot, w.head);
-        const int r = (int)(slot % kTileTokens);
+        for (int j = 0; j < G; ++j) words[c][j] = quantise<T, 4, 8, 4>(x[c][j], scales[c][j]);
+    const int64_t after = __shfl_down_sync(~0u, slot[0], 1, 4), before = __shfl_up_sync(~0u, slot[1], 1, 4);
+    slot[2] = t < 3 ? after : -1;
+#pragma unroll
+    for (int j = 0; j < G; ++j) {
+        words[2][j] = __shfl_down_sync(~0u, words[0][j], 1, 4);
+        scales[2][j] = __ushort_as_bfloat16((unsigned short)__shfl_down_sync(~0u, (unsigned)__bfloat16_as_ushort(scales[0][j]), 1, 4));
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int64_t here = slot[c], prior = c ? slot[0] : t > 0 ? before : -1;
+        const bool even = here % 2 == 0, pair = even && slot[c + 1] == here + 1;
+        if (here < 0 || (!even && prior == here - 1)) continue;       // (the latter: the token before has written it)
+        uint8_t *tile = tile_of<D>(a, here, w.head);
+        const int r = (int)(here % kTileTokens);
         uint32_t *dst = reinterpret_cast<uint32_t *>(tile + tile_v(D)) + v_word(G, r, g, 0);
         __nv_bfloat16 *vs = reinterpret_cast<__nv_bfloat16 *>(tile + tile_vs(D)) + r * G;
         if (pair) {
             uint32_t both[G];
 #pragma unroll
-            for (int j = 0; j < G; ++j) both[j] = words[0][j] | words[1][j] << 16;
+            for (int j = 0; j < G; ++j) both[j] = words[c][j] | words[c + 1][j] << 16;
             put_words(dst, both);
         } else {
 #pragma unroll
-            for (int j = 0; j < G; ++j) reinterpret_cast<uint16_t *>(dst + j)[r & 1] = (uint16_t)words[0][j];
+            for (int j = 0; j < G; ++j) reinterpret_cast<uint16_t *>(dst + j)[r & 1] = (uint16_t)words[c][j];
         }
         // lane g has the g-th scale of both tokens
 #pragma unroll
         for (int j = 0; j < G; ++j)
             if (j == g) {
-                vs[j] = scales[0][j];
-                if (pair) vs[G + j] = scales[1][j];
+                vs[j] = scales[c][j];
+                if (pair) vs[G + j] = scales[c + 1][j];
             }
     }
 }
@@ -228,35 +268,46 @@ __global__ void __launch_bounds__(kRowThreads) load_kernel(Rows a) {
         for (int j = 0; j < G; ++j) {
             float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = slot >= 0 ? (float)((int)(words[j] >> (4 * i) & 15) - 8) * s[j] : 0.0f;
+            for (int i = 0; i < 8; ++i) x[i] = slot >= 0 ? nibble(words[j], i) * s[j] : 0.0f;
             put_row(dst + 32 * j, a.vec != 0, x);
         }
         return;
     }
-    const int g = w.lane / 4, t = w.lane % 4;
     // A lane's two tokens, if they share words, need them once: the second read of the same words is from the first level cache.
+    const int g = w.lane / 4, t = w.lane % 4;
+    uint32_t words[2][G];
+    float s[2][G];
+    bool in[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        const int64_t token = w.token0 + 2 * t + c, slot = slot_at(a, token);
-        if (token >= a.tokens) return;
-        T *dst = static_cast<T *>(a.v) + token * a.v_token + w.head * a.v_head + 4 * g;
-        uint32_t words[G] = {};
-        float s[G] = {};
-        if (slot >= 0) {
+        const int64_t slot = slot_at(a, w.token0 + 2 * t + c);
+        in[c] = slot >= 0;
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            words[c][j] = 0;
+            s[c][j] = 0;
+        }
+        if (in[c]) {
             const uint8_t *tile = tile_of<D>(a, slot, w.head);
             const int r = (int)(slot % kTileTokens);
-            get_words(reinterpret_cast<const uint32_t *>(tile + tile_v(D)) + v_word(G, r, g, 0), words);
+            get_words(reinterpret_cast<const uint32_t *>(tile + tile_v(D)) + v_word(G, r, g, 0), words[c]);
 #pragma unroll
             for (int j = 0; j < G; ++j) {
-                words[j] >>= 16 * (r & 1);
-                s[j] = bf16_bits(reinterpret_cast<const uint16_t *>(tile + tile_vs(D))[r * G + j]);
+                words[c][j] >>= 16 * (r & 1);
+                s[c][j] = bf16_bits(reinterpret_cast<const uint16_t *>(tile + tile_vs(D))[r * G + j]);
             }
         }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int64_t token = w.token0 + 2 * t + c;
+        if (token >= a.tokens) continue;
+        T *dst = static_cast<T *>(a.v) + token * a.v_token + w.head * a.v_head + 4 * g;
 #pragma unroll
         for (int j = 0; j < G; ++j) {
             float x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = slot >= 0 ? (float)((int)(words[j] >> (4 * i) & 15) - 8) * s[j] : 0.0f;
+            for (int i = 0; i < 4; ++i) x[i] = in[c] ? nibble(words[c][j], i) * s[c][j] : 0.0f;
             put_row(dst + 32 * j, a.vec != 0, x);
         }
     }
