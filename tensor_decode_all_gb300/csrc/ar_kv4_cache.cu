@@ -87,16 +87,57 @@ __device__ __forceinline__ void put_row(T *p, bool vec, const float (&x)[N]) {
     }
 }
 
-// A group's scale and N of its channels as nibbles; Lanes threads (First to First * Lanes / 2 apart) hold the group.
-template <typename T, int N, int Lanes, int First>
-__device__ __forceinline__ uint32_t quantise(const uint32_t (&pairs)[N / 2], __nv_bfloat16 &scale) {
-    // The largest magnitude by its bits, so that a NaN (above every number) wins.
-    uint32_t top = 0;
+// The scales of M groups whose channels lie in 2^Bits lanes, First apart: the maxima are reduced while they are dealt out,
+// so that a lane ends with M >> Bits of the groups (or shares one), makes their scales, and the others get
+// them by shuffles.  Group m is made in lane m * 2^Bits / M of the 2^Bits.
+template <typename T, int M, int Bits, int First>
+struct Scales {
+    static constexpr int kOwn = M >> Bits ? M >> Bits : 1;
+    __nv_bfloat16 scale[kOwn];      // of groups own .. own + kOwn - 1
+    float s[kOwn], r[kOwn];
+    int own;
+    bool first;                     // of the lanes that made the same group
+
+    // top: largest magnitudes of this lane's share by their bits, two elements to a word (a NaN is above every number)
+    __device__ __forceinline__ Scales(uint32_t (&top)[M], int lane) {
+        int n = M;
+        own = 0;
+        first = true;
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) top = __vmaxu2(top, pairs[i] & 0x7fff7fffu);
+        for (int b = Bits - 1; b >= 0; --b) {
+            const bool up = lane & (First << b);
+            if (n > 1) {
+                n /= 2;
 #pragma unroll
-    for (int d = First; d < First * Lanes; d *= 2) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, d));
-    const float2 tops = pair_of(max(top & 0xffffu, top >> 16), T());
+                for (int i = 0; i < M / 2; ++i)
+                    if (i < n) {
+                        const uint32_t give = up ? top[i] : top[i + n], keep = up ? top[i + n] : top[i];
+                        top[i] = __vmaxu2(keep, __shfl_xor_sync(~0u, give, First << b));
+                    }
+                own += up ? n : 0;
+            } else {
+                top[0] = __vmaxu2(top[0], __shfl_xor_sync(~0u, top[0], First << b));
+                first &= !up;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) {
+            scale[i] = __float2bfloat16_rn(__fdiv_rn(pair_of(max(top[i] & 0xffffu, top[i] >> 16), T()).x, 7.0f));
+            s[i] = __bfloat162float(scale[i]);
+            r[i] = __frcp_rn(s[i]);
+        }
+    }
+    // group m's scale and its reciprocal; base: the lane with the lowest number of the 2^Bits
+    __device__ __forceinline__ float2 of(int m, int base) const {
+        const int from = base + (m << Bits) / M * First;
+        return make_float2(__shfl_sync(~0u, s[m % kOwn], from), __shfl_sync(~0u, r[m % kOwn], from));
+    }
+};
+
+// N channels of a group as nibbles.
+template <typename T, int N>
+__device__ __forceinline__ uint32_t quantise(const uint32_t (&pairs)[N / 2], float2 sr) {
+    const float s = sr.x, r = sr.y;
     float x[N];
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
@@ -104,30 +145,45 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&pairs)[N / 2], __n
         x[2 * i] = v.x;
         x[2 * i + 1] = v.y;
     }
-    scale = __float2bfloat16_rn(__fdiv_rn(tops.x, 7.0f));
-    const float s = __bfloat162float(scale);
     uint32_t w = 0;
     if (s >= 0x1p-100f && s <= 0x1p100f) {
         // x / s rounded as IEEE division rounds it, from the rounded 1 / s and one exact remainder (P. Markstein,
         // "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).  |x / s| < 7.02, so the
         // sum with 1.5 * 2^23 rounds it half to even into the low bits.
-        const float r = __frcp_rn(s);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const float q = x[i] * r, n = fmaf(fmaf(-q, s, x[i]), r, q) + (12582912.0f + 8.0f);
             w |= (__float_as_uint(n) & 15u) << (4 * i);
         }
     } else {
-        // zeros, the type's ends, infinities and NaN
+        // zeros, the type's ends, infinities and NaN: a pair at a time, the pairs moving up (an index that varies would
+        // put them into local memory)
+        uint32_t p[N / 2];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float f = rintf(__fdiv_rn(x[i], s));
-            // fmax and fmin turn NaN into a bound, so NaN (and 0 / 0) is asked for first
-            const uint32_t n = (uint32_t)(f == f ? (int)fminf(fmaxf(f, -7.0f), 7.0f) + 8 : 8);
-            w |= n << (4 * i);
+        for (int i = 0; i < N / 2; ++i) p[i] = pairs[i];
+#pragma unroll 1
+        for (int i = 0; i < N / 2; ++i) {
+            const float2 v = pair_of(p[0], T());
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float f = rintf(__fdiv_rn(e ? v.y : v.x, s));
+                // fmax and fmin turn NaN into a bound, so NaN (and 0 / 0) is asked for first
+                const uint32_t n = (uint32_t)(f == f ? (int)fminf(fmaxf(f, -7.0f), 7.0f) + 8 : 8);
+                w = w >> 4 | n << (4 * N - 4);
+            }
+#pragma unroll
+            for (int k = 0; k + 1 < N / 2; ++k) p[k] = p[k + 1];
         }
     }
     return w;
+}
+
+template <int N>
+__device__ __forceinline__ uint32_t top_of(const uint32_t (&pairs)[N]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = __vmaxu2(top, pairs[i] & 0x7fff7fffu);
+    return top;
 }
 
 // Nibble i of w as u - 8: under the exponent of 2^23 it is a whole number, and one subtraction is exact.
@@ -173,21 +229,22 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(Rows a) {
         const bool in = slot >= 0;
         // (the row does not wait for its slot)
         const T *src = static_cast<const T *>(a.k) + (token < a.tokens ? token : 0) * a.k_token + w.head * a.k_head + 8 * t;
-        uint32_t words[G];
-        __nv_bfloat16 scales[G];
-        uint32_t x[G][4];
+        uint32_t words[G], x[G][4], top[G];
 #pragma unroll
         for (int j = 0; j < G; ++j) get_row<T, 8>(src + 32 * j, a.vec != 0, x[j]);
 #pragma unroll
-        for (int j = 0; j < G; ++j) words[j] = quantise<T, 8, 4, 1>(x[j], scales[j]);
+        for (int j = 0; j < G; ++j) top[j] = top_of(x[j]);
+        const Scales<T, G, 2, 1> scales(top, w.lane);
+#pragma unroll
+        for (int j = 0; j < G; ++j) words[j] = quantise<T, 8>(x[j], scales.of(j, w.lane & ~3));
         if (!in) return;
         uint8_t *tile = tile_of<D>(a, slot, w.head);
         const int r = (int)(slot % kTileTokens);
         put_words(reinterpret_cast<uint32_t *>(tile) + k_word(G, r, t, 0), words);
-        // lane t has the t-th share of the scales
+        __nv_bfloat16 *ks = reinterpret_cast<__nv_bfloat16 *>(tile + tile_ks(D)) + r * G + scales.own;
 #pragma unroll
-        for (int j = 0; j < G; ++j)
-            if (j % 4 == t) reinterpret_cast<__nv_bfloat16 *>(tile + tile_ks(D))[r * G + j] = scales[j];
+        for (int i = 0; i < scales.kOwn; ++i)
+            if (scales.first) ks[i] = scales.scale[i];
         return;
     }
     const int g = w.lane / 4, t = w.lane % 4;
@@ -195,9 +252,7 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(Rows a) {
     // first writes whole words: tokens 2 t and 2 t + 1 of a lane in a run that begins at an even slot, 2 t + 1 and the next
     // lane's first in one that begins at an odd slot.  Other tokens write their halves of the words.
     int64_t slot[3];
-    uint32_t words[3][G];
-    __nv_bfloat16 scales[3][G];
-    uint32_t x[2][G][2];
+    uint32_t words[3][G], x[2][G][2], top[2 * G];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         const int64_t token = w.token0 + 2 * t + c;
@@ -207,15 +262,20 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(Rows a) {
         for (int j = 0; j < G; ++j) get_row<T, 4>(src + 32 * j, a.vec != 0, x[c][j]);
     }
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int m = 0; m < 2 * G; ++m) top[m] = top_of(x[m / G][m % G]);
+    const Scales<T, 2 * G, 3, 4> scales(top, w.lane);
 #pragma unroll
-        for (int j = 0; j < G; ++j) words[c][j] = quantise<T, 4, 8, 4>(x[c][j], scales[c][j]);
+    for (int m = 0; m < 2 * G; ++m) words[m / G][m % G] = quantise<T, 4>(x[m / G][m % G], scales.of(m, t));
     const int64_t after = __shfl_down_sync(~0u, slot[0], 1, 4), before = __shfl_up_sync(~0u, slot[1], 1, 4);
     slot[2] = t < 3 ? after : -1;
 #pragma unroll
-    for (int j = 0; j < G; ++j) {
-        words[2][j] = __shfl_down_sync(~0u, words[0][j], 1, 4);
-        scales[2][j] = __ushort_as_bfloat16((unsigned short)__shfl_down_sync(~0u, (unsigned)__bfloat16_as_ushort(scales[0][j]), 1, 4));
+    for (int j = 0; j < G; ++j) words[2][j] = __shfl_down_sync(~0u, words[0][j], 1, 4);
+    // the scales that this lane made: of token own / G
+    const int64_t theirs = scales.own < G ? slot[0] : slot[1];
+    if (theirs >= 0 && scales.first) {
+        __nv_bfloat16 *vs = reinterpret_cast<__nv_bfloat16 *>(tile_of<D>(a, theirs, w.head) + tile_vs(D)) + theirs % kTileTokens * G + scales.own % G;
+#pragma unroll
+        for (int i = 0; i < scales.kOwn; ++i) vs[i] = scales.scale[i];
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -225,7 +285,6 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(Rows a) {
         uint8_t *tile = tile_of<D>(a, here, w.head);
         const int r = (int)(here % kTileTokens);
         uint32_t *dst = reinterpret_cast<uint32_t *>(tile + tile_v(D)) + v_word(G, r, g, 0);
-        __nv_bfloat16 *vs = reinterpret_cast<__nv_bfloat16 *>(tile + tile_vs(D)) + r * G;
         if (pair) {
             uint32_t both[G];
 #pragma unroll
@@ -235,13 +294,6 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(Rows a) {
 #pragma unroll
             for (int j = 0; j < G; ++j) reinterpret_cast<uint16_t *>(dst + j)[r & 1] = (uint16_t)words[c][j];
         }
-        // lane g has the g-th scale of both tokens
-#pragma unroll
-        for (int j = 0; j < G; ++j)
-            if (j == g) {
-                vs[j] = scales[c][j];
-                if (pair) vs[G + j] = scales[c + 1][j];
-            }
     }
 }
 
