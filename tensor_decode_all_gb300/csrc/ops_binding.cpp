@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -16,6 +17,7 @@
 #include <cmath>
 #include <exception>
 #include <initializer_list>
+#include <optional>
 #include <string>
 #include <utility>
 #include <vector>
@@ -110,7 +112,7 @@ double real(const char *what, PyObject *o) {
 constexpr int64_t kInt = 0x7fffffff;
 
 Tensor make(at::IntArrayRef shape, at::ScalarType type, const Tensor &like) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(like.device()));
+    return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);      // (without the dispatcher's way there)
 }
 
 ar_stream_t stream_of(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
