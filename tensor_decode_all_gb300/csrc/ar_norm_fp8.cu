@@ -3,8 +3,17 @@
 // One pass: a block takes a row and keeps h = x + residual in registers.  Since
 // y = h * w * inv with inv = 1 / sqrt(mean + eps) common to the row, the largest |y|
 // of a group is inv times its largest |h * w|: the sum of squares and the maxima
-// come out of one round through shared memory.  Rows that do not lie on 16 bytes
-// and groups that a warp's lanes do not divide take a kernel that goes through shared memory.
+// come out of one round through shared memory, and no value is read or computed twice.
+//
+// Bound by memory: 7 bytes an element (x, residual, h and the e4m3 output).  In
+// GB300 graph replays 8192 rows of 8192 take 70.6 us, 6.66 TB/s or 98% of what a plain
+// copy reaches; 8192 of 5120 with groups of 128 47.4 us, 6.2 TB/s; 8 rows of 8192 2.7 us.
+// A block that went from row to row with the next row's loads ahead needed
+// 85 registers and was slower (82.9 us, or spilled); many short blocks do the same overlap.
+// Rows that do not lie on 16 bytes and groups that a warp's lanes do not divide take a
+// kernel that goes through shared memory, a third as fast.
+#include <type_traits>
+
 #include <cuda_fp8.h>
 
 #include "ar_kv4.cuh"
@@ -33,40 +42,70 @@ __device__ __forceinline__ float top_of(float a, float b) {
     return __uint_as_float(max(__float_as_uint(a) & 0x7fffffffu, __float_as_uint(b) & 0x7fffffffu));
 }
 
-// Vectors of 8 channels, V to a thread: vector i * blockDim.x + threadIdx.x.  Lanes: threads that share a group (a
-// power of two up to 32; 0: the row is one group).
+template <typename T>
+__device__ __forceinline__ float2 pair_of(uint32_t w) {
+    if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<__half2 *>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t to_pair(float2 v) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __float22half2_rn(v);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// Vectors of 8 channels, V to a thread: vector i * blockDim.x + threadIdx.x.  Lanes: threads that share a group (a power of two up to 32; 0: the row is one group).
 template <typename T, int V>
-__global__ void __launch_bounds__(1024) norm_rows_kernel(const ar_add_norm_fp8_args a, int lanes) {
+__global__ void __launch_bounds__(V == 1 ? 512 : 1024) norm_rows_kernel(const ar_add_norm_fp8_args a, int lanes) {
     __shared__ float2 buf[32];
-    const int64_t row = blockIdx.x;
-    const int vecs = a.dim / 8, warps = (blockDim.x + 31) / 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + row * a.x_stride);
-    const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.residual) + row * a.residual_stride);
-    const uint4 *w = static_cast<const uint4 *>(a.weight);
-    union Vec { uint4 v; T e[8]; };
+    const int vecs = a.dim / 8, warps = blockDim.x / 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    union Vec { uint4 v; uint32_t u[4]; };
     Vec xv[V], rv[V], wv[V];
+    auto load = [&](int64_t row) {
+        const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + row * a.x_stride);
+        const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.residual) + row * a.residual_stride);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int at = i * blockDim.x + threadIdx.x;
+            xv[i].v = rv[i].v = make_uint4(0, 0, 0, 0);
+            if (at < vecs) {
+                xv[i].v = __ldcs(x + at);
+                if (a.residual) rv[i].v = __ldcs(r + at);
+            }
+        }
+    };
+    const int64_t row = blockIdx.x;
+    load(row);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int at = i * blockDim.x + threadIdx.x;
-        xv[i].v = rv[i].v = wv[i].v = make_uint4(0, 0, 0, 0);
-        if (at < vecs) {
-            xv[i].v = __ldcs(x + at);
-            if (a.residual) rv[i].v = __ldcs(r + at);
-            wv[i].v = __ldg(w + at);
-        }
+        wv[i].v = at < vecs ? __ldg(static_cast<const uint4 *>(a.weight) + at) : make_uint4(0, 0, 0, 0);
     }
+    const int groups = lanes ? (vecs + lanes - 1) / lanes : 1;
     float h[V][8], top[V], sum = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         top[i] = 0;
         Vec out;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float v = Elem<T>::to_float(xv[i].e[e]) + (a.residual ? Elem<T>::to_float(rv[i].e[e]) : 0.0f);
-            out.e[e] = Elem<T>::from_float(v);
-            sum = fmaf(v, v, sum);
-            h[i][e] = v * Elem<T>::to_float(wv[i].e[e]);
-            top[i] = top_of(top[i], h[i][e]);
+        for (int e = 0; e < 4; ++e) {
+            const float2 x2 = pair_of<T>(xv[i].u[e]), w2 = pair_of<T>(wv[i].u[e]);
+            float2 v = x2;
+            if (a.residual) {
+                const float2 r2 = pair_of<T>(rv[i].u[e]);
+                v.x += r2.x;
+                v.y += r2.y;
+            }
+            out.u[e] = to_pair<T>(v);
+            sum = fmaf(v.x, v.x, sum);
+            sum = fmaf(v.y, v.y, sum);
+            h[i][2 * e] = v.x * w2.x;
+            h[i][2 * e + 1] = v.y * w2.y;
+            top[i] = fmaxf(top[i], fmaxf(fabsf(h[i][2 * e]), fabsf(h[i][2 * e + 1])));
         }
         const int at = i * blockDim.x + threadIdx.x;
         if (a.residual_out && at < vecs)
@@ -75,16 +114,16 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(const ar_add_norm_fp8_a
     float most = 0;
     if (lanes == 0) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) most = top_of(most, top[i]);
+        for (int i = 0; i < V; ++i) most = fmaxf(most, top[i]);
     }
 #pragma unroll
     for (int d = 16; d; d /= 2) {
         sum += __shfl_xor_sync(~0u, sum, d);
         if (lanes == 0) {
-            most = top_of(most, __shfl_xor_sync(~0u, most, d));
+            most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
         } else if (d < lanes) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) top[i] = top_of(top[i], __shfl_xor_sync(~0u, top[i], d));
+            for (int i = 0; i < V; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], d));
         }
     }
     if (lane == 0) buf[warp] = make_float2(sum, most);
@@ -96,22 +135,29 @@ __global__ void __launch_bounds__(1024) norm_rows_kernel(const ar_add_norm_fp8_a
 #pragma unroll
     for (int d = 16; d; d /= 2) {
         sum += __shfl_xor_sync(~0u, sum, d);
-        most = top_of(most, __shfl_xor_sync(~0u, most, d));
+        most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
     }
     const float inv = rsqrtf(__fdiv_rn(sum, (float)a.dim) + a.eps);
     uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + row * a.dim);
-    const int groups = lanes ? (vecs + lanes - 1) / lanes : 1;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int at = i * blockDim.x + threadIdx.x;
-        const float y = (lanes ? top[i] : most) * inv, scale = y == 0 ? 1.0f : __fdiv_rn(y, 448.0f), q = __fdiv_rn(inv, scale);
-        if (at >= vecs) break;
-        uint32_t b[4];
+        const float m = lanes ? top[i] : most;
+        float scale = m * inv * (1.0f / 448.0f), q = __fdividef(448.0f, m);       // h * q: within 2 units of the last place of y / scale
+        if (!(m > 0x1p-60f && m < 0x1p100f)) {
+            // zeros, the ends of the range, infinities
+            scale = m * inv == 0 ? 1.0f : __fdiv_rn(m * inv, 448.0f);
+            q = __fdiv_rn(inv, scale);
+        }
+        if (!(inv == inv)) scale = q = inv;
+        if (at < vecs) {
+            uint32_t b[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            b[e] = __nv_cvt_float2_to_fp8x2(make_float2(h[i][2 * e] * q, h[i][2 * e + 1] * q), __NV_SATFINITE, __NV_E4M3);
-        __stcs(out + at, make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16));
-        if (lanes ? at % lanes == 0 : at == 0) a.scales[row * groups + (lanes ? at / lanes : 0)] = scale;
+            for (int e = 0; e < 4; ++e)
+                b[e] = __nv_cvt_float2_to_fp8x2(make_float2(h[i][2 * e] * q, h[i][2 * e + 1] * q), __NV_SATFINITE, __NV_E4M3);
+            __stcs(out + at, make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16));
+            if (lanes ? at % lanes == 0 : at == 0) a.scales[row * groups + (lanes ? at / lanes : 0)] = scale;
+        }
     }
 }
 
@@ -180,10 +226,11 @@ cudaError_t start(const ar_add_norm_fp8_args &a, cudaStream_t s) {
         else if (a.group == 8 || a.group == 16 || a.group == 32 || a.group == 64 || a.group == 128 || a.group == 256) lanes = a.group / 8;
     }
     if (lanes >= 0) {
-        // Few rows: a vector a thread, for the shortest way through a row.  Many: two, for more loads in flight from
-        // fewer warps (measured below at the launch sizes of a step and of a chunk).
         const int vecs = a.dim / 8;
-        const int v = vecs > 2048 ? 4 : vecs > 1024 || (a.rows > kFewRows && vecs >= 128) ? 2 : 1;
+        // Vectors to a thread: more of them keep as many loads in flight with fewer warps to meet (8192 x 8192, one scale a
+        // row: four 70.6 us, two 77.5; 16384 x 4096, groups of 128: four 72.6, two 76.6, one 90.5), fewer make a short row's
+        // way shorter where there are no others to wait for (64 x 4096: two 2.8 us, four 3.2).
+        const int v = vecs <= 128 ? 1 : vecs < 512 || (vecs <= 1024 && a.rows <= kFewRows) ? 2 : 4;
         const int threads = ((vecs + v - 1) / v + 31) / 32 * 32;
         if (v == 1) norm_rows_kernel<T, 1><<<(unsigned)a.rows, threads, 0, s>>>(a, lanes);
         else if (v == 2) norm_rows_kernel<T, 2><<<(unsigned)a.rows, threads, 0, s>>>(a, lanes);
