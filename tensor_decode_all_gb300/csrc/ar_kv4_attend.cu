@@ -34,7 +34,7 @@ constexpr int kMaxRequests = 8192;
 constexpr int kWarps = 4;                 // warps of a block; each works alone
 constexpr float kNoScore = -3.0e38f;      // below every score; finite, so that differences are numbers
 constexpr int kHead = 8;                  // weights stand near 2^kHead ...
-constexpr int kStart = 2;                 // chunks that beginning a segment is worth
+constexpr int kStart = 3;                 // chunks that beginning a segment is worth
 constexpr int kLead = 6;                  // ... and may pass it by 2^kLead before the reference moves
 
 // Workspace: status, a record for each warp, and two partial results to a warp.
@@ -513,8 +513,8 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
         // V scales: the largest among tokens that some row sees, infinities and NaN left out
         float vtop = 0;
 #pragma unroll
-        for (int i = 0; i < CI * D / 128; ++i) {
-            const int wd = i * 32 + lane, ct = wd / (D / 4), in = wd % (D / 4);
+        for (int i = 0; i < (CI * D + 127) / 128; ++i) {
+            const int wd = (i * 32 + lane) % (CI * D / 4), ct = wd / (D / 4), in = wd % (D / 4);   // (16 words: each twice)
             uint32_t w = *reinterpret_cast<const uint32_t *>(data + ct * tile_bytes(D) + tile_vs(D) + in * 4);
             if constexpr (!Full) {
                 const int tok = tok0 + ct * kTileTokens + in / (G / 2);
@@ -552,8 +552,9 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
                 // an infinite scale spoils its own group; the others keep theirs
                 vtop = 0;
 #pragma unroll 1
-                for (int i = 0; i < CI * D / 64; ++i) {
-                    const int half = (i / 2 * 32 + lane) * 2 + i % 2, ct = half / (D / 2), in = half % (D / 2), tok = tok0 + ct * kTileTokens + in / G;
+                for (int i = 0; i < 2 * ((CI * D + 127) / 128); ++i) {
+                    const int half = (i / 2 * 32 + lane) % (CI * D / 4) * 2 + i % 2, ct = half / (D / 2), in = half % (D / 2),
+                              tok = tok0 + ct * kTileTokens + in / G;
                     const float v = fabsf(bf16_bits(*reinterpret_cast<const uint16_t *>(data + ct * tile_bytes(D) + tile_vs(D) + in * 2)));
                     const bool see = Full || (tok <= seg().pos_hi && (!a.window || tok > seg().pos_lo - a.window || tok < a.sinks));
                         if (see && v < INFINITY) vtop = fmaxf(vtop, v);
@@ -877,8 +878,8 @@ template <typename T>
 int start(const Attend &c, cudaStream_t s) {
     const long long rows = (long long)max(c.a.max_new, 1) * c.group;
     switch (c.a.head_dim) {
-        case 64: return rows <= 8 ? start<T, Shape<64, 1, 4, 2, 3, 3>>(c, s) : start<T, Shape<64, 2, 4, 2, 3, 3>>(c, s);
-        case 128: return rows <= 8 ? start<T, Shape<128, 1, 4, 2, 2, 3>>(c, s) : start<T, Shape<128, 2, 2, 1, 4, 2>>(c, s);
+        case 64: return rows <= 8 ? start<T, Shape<64, 1, 4, 2, 3, 3>>(c, s) : start<T, Shape<64, 2, 4, 1, 3, 3>>(c, s);
+        case 128: return rows <= 8 ? start<T, Shape<128, 1, 4, 2, 2, 3>>(c, s) : start<T, Shape<128, 2, 4, 1, 2, 2>>(c, s);
         default: return start<T, Shape<256, 1, 1, 1, 5, 2>>(c, s);
     }
 }

@@ -632,3 +632,54 @@ def test_binding_refusals_on_the_gpu():
         tda.kv_plan(n, n, t, n, n[:1], page=17, max_tokens=3)
     with pytest.raises(tda.ArError):
         tda.kv4_attend(q, pool, t, n, window=-1)
+
+
+# ------------------------------------------------------- sizes and places
+
+@pytest.mark.parametrize("page", [48, 112])
+def test_pages_that_are_no_power_of_two(page):
+    tda = _tda()
+    lens, Hk, D = [page * 3 + 5, 7, page], 2, 128
+    q, pool, K, V, table, cu = _attend_case(37, 3, lens, [1] * 3, Hk, 8, D, page, "bf16")
+    out, lse = tda.kv4_attend(q.cuda(), pool.cuda(), _i32(table), _i32(lens), return_lse=True)
+    _check_attend(q, K, V, table, lens, cu, 0, 0, D ** -0.5, out, lse)
+    k = torch.randn(page + 3, Hk, D, generator=_gen(2)).to(torch.bfloat16)
+    slots = torch.arange(page + 3) + 11
+    dev = pool.cuda()
+    tda.kv4_append(k.cuda(), k.flip(0).cuda(), dev, slots.cuda())
+    _same_pool(dev.cpu(), _write(pool, slots.tolist(), k, k.flip(0), page))
+
+
+@pytest.mark.parametrize("new", [[1], [0, 1, 3, 0, 0, 2]])
+def test_attend_many_requests(new):
+    """More requests than a block has threads, most of them short, some without new tokens."""
+    tda = _tda()
+    B = 1500
+    g = np.random.RandomState(1)
+    lens = [int(x) for x in g.randint(1, 40, B)]
+    lens[700] = 3000
+    new = [min(new[i % len(new)], lens[i]) for i in range(B)]
+    q, pool, K, V, table, cu = _attend_case(41, B, lens, new, 1, 4, 64, 16, "f16")
+    out, lse = tda.kv4_attend(q.cuda(), pool.cuda(), _i32(table), _i32(lens), _i32(cu), max_new=max(new), return_lse=True)
+    _check_attend(q, K, V, table, lens, cu, 0, 0, 64 ** -0.5, out, lse)
+
+
+def test_offsets_past_32_bits():
+    """A cache of over 4 GiB: pages at its end are written, read back and attended over like those at its start."""
+    tda = _tda()
+    D, page, n = 128, 16, 75
+    pages = (4 << 30) // 2304 + 50
+    pool = torch.empty(pages, 1, 1, 2304, dtype=torch.uint8, device="cuda")
+    g = _gen(43)
+    k, v = ((torch.randn(n, 1, D, generator=g)).to(torch.bfloat16).cuda() for _ in range(2))
+    q = torch.randn(1, 8, D, generator=g).to(torch.bfloat16).cuda()
+    slots = torch.arange(n, device="cuda")
+    got = []
+    for first in (0, pages - 5):
+        at = slots + first * page
+        tda.kv4_append(k, v, pool, at)
+        table = torch.arange(first, first + 5, dtype=torch.int32, device="cuda")[None]
+        got.append((*tda.kv4_load(pool, at), tda.kv4_attend(q, pool, table, _i32([n]))))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert (got[0][0].float() - k.float()).abs().max() < 0.5 and got[0][2].abs().sum() > 0
