@@ -72,6 +72,33 @@ inline bool rows_aligned(const void *p, int64_t a, int64_t b) {
 
 inline bool misaligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
+// Every kernel of these operators is launched as a programmatic dependent of the work before it on its stream: its blocks
+// may come to the GPU while that work ends, which hides the launch, and wait here, before they touch any memory, until it has
+// ended and its writes are visible.  The next such kernel may come as soon as all blocks of this one have.
+__device__ __forceinline__ void after_the_stream() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... P, typename... A>
+inline cudaError_t launch_next(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, unsigned cluster, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The launch's own error, not one left by an earlier call of the program.
 inline int launch_status(cudaError_t e) {
     if (e == cudaSuccess) return AR_OK;

@@ -267,6 +267,7 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
 
     // Running sum over the requests' chunks: every warp finds its share by itself.
     long long u0, u1, per;
+    after_the_stream();
     {
         const int each = (a.requests + kWarps * 32 - 1) / (kWarps * 32);
         const int b0 = min((int)threadIdx.x * each, a.requests), b1 = min(b0 + each, a.requests);
@@ -319,7 +320,6 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
         u1 = min(u0 + per, total);
         __syncthreads();
     }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int self = blockIdx.x * kWarps + warp;
     Record *record = reinterpret_cast<Record *>(static_cast<uint8_t *>(a.workspace) + kRecordAt) + self;
     if (lane == 0) record->parts = 0;
@@ -780,6 +780,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     constexpr int D = C::D, Quads = D / 4, Groups = Spread ? kJoinThreads / Quads : 1;
     __shared__ float4 rows[Groups][Quads];
     __shared__ float2 facts[Groups];
+    // (no early word to the kernel after: an attention's blocks would take the multiprocessors from this one's)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint8_t *ws = static_cast<const uint8_t *>(c.a.workspace);
     const Record r = reinterpret_cast<const Record *>(ws + kRecordAt)[blockIdx.x];
@@ -855,21 +856,11 @@ int start(const Attend &c, cudaStream_t s) {
     const long long blocks = ((long long)c.a.tokens * c.group + C::Rows - 1) / C::Rows + c.a.requests;
     const long long share = (long long)c.min_chunks * kWarps, most = (blocks * (chunks + kStart) * c.a.kv_heads + share - 1) / share;
     grid = (int)min((long long)grid, most);
-    void *args[] = {const_cast<Attend *>(&c)};
-    cudaError_t e = cudaLaunchKernel(kernel, dim3((unsigned)grid), dim3(kWarps * 32), args, C::Smem, s);
-    // The joining kernel comes to the GPU beside the end of the first, and waits for it.
+    cudaError_t e = launch_next(attend_kernel<T, C>, dim3((unsigned)grid), kWarps * 32, C::Smem, s, 0, c);
     if (e == cudaSuccess && chunks > 1) {     // one chunk is never split
         const bool spread = (long long)c.a.requests * c.a.kv_heads <= kSpreadSegments;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(grid * kWarps), spread ? C::Rows : 1);
-        cfg.blockDim = dim3(spread ? 256 : 128);
-        cfg.stream = s;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        e = spread ? cudaLaunchKernelEx(&cfg, join_kernel<T, C, true>, c) : cudaLaunchKernelEx(&cfg, join_kernel<T, C, false>, c);
+        const dim3 blocks((unsigned)(grid * kWarps), spread ? C::Rows : 1);
+        e = spread ? launch_next(join_kernel<T, C, true>, blocks, 256, 0, s, 0, c) : launch_next(join_kernel<T, C, false>, blocks, 128, 0, s, 0, c);
     }
     return launch_status(e);
 }

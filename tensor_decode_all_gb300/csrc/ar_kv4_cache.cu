@@ -221,6 +221,7 @@ __device__ __forceinline__ int64_t slot_at(const Rows &a, int64_t token) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads) append_kernel(Rows a) {
     constexpr int G = D / kGroup;
+    after_the_stream();
     const Job w = job_of(a);
     if (!w.any) return;
     if (!w.v) {
@@ -300,6 +301,7 @@ __global__ void __launch_bounds__(kRowThreads) append_kernel(Rows a) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads) load_kernel(Rows a) {
     constexpr int G = D / kGroup;
+    after_the_stream();
     const Job w = job_of(a);
     if (!w.any) return;
     if (!w.v) {
@@ -382,9 +384,7 @@ template <typename T, int D>
 cudaError_t start(const Rows &a, bool append, cudaStream_t s) {
     const int64_t per = kRowThreads / 32, blocks = ((a.tokens + 7) / 8 * a.heads * 2 + per - 1) / per;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    if (append) append_kernel<T, D><<<(unsigned)blocks, kRowThreads, 0, s>>>(a);
-    else load_kernel<T, D><<<(unsigned)blocks, kRowThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_next(append ? append_kernel<T, D> : load_kernel<T, D>, dim3((unsigned)blocks), kRowThreads, 0, s, 0, a);
 }
 
 template <typename T>

@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ar_kv_plan_arg
     int *len = sh, *token0 = sh + a.requests, *page0 = token0 + a.requests;
     __shared__ Sums warp_sums[kPlanThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    after_the_stream();
     const int used = a.free_used[0];
     Sums carry = {0, 0};
     int bad = used < 0 ? 1 : 0;   // bit 0: AR_EINVAL, bit 1: AR_ETOOBIG
@@ -154,17 +155,5 @@ extern "C" AR_API int ar_kv_plan(const ar_kv_plan_args *args, ar_stream_t stream
             return launch_status(cudaErrorUnknown);
         *(volatile bool *)&ready[dev] = true;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3(kPlanThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)blocks;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return launch_status(cudaLaunchKernelEx(&cfg, plan_kernel, a));
+    return launch_status(launch_next(plan_kernel, dim3((unsigned)blocks), kPlanThreads, smem, stream, (unsigned)blocks, a));
 }

@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) norm_rows_kernel(const ar
             }
         }
     };
+    after_the_stream();
     const int64_t row = blockIdx.x;
     load(row);
 #pragma unroll
@@ -163,6 +164,7 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) norm_rows_kernel(const ar
 
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) norm_kernel(const ar_add_norm_fp8_args a) {
+    after_the_stream();
     extern __shared__ float h[];
     __shared__ float buf[kNormThreads / 32];
     const int64_t row = blockIdx.x;
@@ -232,10 +234,8 @@ cudaError_t start(const ar_add_norm_fp8_args &a, cudaStream_t s) {
         // way shorter where there are no others to wait for (64 x 4096: two 2.8 us, four 3.2).
         const int v = vecs <= 128 ? 1 : vecs < 512 || (vecs <= 1024 && a.rows <= kFewRows) ? 2 : 4;
         const int threads = ((vecs + v - 1) / v + 31) / 32 * 32;
-        if (v == 1) norm_rows_kernel<T, 1><<<(unsigned)a.rows, threads, 0, s>>>(a, lanes);
-        else if (v == 2) norm_rows_kernel<T, 2><<<(unsigned)a.rows, threads, 0, s>>>(a, lanes);
-        else norm_rows_kernel<T, 4><<<(unsigned)a.rows, threads, 0, s>>>(a, lanes);
-        return cudaGetLastError();
+        return launch_next(v == 1 ? norm_rows_kernel<T, 1> : v == 2 ? norm_rows_kernel<T, 2> : norm_rows_kernel<T, 4>, dim3((unsigned)a.rows),
+                           threads, 0, s, 0, a, lanes);
     }
     static bool ready[64] = {};
     int dev = 0;
@@ -245,8 +245,7 @@ cudaError_t start(const ar_add_norm_fp8_args &a, cudaStream_t s) {
         if (e == cudaSuccess && dev < 64) *(volatile bool *)&ready[dev] = true;
     }
     if (e != cudaSuccess) return e;
-    norm_kernel<T><<<(unsigned)a.rows, kNormThreads, (size_t)a.dim * 4, s>>>(a);
-    return cudaGetLastError();
+    return launch_next(norm_kernel<T>, dim3((unsigned)a.rows), kNormThreads, (size_t)a.dim * 4, s, 0, a);
 }
 
 }  // namespace
