@@ -3,6 +3,8 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -38,31 +40,21 @@ template <> struct Elem<__nv_bfloat16> {
 
 __device__ __forceinline__ float bf16_bits(uint32_t bits) { return __uint_as_float(bits << 16); }
 
-// Eight 16-bit elements: one 16-byte access where the address allows it.
+// Both elements of a pair, and a pair of two rounded elements.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, bool vec, float (&x)[8]) {
-    union { uint4 v; T e[8]; } u;
-    if (vec) {
-        u.v = *reinterpret_cast<const uint4 *>(p);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u.e[i] = p[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = Elem<T>::to_float(u.e[i]);
+__device__ __forceinline__ float2 pair_of(uint32_t w) {
+    if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<__half2 *>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(T *p, bool vec, const float (&x)[8]) {
-    union { uint4 v; T e[8]; } u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u.e[i] = Elem<T>::from_float(x[i]);
-    if (vec) {
-        *reinterpret_cast<uint4 *>(p) = u.v;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = u.e[i];
+__device__ __forceinline__ uint32_t to_pair(float2 v) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __float22half2_rn(v);
+        return *reinterpret_cast<const uint32_t *>(&h);
     }
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // Whether rows at p with these strides (elements of 2 bytes) all start on 16 bytes.
@@ -72,9 +64,10 @@ inline bool rows_aligned(const void *p, int64_t a, int64_t b) {
 
 inline bool misaligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
 
-// Every kernel of these operators is launched as a programmatic dependent of the work before it on its stream: its blocks
-// may come to the GPU while that work ends, which hides the launch, and wait here, before they touch any memory, until it has
-// ended and its writes are visible.  The next such kernel may come as soon as all blocks of this one have.
+// Every kernel of these operators is launched as a programmatic dependent of the work before it on its stream:
+// its blocks may come to the GPU while that work ends, which hides the launch, and wait here, before they
+// touch any memory, until it has ended and its writes are visible.  The next such kernel may come as soon as
+// all blocks of this one have.
 __device__ __forceinline__ void after_the_stream() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

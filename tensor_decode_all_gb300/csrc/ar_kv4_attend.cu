@@ -1,29 +1,36 @@
 // ar_kv4_attend.cu -- ar_kv4_attend: attention over the 4-bit paged cache.
 //
-// A warp takes 8 or 16 query rows (new tokens x heads) of one request and kv
-// head over a run of the request's tokens, with its own ring of stages in shared
-// memory and no other warp to wait for.  The runs cut the chunks of all
-// requests, heads and row blocks, laid end to end, into equal shares, one to a
-// warp of a resident grid; where a cut separates a row's tokens the partial results go to
-// the workspace, and a second, small kernel joins them in order.
+// A warp takes 8 or 16 query rows (new tokens x heads) of one request and kv head over a run of the request's
+// tokens, with its own ring of stages in shared memory and no other warp to wait for.  The runs cut the chunks
+// of all requests, heads and row blocks, laid end to end, into equal shares, one to a warp of a resident grid;
+// where a cut separates a row's tokens the partial results go to the workspace, and a second, small kernel
+// joins them in order.
 //
-// The products are S^T = K Q^T and O^T = V^T P^T (mma.m16n8k16, fp16 operands,
-// binary32 sums), with the tokens (channels) as the 16 rows and the query rows
-// as the 8 columns, so that a group of 8 heads fills the instruction.  K and V
-// enter as the whole numbers they are: a nibble under fp16's exponent of 1024
-// is 1024 + u, and one subtraction gives u - 8 exactly.  K's scales multiply
-// the sums of each group of 32 channels, V's the weights, both in binary32.
+// The products are S^T = K Q^T and O^T = V^T P^T (mma.m16n8k16, fp16 operands, binary32 sums), with the tokens
+// (channels) as the 16 rows and the query rows as the 8 columns, so that a group of 8 heads fills the
+// instruction.  (tcgen05 has 64 rows at least, and wants its operands in shared memory: each nibble would be
+// written there at four times its size and read once.)  K and V enter as the whole numbers they are.  A nibble
+// u in the mantissa of a power of two is that power plus u: K's operands stay so, and what that adds to a
+// group's sum, a constant of the query row, is where the accumulator starts; V's get it subtracted, since its
+// sums run over all tokens.  K's scales multiply the sums of each group of 32 channels, V's the weights, both
+// in binary32; weight x scale is rounded once, to fp16.
 //
-// Softmax runs in base 2 under a reference M per row, common to a warp, that moves
-// only when a score passes it by 2^6: p = 2^(s - M).  M also holds the exponent of the largest V
-// scale seen, so that a weight p * scale stays within fp16 with 2^-14 of
-// it still a normal number, whatever the scales.
+// Softmax runs in base 2 under a reference M per row, common to a warp, that moves only when a score passes it
+// by 2^6: p = 2^(s - M), and the usual step costs a vote in place of a reduction.  M also holds the exponent
+// of the largest V scale seen, so that a weight p * scale stays within fp16 with 2^-14 of it still a normal
+// number, whatever the scales.
 //
-// Each warp reads its tokens on its own: a ring of stages in shared memory,
-// filled by bulk copies (a tile is 18 D contiguous bytes) a stage ahead, the
-// next segment's first stages before the last one's results are written.
-#include <type_traits>
-
+// Each warp reads its tokens on its own: a ring of stages in shared memory, filled by bulk copies (a tile is
+// 18 D contiguous bytes) a stage ahead, the next segment's first stages before the last one's results are
+// written.
+//
+// Measured on a GB300 (graph replays): 64 requests of 16385 to 32768 tokens, 8 kv heads of 8, D 128: 307 us,
+// 5.9 TB/s of cache or 87% of what a plain copy reaches; 64 ragged ones of 517 to 8001: 69 us, 67%; 128 ragged
+// with a window of 1024 and D 64: 33 us; one of 1003 tokens and one kv head: 9.6 us.  The short ones are bound
+// by the instructions they issue: 308 for a tile of 16 tokens and one head of 128, 0.56 a cycle and scheduler,
+// two of five on the ALU pipe, which takes one every other cycle; DRAM carries 1.006 times the bytes that have
+// to be read, and the matrix instructions take a quarter of the time.  12 warps a multiprocessor: 16 with 126
+// registers each were 12% slower.
 #include "ar_kv4.cuh"
 
 namespace {
@@ -34,8 +41,11 @@ constexpr int kMaxRequests = 8192;
 constexpr int kWarps = 4;                 // warps of a block; each works alone
 constexpr float kNoScore = -3.0e38f;      // below every score; finite, so that differences are numbers
 constexpr int kHead = 8;                  // weights stand near 2^kHead ...
-constexpr int kStart = 3;                 // chunks that beginning a segment is worth
 constexpr int kLead = 6;                  // ... and may pass it by 2^kLead before the reference moves
+// Chunks that beginning a segment is worth in the shares: its latency and its results.  64 ragged requests,
+// and a window of 17 chunks a segment: 1: 71.9 and 38.6 us, 2: 70.2 and 34.1, 3: 69.4 and 33.0, 4: 71.4 and
+// 33.5, 6: 71.5 and 34.6.
+constexpr int kStart = 3;
 
 // Workspace: status, a record for each warp, and two partial results to a warp.
 struct Record {
@@ -52,7 +62,6 @@ struct Attend {
     ar_kv4_attend_args a;
     int group;        // query heads of a kv head
     int vec_q, vec_o;
-    int min_chunks;   // least share of a warp
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -143,14 +152,14 @@ struct Shape {
     static constexpr int D = D_;              // head dim
     static constexpr int NT = NT_;            // 8-row tiles of query rows
     static constexpr int CT = CT_;            // tiles of a chunk, the unit of work and a stage of the ring
-    static constexpr int CI = CI_;            // tiles multiplied together: enough to hide latencies, few enough for the instruction cache
+    static constexpr int CI = CI_;            // tiles multiplied together, see the shapes below
     static constexpr int S = S_;              // stages
     static constexpr int Blocks = Blocks_;    // of an SM, for which registers are kept
     static constexpr int G = D / kGroup;
     static constexpr int Tokens = CT * kTileTokens;
     static constexpr int Rows = 8 * NT;
-    // One row tile: the constants that nibbles stand on come out of K's sums; with more of them subtracting before
-    // the products costs less, each nibble serving all (and needs no registers for what to take out).
+    // One row tile: the constants that nibbles stand on come out of K's sums; with more of them subtracting
+    // before the products costs less, each nibble serving all (and needs no registers for what to take out).
     static constexpr bool Over = NT == 1;
     static constexpr int Stage = CT * tile_bytes(D);
     static constexpr int Smem = kWarps * S * Stage;
@@ -294,7 +303,7 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
             total += sums[w];
         }
         const long long warps = (long long)gridDim.x * kWarps;
-        per = max((total + warps - 1) / warps, (long long)c.min_chunks);
+        per = max((total + warps - 1) / warps, 1ll);
         // (the block's first share tells whether there is any)
         const long long first = per * kWarps * blockIdx.x;
         if (first < total) {
@@ -333,8 +342,8 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
     bool late = false;
     uint32_t filled = 0, used = 0;       // stages filled and used, over all segments
     int walked = 0;                      // segments walked to
-    // Of the segment walked to last: its chunks and how many of them are sent.  Lane l has the address of tile l % CT of
-    // its chunk l / CT of a batch, and reads the page ids of the batch after.
+    // Of the segment walked to last: its chunks and how many of them are sent.  Lane l has the address of tile
+    // l % CT of its chunk l / CT of a batch, and reads the page ids of the batch after.
     int p_chunks = 0, sent = 0, batch_tile = 0, batch_id = 0;
     const uint8_t *src = nullptr;
     unsigned have = 0;                   // lanes whose tile exists
@@ -638,7 +647,8 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
 
 
     for (;;) {
-        // Fill the free stages, going on into the next segment; at the start one, so that every warp's first data come early.
+        // Fill the free stages, going on into the next segment; at the start one, so that every warp's first
+        // data come early.
 #pragma unroll 1
         while (filled - used < (at < 0 ? 1 : S)) {
             if (sent < p_chunks) send();
@@ -830,6 +840,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     }
 }
 
+// Up to this many segments a row's parts are many (one request of 262139 tokens: 228 to a row), and a block
+// takes one row and shares them out; beyond, a block takes all rows of a record (that request with one kv
+// head, parts in one line: 116 us, shared out: 38).
 constexpr int kSpreadSegments = 64;
 
 template <typename T, class C>
@@ -854,7 +867,7 @@ int start(const Attend &c, cudaStream_t s) {
     // No more blocks than the longest contexts the table can hold would fill.
     const long long chunks = max(((long long)c.a.table_width * c.a.page + C::Tokens - 1) / C::Tokens, 1ll);
     const long long blocks = ((long long)c.a.tokens * c.group + C::Rows - 1) / C::Rows + c.a.requests;
-    const long long share = (long long)c.min_chunks * kWarps, most = (blocks * (chunks + kStart) * c.a.kv_heads + share - 1) / share;
+    const long long most = (blocks * (chunks + kStart) * c.a.kv_heads + kWarps - 1) / kWarps;
     grid = (int)min((long long)grid, most);
     cudaError_t e = launch_next(attend_kernel<T, C>, dim3((unsigned)grid), kWarps * 32, C::Smem, s, 0, c);
     if (e == cudaSuccess && chunks > 1) {     // one chunk is never split
@@ -868,6 +881,10 @@ int start(const Attend &c, cudaStream_t s) {
 template <typename T>
 int start(const Attend &c, cudaStream_t s) {
     const long long rows = (long long)max(c.a.max_new, 1) * c.group;
+    // Chunks of 64 tokens in two or three stages, 3 blocks an SM with one row tile (with chunks of 32 tokens
+    // 75 us where this takes 70, 64 ragged requests).  Steps of two tiles: of one 71 us, of four 76, which do
+    // not fit the instruction cache.  Two row tiles have room for 2 blocks and steps of one tile (drafts of up
+    // to 6 tokens: 51 us, of two 54); three and four row tiles, with q in shared memory, took 69 and 99.
     switch (c.a.head_dim) {
         case 64: return rows <= 8 ? start<T, Shape<64, 1, 4, 2, 3, 3>>(c, s) : start<T, Shape<64, 2, 4, 1, 3, 3>>(c, s);
         case 128: return rows <= 8 ? start<T, Shape<128, 1, 4, 2, 2, 3>>(c, s) : start<T, Shape<128, 2, 4, 1, 2, 2>>(c, s);
@@ -913,14 +930,14 @@ AR_API int ar_kv4_attend(const ar_kv4_attend_args *args, ar_stream_t stream) {
         misaligned(a.lens, 4) || misaligned(a.cu, 4) || misaligned(a.workspace, 256))
         return AR_EINVAL;
     c.group = a.q_heads / a.kv_heads;
-    // A window or sinks that cover the table limit nothing; smaller ones and the rows stay where sums fit 32 bits.
+    // A window or sinks that cover the table limit nothing; smaller ones and the rows stay where sums fit 32
+    // bits.
     const long long room = (long long)a.table_width * a.page;
     if (a.window >= room || a.sinks >= room) c.a.window = 0;
     if ((long long)a.tokens * c.group > 1 << 30 || c.a.window > 1 << 30 || (long long)a.tokens * a.q_heads > 0x7fffffff)
         return AR_ETOOBIG;
     c.vec_q = rows_aligned(a.q, a.q_token_stride, a.q_head_stride);
     c.vec_o = rows_aligned(a.out, a.out_token_stride, a.out_head_stride);
-    c.min_chunks = 1;
     return a.dtype == AR_F16 ? start<__half>(c, stream) : start<__nv_bfloat16>(c, stream);
 }
 

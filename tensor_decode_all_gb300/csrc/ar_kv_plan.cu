@@ -1,11 +1,13 @@
 // ar_kv_plan.cu -- ar_kv_plan: block tables and slot maps from the requests' lengths.
 //
-// Two running sums over the requests (new tokens, new pages) give every new
-// token and page its place; each token then finds its request by bisection.
-// Every block makes the whole sums for itself in shared memory (at most 8192
-// requests, a few passes of one block) and writes its share of the tokens; the
-// blocks are one cluster, whose barrier stands between the reads of lens and
-// *free_used and their writes, so that both may be updated in place.
+// Two running sums over the requests (new tokens, new pages) give every new token and page its place; each
+// token then finds its request by bisection. Every block makes the whole sums for itself in shared memory (at
+// most 8192 requests, a few passes of one block) and writes its share of the tokens; the blocks are one
+// cluster, whose barrier stands between the reads of lens and *free_used and their writes, so that both may be
+// updated in place.
+//
+// Bound by latency: 64 requests of a token each take 4.9 us on a GB300, 1000 requests with 23524 new tokens
+// 9.2 (graph replays; the second writes 0.4 MB).
 #include "ar_kv4.cuh"
 
 namespace {

@@ -7,13 +7,11 @@
 //
 // Bound by memory: 7 bytes an element (x, residual, h and the e4m3 output).  In
 // GB300 graph replays 8192 rows of 8192 take 70.6 us, 6.66 TB/s or 98% of what a plain
-// copy reaches; 8192 of 5120 with groups of 128 47.4 us, 6.2 TB/s; 8 rows of 8192 2.7 us.
+// copy reaches; 8192 of 5120 with groups of 128 45.9 us, 6.4 TB/s; 8 rows of 8192 2.0 us.
 // A block that went from row to row with the next row's loads ahead needed
 // 85 registers and was slower (82.9 us, or spilled); many short blocks do the same overlap.
 // Rows that do not lie on 16 bytes and groups that a warp's lanes do not divide take a
 // kernel that goes through shared memory, a third as fast.
-#include <type_traits>
-
 #include <cuda_fp8.h>
 
 #include "ar_kv4.cuh"
@@ -42,23 +40,8 @@ __device__ __forceinline__ float top_of(float a, float b) {
     return __uint_as_float(max(__float_as_uint(a) & 0x7fffffffu, __float_as_uint(b) & 0x7fffffffu));
 }
 
-template <typename T>
-__device__ __forceinline__ float2 pair_of(uint32_t w) {
-    if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<__half2 *>(&w));
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t to_pair(float2 v) {
-    if constexpr (std::is_same<T, __half>::value) {
-        const __half2 h = __float22half2_rn(v);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-    const __nv_bfloat162 h = __float22bfloat162_rn(v);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// Vectors of 8 channels, V to a thread: vector i * blockDim.x + threadIdx.x.  Lanes: threads that share a group (a power of two up to 32; 0: the row is one group).
+// Vectors of 8 channels, V to a thread: vector i * blockDim.x + threadIdx.x.  Lanes: threads that share a
+// group (a power of two up to 32; 0: the row is one group).
 template <typename T, int V>
 __global__ void __launch_bounds__(V == 1 ? 512 : 1024) norm_rows_kernel(const ar_add_norm_fp8_args a, int lanes) {
     __shared__ float2 buf[32];
@@ -229,9 +212,10 @@ cudaError_t start(const ar_add_norm_fp8_args &a, cudaStream_t s) {
     }
     if (lanes >= 0) {
         const int vecs = a.dim / 8;
-        // Vectors to a thread: more of them keep as many loads in flight with fewer warps to meet (8192 x 8192, one scale a
-        // row: four 70.6 us, two 77.5; 16384 x 4096, groups of 128: four 72.6, two 76.6, one 90.5), fewer make a short row's
-        // way shorter where there are no others to wait for (64 x 4096: two 2.8 us, four 3.2).
+        // Vectors to a thread: more of them keep as many loads in flight with fewer warps to meet (8192 x
+        // 8192, one scale a row: four 70.6 us, two 77.5; 16384 x 4096, groups of 128: four 72.6, two 76.6, one
+        // 90.5), fewer make a short row's way shorter where there are no others to wait for (64 x 4096: two
+        // 2.8 us, four 3.2).
         const int v = vecs <= 128 ? 1 : vecs < 512 || (vecs <= 1024 && a.rows <= kFewRows) ? 2 : 4;
         const int threads = ((vecs + v - 1) / v + 31) / 32 * 32;
         return launch_next(v == 1 ? norm_rows_kernel<T, 1> : v == 2 ? norm_rows_kernel<T, 2> : norm_rows_kernel<T, 4>, dim3((unsigned)a.rows),

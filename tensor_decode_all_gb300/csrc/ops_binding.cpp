@@ -321,7 +321,8 @@ PyObject *attend(PyObject *const *o) {
                                                : Py_BuildValue("NN", THPVariable_Wrap(out), THPVariable_Wrap(lse));
 }
 
-// norm(x, weight, residual | None, eps, group, out | None, scales | None, residual_out | None) -> (out, scales, residual_out | None)
+// norm(x, weight, residual | None, eps, group, out | None, scales | None, residual_out | None) -> (out,
+// scales, residual_out | None)
 PyObject *norm(PyObject *const *o) {
     const Tensor &x = tensor("x", o[0]), &w = tensor("weight", o[1]);
     const int dev = device_of("x", x);
