@@ -663,9 +663,15 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
 #pragma unroll 1
                 for (int i = 0; i < CT; i += CI) multiply(std::true_type(), data + i * tile_bytes(D), 0);
             } else {
-                const int tok0 = chunk_at(next, seg().sink_chunks, seg().low_chunk) * C::Tokens;
+                const Segment &s = seg();
+                const int tok0 = chunk_at(next, s.sink_chunks, s.low_chunk) * C::Tokens;
 #pragma unroll 1
-                for (int i = 0; i < CT; i += CI) multiply(std::false_type(), data + i * tile_bytes(D), tok0 + i * kTileTokens);
+                for (int i = 0; i < CT; i += CI) {
+                    const int from = tok0 + i * kTileTokens, to = from + CI * kTileTokens - 1;
+                    // (a step that no row sees is left out)
+                    if (from <= s.pos_hi && (!a.window || to > s.pos_lo - a.window || from < a.sinks))
+                        multiply(std::false_type(), data + i * tile_bytes(D), from);
+                }
             }
             ++next;
             ++used;
