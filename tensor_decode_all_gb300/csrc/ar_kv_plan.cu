@@ -97,29 +97,43 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const ar_kv_plan_arg
     // Every block of the cluster has read what follows may overwrite.
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 
-    const int first = blockIdx.x * kPlanThreads + threadIdx.x, stride = gridDim.x * kPlanThreads;
-    for (int b = first; b < a.requests; b += stride) {
+    const unsigned first = blockIdx.x * kPlanThreads + threadIdx.x, stride = gridDim.x * kPlanThreads;
+    for (int b = (int)first; b < a.requests; b += (int)stride) {
         const int end = b + 1 < a.requests ? token0[b + 1] : tokens;
         a.lens_out[b] = len[b] + (status ? 0 : end - token0[b]);
         a.cu[b] = status ? 0 : token0[b];
     }
-    for (int i = first; i < pages; i += stride) {
-        const int b = find(page0, a.requests, i);
+    for (unsigned n = first; n < (unsigned)pages; n += stride) {
+        const int i = (int)n, b = find(page0, a.requests, i);
         a.table[(int64_t)b * a.table_stride + pages_of(len[b], a.page) + i - page0[b]] = a.free_pages[used + i];
     }
-    for (int i = first; i < a.max_tokens; i += stride) {
-        int64_t slot = -1;
-        int b = -1, p = -1;
-        if (i < tokens) {
-            b = find(token0, a.requests, i);
-            p = len[b] + i - token0[b];
-            const int col = p / a.page, had = pages_of(len[b], a.page);
-            const int64_t id = col < had ? a.table[(int64_t)b * a.table_stride + col] : a.free_pages[used + page0[b] + col - had];
-            slot = id * a.page + p % a.page;
+    // Four tokens of a thread at a time: their loads are under way together.
+    // (unsigned: a stride past the last of 2^31 stays above it)
+    for (unsigned i0 = first; i0 < (unsigned)a.max_tokens; i0 += 4 * stride) {
+        int b[4], p[4], in[4];
+        int64_t id[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const unsigned i = i0 + e * stride;
+            b[e] = p[e] = in[e] = -1;
+            id[e] = 0;
+            if (i < (unsigned)tokens) {
+                b[e] = find(token0, a.requests, (int)i);
+                p[e] = len[b[e]] + (int)i - token0[b[e]];
+                const int col = p[e] / a.page, had = pages_of(len[b[e]], a.page);
+                in[e] = p[e] - col * a.page;
+                id[e] = col < had ? a.table[(int64_t)b[e] * a.table_stride + col] : a.free_pages[used + page0[b[e]] + col - had];
+            }
         }
-        a.slots[i] = slot;
-        a.request[i] = b;
-        a.position[i] = p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const unsigned i = i0 + e * stride;
+            if (i < (unsigned)a.max_tokens) {
+                a.slots[i] = id[e] * a.page + in[e];
+                a.request[i] = b[e];
+                a.position[i] = p[e];
+            }
+        }
     }
     if (first == 0) {
         a.cu[a.requests] = tokens;

@@ -115,6 +115,15 @@ Tensor make(at::IntArrayRef shape, at::ScalarType type, const Tensor &like) {
     return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);      // (without the dispatcher's way there)
 }
 
+// n elements of another tensor's memory, from a byte on: cheaper than an allocation of their own.
+Tensor part_of(const Tensor &room, at::ScalarType type, int64_t byte, int64_t n) {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(room.storage()), room.key_set(),
+                                                        c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_storage_offset(byte / (int64_t)c10::elementSize(type));
+    t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+    return t;
+}
+
 ar_stream_t stream_of(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
 
 PyObject *fail(int rc, const char *call) {
@@ -174,11 +183,14 @@ PyObject *plan(PyObject *const *o) {
     static const char *const names[7] = {"out.lens", "out.cu", "out.request", "out.position", "out.free_used", "out.status", "out.slots"};
     const int64_t sizes[7] = {B, B + 1, cap, cap, 1, 1, cap};
     if (o[7] != Py_None && (!PyTuple_Check(o[7]) || PyTuple_GET_SIZE(o[7]) != 7)) refuse("out", "not a KvPlan");
-    Tensor out[7];
+    Tensor out[7], room;
+    int64_t at = 8 * cap;        // slots come first
+    if (o[7] == Py_None) room = make({cap + B + 2 + cap}, at::kLong, lens);
     for (int i = 0; i < 7; ++i) {
         const at::ScalarType type = i == 6 ? at::kLong : at::kInt;
         if (o[7] == Py_None) {
-            out[i] = make({sizes[i]}, type, lens);
+            out[i] = part_of(room, type, i == 6 ? 0 : at, sizes[i]);
+            if (i < 6) at += 4 * sizes[i];
         } else {
             out[i] = tensor(names[i], PyTuple_GET_ITEM(o[7], i));
             check(names[i], out[i], dev, type, 1, true);
