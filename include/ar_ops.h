@@ -138,6 +138,7 @@ AR_API int ar_kv4_load(const ar_kv4_rows_args *args, ar_stream_t stream);
  * stays inside the buffers; outputs of such requests are undefined), and AR_ETIMEOUT
  * after a copy into shared memory that did not arrive.
  * Results do not depend on the order in which blocks run.
+ * out must not overlap q (AR_EINVAL for the same address).
  * Errors: AR_EINVAL, AR_ETOOBIG (requests > 8192, tokens * query heads of a kv
  * head > 2^30, or a window > 2^30 shorter than the table), AR_ECUDA.
  */
@@ -177,7 +178,8 @@ AR_API int ar_kv4_status(const void *workspace);
  * Per row: h = x + residual (binary32; residual NULL: h = x), y = h / sqrt(mean(h^2) +
  * eps) * weight; per group of `group` channels (0: the row; the last group may
  * be short): scale = max|y| / 448 (1 if that is 0), out = e4m3(y / scale).
- * residual_out (may be residual or x): h rounded to dtype; NULL: not written.
+ * residual_out (may be residual or x themselves, by their strides; no other overlap): h rounded to dtype;
+ * NULL: not written.
  * out [rows][dim] and scales [rows][ceil(dim / group)] are contiguous; the others go by their row strides.
  * Errors: AR_EINVAL, AR_ETOOBIG (dim > 32768), AR_ECUDA.
  */

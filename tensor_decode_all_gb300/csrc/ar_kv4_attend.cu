@@ -929,6 +929,7 @@ AR_API int ar_kv4_attend(const ar_kv4_attend_args *args, ar_stream_t stream) {
         return AR_EINVAL;
     if (a.requests > kMaxRequests) return AR_ETOOBIG;
     if (a.tokens == 0) return AR_OK;
+    if (a.q == a.out) return AR_EINVAL;      // other blocks may still read q when a row is written
     if (!a.q || !a.out || !a.workspace || a.requests < 1 || !a.lens || (!a.table && a.table_width > 0) ||
         (a.table_width > 0 && (!a.pool || a.pages < 1)))
         return AR_EINVAL;

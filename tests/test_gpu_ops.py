@@ -683,3 +683,11 @@ def test_offsets_past_32_bits():
     for a, b in zip(*got):
         assert torch.equal(a, b)
     assert (got[0][0].float() - k.float()).abs().max() < 0.5 and got[0][2].abs().sum() > 0
+
+
+def test_attend_refuses_to_write_over_q():
+    tda = _tda()
+    q, pool, K, V, table, cu = _attend_case(1, 1, [20], [1], 1, 8, 64, 16, "f16")
+    qd = q.cuda()
+    with pytest.raises(tda.ArError):
+        tda.kv4_attend(qd, pool.cuda(), _i32(table), _i32([20]), out=qd)
