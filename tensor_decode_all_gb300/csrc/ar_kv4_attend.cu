@@ -24,9 +24,9 @@
 // 18 D contiguous bytes) a stage ahead, the next segment's first stages before the last one's results are
 // written.
 //
-// Measured on a GB300 (graph replays): 64 requests of 16385 to 32768 tokens, 8 kv heads of 8, D 128: 307 us,
+// Measured on a GB300 (graph replays): 64 requests of 16385 to 32768 tokens, 8 kv heads of 8, D 128: 308 us,
 // 5.9 TB/s of cache or 87% of what a plain copy reaches; 64 ragged ones of 517 to 8001: 69 us, 67%; 128 ragged
-// with a window of 1024 and D 64: 33 us; one of 1003 tokens and one kv head: 9.6 us.  The short ones are bound
+// with a window of 1024 and D 64: 32 us; one of 1003 tokens and one kv head: 9.6 us.  The short ones are bound
 // by the instructions they issue: 308 for a tile of 16 tokens and one head of 128, 0.56 a cycle and scheduler,
 // two of five on the ALU pipe, which takes one every other cycle; DRAM carries 1.006 times the bytes that have
 // to be read, and the matrix instructions take a quarter of the time.  12 warps a multiprocessor: 16 with 126

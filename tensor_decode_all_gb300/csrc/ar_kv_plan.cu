@@ -7,7 +7,7 @@
 // updated in place.
 //
 // Bound by latency: 64 requests of a token each take 4.9 us on a GB300, 1000 requests with 23524 new tokens
-// 9.2 (graph replays; the second writes 0.4 MB).
+// 9.1 (graph replays; the second writes 0.4 MB).
 #include "ar_kv4.cuh"
 
 namespace {
