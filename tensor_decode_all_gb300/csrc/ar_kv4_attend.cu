@@ -396,6 +396,7 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
             }
             break;
         }
+        __syncwarp();                    // every lane has read where the walk stood
         if (lane == 0) {
             segments[warp][walked & 1] = s;
             start_b[warp] = b;
