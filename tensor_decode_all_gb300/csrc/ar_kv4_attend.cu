@@ -9,11 +9,12 @@
 // The products are S^T = K Q^T and O^T = V^T P^T (mma.m16n8k16, fp16 operands, binary32 sums), with the tokens
 // (channels) as the 16 rows and the query rows as the 8 columns, so that a group of 8 heads fills the
 // instruction.  (tcgen05 has 64 rows at least, and wants its operands in shared memory: each nibble would be
-// written there at four times its size and read once.)  K and V enter as the whole numbers they are.  A nibble
-// u in the mantissa of a power of two is that power plus u: K's operands stay so, and what that adds to a
-// group's sum, a constant of the query row, is where the accumulator starts; V's get it subtracted, since its
-// sums run over all tokens.  K's scales multiply the sums of each group of 32 channels, V's the weights, both
-// in binary32; weight x scale is rounded once, to fp16.
+// written there at four times its size and read once.)  K and V enter as the whole numbers u - 8 that they are: a
+// nibble u in the mantissa of a power of two is that power plus u, and one exact instruction to a pair takes the
+// rest off.  (Taking K's out of the sums instead, by where the accumulators start, saves that instruction and
+// loses bits, up to 8 where most of a group is 0, and the product of an infinite scale with a sum that is 0.)  K's
+// scales multiply the sums of each group of 32 channels, V's the weights, both in binary32; weight x scale is
+// rounded once, to fp16.
 //
 // Softmax runs in base 2 under a reference M per row, common to a warp, that moves only when a score passes it
 // by 2^6: p = 2^(s - M), and the usual step costs a vote in place of a reduction.  M also holds the exponent
@@ -117,19 +118,6 @@ __device__ __forceinline__ void nibbles_to_half(uint32_t w, uint32_t (&h)[4]) {
     }
 }
 
-// The 8 nibbles of w as fp16 pairs in the same order, the pairs 0 and 2 as
-// 256 + u and 1 and 3 as 16 + u: a nibble in the upper bits of a mantissa is a
-// whole number above a power of two.  What is too much, kOver0 or kOver1 of each, is
-// taken out of the sums (see the products with q).
-constexpr float kOver0 = 256 + 8, kOver1 = 16 + 8;
-__device__ __forceinline__ void nibbles_over(uint32_t w, uint32_t (&h)[4]) {
-    const uint32_t lo = w << 2, hi = w >> 6, k256 = 0x5c005c00u, k16 = 0x4c004c00u;
-    asm("lop3.b32 %0, %1, 0x003c003c, %2, 0xea;" : "=r"(h[0]) : "r"(lo), "r"(k256));
-    asm("lop3.b32 %0, %1, 0x03c003c0, %2, 0xea;" : "=r"(h[1]) : "r"(lo), "r"(k16));
-    asm("lop3.b32 %0, %1, 0x003c003c, %2, 0xea;" : "=r"(h[2]) : "r"(hi), "r"(k256));
-    asm("lop3.b32 %0, %1, 0x03c003c0, %2, 0xea;" : "=r"(h[3]) : "r"(hi), "r"(k16));
-}
-
 // N words from shared memory in the widest accesses (the address is a multiple of 4 N, up to 16).
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
@@ -158,9 +146,6 @@ struct Shape {
     static constexpr int G = D / kGroup;
     static constexpr int Tokens = CT * kTileTokens;
     static constexpr int Rows = 8 * NT;
-    // One row tile: the constants that nibbles stand on come out of K's sums; with more of them subtracting
-    // before the products costs less, each nibble serving all (and needs no registers for what to take out).
-    static constexpr bool Over = NT == 1;
     static constexpr int Stage = CT * tile_bytes(D);
     static constexpr int Smem = kWarps * S * Stage;
     static constexpr size_t PartFloats = (size_t)Rows * (D + 2);   // rows, then their references and sums
@@ -466,7 +451,6 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
 
     // ---- the products' side
     uint2 qf[NT][D / 16];
-    float less[C::Over ? NT : 1][G][2];   // minus what nibbles_over puts on top of a group's products
     float mult[NT][2];                    // what a sum of products is worth, in base 2: columns 2 t and 2 t + 1
     float o[D / 16][NT][4];
     float ref[NT][2], l[NT][2];
@@ -491,13 +475,8 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 uint32_t h0[4], h1[4];
-                if constexpr (C::Over) {
-                    nibbles_over(w0[j], h0);
-                    nibbles_over(w1[j], h1);
-                } else {
-                    nibbles_to_half(w0[j], h0);
-                    nibbles_to_half(w1[j], h1);
-                }
+                nibbles_to_half(w0[j], h0);
+                nibbles_to_half(w1[j], h1);
                 const uint32_t a0[4] = {h0[0], h1[0], h0[1], h1[1]}, a1[4] = {h0[2], h1[2], h0[3], h1[3]};
                 const float s0 = __uint_as_float(j & 1 ? sc0[j / 2] & 0xffff0000u : sc0[j / 2] << 16);
                 const float s1 = __uint_as_float(j & 1 ? sc1[j / 2] & 0xffff0000u : sc1[j / 2] << 16);
@@ -505,10 +484,7 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
                 for (int n = 0; n < NT; ++n) {
                     float acc[4];
                     const uint2 q0 = qf[n][2 * j], q1 = qf[n][2 * j + 1];
-                    if constexpr (C::Over)
-                        mma16816(acc, a0, q0.x, q0.y, less[n][j][0], less[n][j][1], less[n][j][0], less[n][j][1]);
-                    else
-                        mma16816(acc, a0, q0.x, q0.y, 0.0f, 0.0f, 0.0f, 0.0f);
+                    mma16816(acc, a0, q0.x, q0.y, 0.0f, 0.0f, 0.0f, 0.0f);
                     mma16816(acc, a1, q1.x, q1.y);
                     if (j == 0) {
                         x[ct][n][0] = acc[0] * s0; x[ct][n][1] = acc[1] * s0;
@@ -750,24 +726,10 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 uint32_t h[4];
-                float over = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    h[i] = pack_half(x[j][i] * unit, x[j][i + 4] * unit);
-                    if constexpr (C::Over) {
-                        // of the operands as they are, rounded
-                        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
-                        over = fmaf(i & 1 ? kOver1 : kOver0, v.x + v.y, over);
-                    }
-                }
+                for (int i = 0; i < 4; ++i) h[i] = pack_half(x[j][i] * unit, x[j][i + 4] * unit);
                 qf[n][2 * j] = make_uint2(h[0], h[1]);
                 qf[n][2 * j + 1] = make_uint2(h[2], h[3]);
-                if constexpr (C::Over) {
-                    over += __shfl_xor_sync(~0u, over, 1);
-                    over += __shfl_xor_sync(~0u, over, 2);
-                    less[n][j][0] = -__shfl_sync(~0u, over, 8 * t);
-                    less[n][j][1] = -__shfl_sync(~0u, over, 8 * t + 4);
-                }
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) mult[n][i] = __shfl_sync(~0u, worth, (2 * t + i) * 4);

@@ -36,3 +36,46 @@ def test_attend_many_segments_to_a_warp(window, sinks):
                               sinks=sinks, return_lse=True)
     assert ((out.cpu().double() - want[pick]).abs() <= bo[pick]).all()
     assert ((lse.cpu().double() - wl[pick]).abs() <= bl[pick]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,G,max_new", [(128, 8, 1), (64, 4, 1), (256, 8, 1), (128, 8, 2), (64, 8, 2)])
+@pytest.mark.parametrize("inf", [math.inf, -math.inf])
+def test_attend_infinity_in_k_is_nan(dtype, D, G, max_new, inf):
+    """An infinity that kv4_append met in K reads back as NaN (0 x inf), so every row that sees its token is NaN,
+    whatever shape the call takes, and no other row changes."""
+    tda = _tda()
+    B, n, page = 48, 40, 16
+    q, pool, K, V, table, cu = _attend_case(53, B, [n] * B, [1] * B, 1, G, D, page, dtype)
+    pd, args = pool.cuda(), (_i32(table), _i32([n] * B), _i32(cu))
+    clean = tda.kv4_attend(q.cuda(), pd, *args, max_new=max_new, return_lse=True)
+    k = torch.randn(B // 2, 1, D, generator=_gen(54)).to(H.DT[dtype])
+    for b in range(B // 2):
+        k[b, 0, (7 * b) % D] = inf
+    slots = torch.tensor([table[b][(b + 3) % n // page] * page + (b + 3) % n % page for b in range(B // 2)])
+    tda.kv4_append(k.cuda(), k.nan_to_num(0, 0, 0).cuda(), pd, slots.cuda())
+    out, lse = tda.kv4_attend(q.cuda(), pd, *args, max_new=max_new, return_lse=True)
+    assert out[:B // 2].isnan().all() and lse[:B // 2].isnan().all()
+    assert torch.equal(out[B // 2:], clean[0][B // 2:]) and torch.equal(lse[B // 2:], clean[1][B // 2:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,G,max_new", [(128, 8, 1), (64, 4, 1), (256, 8, 1), (128, 8, 2)])
+def test_attend_large_channels_in_k(dtype, D, G, max_new):
+    """One large channel to each group of K, as trained caches have: most nibbles are 0 and sum |q k| small beside
+    sum |q|, and the queries have an offset; the bounds on the scores' sums (of |q k|) hold all the same."""
+    tda = _tda()
+    lens, page = [300, 77, 1, 64], 16
+    q, pool, K, V, table, cu = _attend_case(59, 4, lens, [1] * 4, 2, G, D, page, dtype)
+    kn, ks, vn, vs = H.unpack(pool)
+    small = kn.sign() * (kn.abs() == 7)
+    large = torch.zeros(D)
+    large[5::32] = 7
+    kn = torch.where(large > 0, large * kn.sign(), small)
+    pool = H.pack(kn, ks[..., ::32].to(torch.bfloat16), vn, vs[..., ::32].to(torch.bfloat16))
+    K = (kn * ks).reshape(K.shape)
+    q = q.float() + 3
+    q[..., 5::32] *= 2.0 ** -12
+    q = q.to(H.DT[dtype])
+    out, lse = tda.kv4_attend(q.cuda(), pool.cuda(), _i32(table), _i32(lens), max_new=max_new, return_lse=True)
+    _check_attend(q, K, V, table, lens, cu, 0, 0, D ** -0.5, out, lse)
