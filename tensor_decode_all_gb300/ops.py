@@ -177,7 +177,10 @@ _workspace_lock = threading.Lock()
 
 class Kv4Workspace:
     """Working memory of kv4_attend on one device: one for calls that may overlap on the GPU.  Calls
-    without one share a workspace of their stream's (see kv4_workspace), which lives as long as the process."""
+    without one share a workspace of their stream's (see kv4_workspace), which lives as long as the process.
+
+    Ready for any stream once made (which waits for the current one); whoever makes it keeps it until the
+    calls that use it, and the graphs they were captured in, are done."""
 
     def __init__(self, device=None, stream=None):
         import torch
@@ -193,6 +196,7 @@ class Kv4Workspace:
         rc = L.ar_kv4_workspace_init(self.ptr, torch.cuda.current_stream(dev).cuda_stream)
         if rc:
             raise ArError(rc, "ar_kv4_workspace_init")
+        torch.cuda.current_stream(dev).synchronize()
 
     def status(self) -> int:
         """The first error recorded since it was made (AR_OK if none); synchronise with the calls first."""
@@ -224,7 +228,6 @@ def kv4_workspace(device=None, stream=None) -> Kv4Workspace:
                     return ws if ws is not None else Kv4Workspace(dev)     # which says why it cannot
                 if (dev, "capture") not in _workspaces:
                     _workspaces[dev, "capture"] = Kv4Workspace(dev)
-                    torch.cuda.current_stream(dev).synchronize()           # ready on every stream
                 ws = _workspaces[key] = Kv4Workspace(dev)
                 _binding().set_workspace(dev, key[1], ws.ptr)
     return ws

@@ -79,3 +79,12 @@ def test_attend_large_channels_in_k(dtype, D, G, max_new):
     q = q.to(H.DT[dtype])
     out, lse = tda.kv4_attend(q.cuda(), pool.cuda(), _i32(table), _i32(lens), max_new=max_new, return_lse=True)
     _check_attend(q, K, V, table, lens, cu, 0, 0, D ** -0.5, out, lse)
+
+
+# --------------------------------------------------------------- workspaces
+
+def test_a_workspace_is_ready_on_every_stream():
+    """Its zeros are written on the current stream, and a call on another one need not wait for that."""
+    torch.cuda._sleep(200_000_000)
+    _tda().Kv4Workspace()
+    assert torch.cuda.current_stream().query()
