@@ -120,7 +120,8 @@ def main(argv=None):
                 same &= all(torch.equal(xs[0][0].view(torch.uint8), x[0].view(torch.uint8)) and torch.equal(residuals[0], r)
                             for x, r in zip(xs, residuals))
         handle.check()
-        tda.kv4_workspace(stream=ranks[0].stream).check()
+        for workspace in tda.kv4_workspaces():
+            workspace.check()
     print(f"{a.steps} steps of {a.layers} layers on {a.ranks} ranks: relative distance from float32 at most {worst:.2g}, "
           f"all ranks {'the same' if same else 'NOT the same'}")
     return worst, same

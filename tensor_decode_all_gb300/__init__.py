@@ -15,4 +15,4 @@ from .ar import (AR_BF16, AR_C64, AR_F16, AR_SLOT_HBM, AR_SLOT_PINNED_HOST, ArEr
                  ar_plan_for, ar_probe_hbm_copy, ar_probe_host_link, ar_probe_host_link_latency, ar_query, ar_reset, ar_set_algo, ar_set_pdl, ar_set_timeout,
                  ar_status, ar_strerror, declared_symbols, lib, library_path, strerror)
 from .builder import build  # noqa: F401
-from .ops import KvPlan, Kv4Workspace, add_norm_fp8, kv4_append, kv4_attend, kv4_load, kv4_pool, kv4_workspace, kv_plan  # noqa: F401
+from .ops import KvPlan, Kv4Workspace, add_norm_fp8, kv4_append, kv4_attend, kv4_load, kv4_pool, kv4_workspace, kv4_workspaces, kv_plan  # noqa: F401

@@ -120,9 +120,10 @@ def _compile_binding() -> str:
 
 def _link_binding(obj: str) -> None:
     t, tmp = os.path.join(_torch_dir(), "lib"), BINDING + f".tmp{os.getpid()}"
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "lib64")
     _run("link of the operators' binding", [
         _cxx(), "-shared", "-o", tmp, obj, f"-L{PKG}", "-l:libtda_ar.so", f"-L{t}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
-        "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{t}"])
+        "-ltorch_cuda", "-lc10", "-lc10_cuda", f"-L{cuda}", "-lcudart", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{t}"])
     os.replace(tmp, BINDING)
 
 

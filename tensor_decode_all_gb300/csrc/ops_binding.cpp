@@ -10,6 +10,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <cuda_runtime_api.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -125,6 +126,17 @@ Tensor part_of(const Tensor &room, at::ScalarType type, int64_t byte, int64_t n)
 }
 
 ar_stream_t stream_of(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
+
+// The capture that a stream is part of, by its id; 0: none.
+unsigned long long capture_of(ar_stream_t stream) {
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaStreamGetCaptureInfo(stream, &status, &id) != cudaSuccess) {
+        (void)cudaGetLastError();      // (the legacy stream beside another's capture: the launch will say so)
+        return 0;
+    }
+    return status == cudaStreamCaptureStatusActive ? id : 0;
+}
 
 PyObject *fail(int rc, const char *call) {
     PyObject *e = PyObject_CallFunction(g_error, "is", rc, call);
@@ -259,7 +271,8 @@ PyObject *load(PyObject *const *o) {
     return tuple_of({&k, &v});
 }
 
-// Workspaces of kv4_attend by device and stream; ops.py makes them and keeps them alive.
+// Workspaces of kv4_attend by device and stream, for calls that are not captured; ops.py makes them and keeps
+// them alive.
 struct Place {
     int dev;
     ar_stream_t stream;
@@ -268,7 +281,7 @@ struct Place {
 std::vector<Place> g_places;   // guarded by the interpreter's lock
 
 // attend(q, pool, table, lens, cu | None, max_new | None, window, sinks, scale | None, out | None, lse | None, return_lse, workspace | None)
-//   -> out, (out, lse), or None where no workspace was given and the stream has none yet
+//   -> out, (out, lse), or None where no workspace was given and the stream has none yet or is being captured
 PyObject *attend(PyObject *const *o) {
     const Tensor &q = tensor("q", o[0]), &pool = tensor("pool", o[1]), &table = tensor("table", o[2]), &lens = tensor("lens", o[3]);
     const int dev = device_of("pool", pool);
@@ -297,8 +310,9 @@ PyObject *attend(PyObject *const *o) {
     if (o[12] != Py_None) {
         ws = PyLong_AsVoidPtr(o[12]);
     } else {
-        for (const Place &p : g_places)
-            if (p.dev == dev && p.stream == stream) ws = p.ws;
+        if (!capture_of(stream))
+            for (const Place &p : g_places)
+                if (p.dev == dev && p.stream == stream) ws = p.ws;
         if (!ws) return Py_INCREF(Py_None), Py_None;
     }
     Tensor out, lse;
@@ -401,6 +415,11 @@ PyObject *set_workspace(PyObject *const *o) {
     Py_RETURN_NONE;
 }
 
+// capture_id(stream): of the capture that the stream is part of, 0 if none
+PyObject *capture_id(PyObject *const *o) {
+    return PyLong_FromUnsignedLongLong(capture_of(static_cast<ar_stream_t>(PyLong_AsVoidPtr(o[0]))));
+}
+
 PyObject *set_error(PyObject *const *o) {
     Py_INCREF(o[0]);
     Py_XDECREF(g_error);
@@ -433,8 +452,8 @@ PyMethodDef method(const char *name) {
 }
 
 PyMethodDef g_methods[] = {method<plan, 8>("plan"), method<append, 4>("append"), method<load, 4>("load"), method<attend, 13>("attend"),
-                           method<norm, 8>("norm"), method<set_workspace, 3>("set_workspace"), method<set_error, 1>("set_error"),
-                           {nullptr, nullptr, 0, nullptr}};
+                           method<norm, 8>("norm"), method<set_workspace, 3>("set_workspace"), method<capture_id, 1>("capture_id"),
+                           method<set_error, 1>("set_error"), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ops_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

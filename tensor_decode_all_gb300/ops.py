@@ -171,7 +171,9 @@ def kv4_load(pool, slots, dtype=None, *, out=None, stream=None):
 
 # ---------------------------------------------------------------- attention
 
-_workspaces = {}
+_workspaces = {}            # by device and stream, for calls that are not captured
+_captured = {}              # by device: the ones of captured calls ...
+_capture_streams = {}       # ... dealt out to the streams of a capture, by device and capture, in the order they come
 _workspace_lock = threading.Lock()
 
 
@@ -211,26 +213,43 @@ class Kv4Workspace:
 def kv4_workspace(device=None, stream=None) -> Kv4Workspace:
     """The workspace that kv4_attend uses on this stream when it is given none.
 
-    Calls that are being captured share one of their device's, made with the first workspace on it:
-    graphs that may run at the same time need one each (``workspace=``)."""
+    While the stream is captured that is another one, kept for captured calls: the replays of a graph may
+    overlap with calls on the stream it was captured on.  The streams of one capture use one each, of those that
+    are made beside the first workspaces of the device's streams (as many, and two at least); a capture of
+    more streams than there are is refused.  Different captures use the same: graphs that may run at the
+    same time need workspaces of their own (``workspace=``)."""
     import torch
     if stream is not None:
         return _under(stream, kv4_workspace, device)
     dev = torch.cuda.current_device() if device is None else torch.device(device).index
     key = dev, torch.cuda.current_stream(dev).cuda_stream
-    ws = _workspaces.get(key)
-    if ws is None:
-        with _workspace_lock:
-            ws = _workspaces.get(key)
-            if ws is None:
-                if torch.cuda.is_current_stream_capturing():
-                    ws = _workspaces.get((dev, "capture"))
-                    return ws if ws is not None else Kv4Workspace(dev)     # which says why it cannot
-                if (dev, "capture") not in _workspaces:
-                    _workspaces[dev, "capture"] = Kv4Workspace(dev)
-                ws = _workspaces[key] = Kv4Workspace(dev)
-                _binding().set_workspace(dev, key[1], ws.ptr)
+    capture = _binding().capture_id(key[1])
+    with _workspace_lock:
+        captured = _captured.setdefault(dev, [])
+        if capture:
+            streams = _capture_streams.setdefault((dev, capture), [])
+            if key[1] not in streams:
+                if len(streams) >= len(captured):
+                    raise RuntimeError(f"kv4_attend is captured on more streams than there are workspaces for it ({len(captured)}): "
+                                       "call kv4_workspace() on as many streams before, or give each its own (workspace=)")
+                streams.append(key[1])
+            return captured[streams.index(key[1])]
+        ws = _workspaces.get(key)
+        if ws is None:
+            while len(captured) < max(2, 1 + sum(d == dev for d, _ in _workspaces)):
+                captured.append(Kv4Workspace(dev))
+            ws = _workspaces[key] = Kv4Workspace(dev)
+            _binding().set_workspace(dev, key[1], ws.ptr)
     return ws
+
+
+def kv4_workspaces(device=None) -> list:
+    """All workspaces kept for kv4_attend on a device, its streams' and those of captured calls, for their
+    ``check()`` after a step (synchronise with its calls and replays first)."""
+    import torch
+    dev = torch.cuda.current_device() if device is None else torch.device(device).index
+    with _workspace_lock:
+        return [ws for (d, _), ws in _workspaces.items() if d == dev] + _captured.get(dev, [])
 
 
 def kv4_attend(q, pool, table, lens, cu=None, *, max_new=None, window=0, sinks=0, scale=None, out=None, lse=None,
@@ -253,7 +272,7 @@ def kv4_attend(q, pool, table, lens, cu=None, *, max_new=None, window=0, sinks=0
             raise ValueError(f"workspace: on cuda:{workspace.device}, not {pool.device}")
         workspace = workspace.ptr
     made = attend(q, pool, table, lens, cu, max_new, window, sinks, scale, out, lse, return_lse, workspace)
-    if made is None:        # this stream's first call
+    if made is None:        # this stream's first call, or a captured one
         made = attend(q, pool, table, lens, cu, max_new, window, sinks, scale, out, lse, return_lse, kv4_workspace().ptr)
     if out is None and lse is None:
         return made

@@ -88,3 +88,111 @@ def test_a_workspace_is_ready_on_every_stream():
     torch.cuda._sleep(200_000_000)
     _tda().Kv4Workspace()
     assert torch.cuda.current_stream().query()
+
+
+def _small_call(B=2):
+    q, pool, K, V, table, cu = _attend_case(61, B, [20] * B, [1] * B, 1, 8, 64, 16, "bf16")
+    return q.cuda(), pool.cuda(), _i32(table), _i32([20] * B)
+
+
+@pytest.mark.parametrize("warm", [True, False])
+def test_captured_calls_keep_to_their_own_workspace(warm):
+    """Whether or not the stream ran calls before its capture: what a replay records is in the workspace that
+    kv4_workspace gave inside the capture, which kv4_workspaces lists, and in no stream's own."""
+    tda = _tda()
+    s = torch.cuda.Stream()
+    q, pool, table, lens = _small_call()
+    tda.kv4_attend(q, pool, table, lens)
+    if warm:
+        tda.kv4_attend(q, pool, table, lens, stream=s)
+    table = table.clone()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s), torch.cuda.graph(graph, stream=s):
+        tda.kv4_attend(q, pool, table, lens)
+        used = tda.kv4_workspace()
+    own = [tda.kv4_workspace(), tda.kv4_workspace(stream=s)]
+    every = tda.kv4_workspaces()
+    assert used not in own and used in every and all(w in every for w in own)
+    table[0, 0] = pool.shape[0]
+    try:
+        graph.replay()
+        torch.cuda.synchronize()
+        assert used.status() == tda.ar.AR_EINVAL
+        assert [w.status() for w in own] == [0, 0]
+    finally:
+        tda.ops._ops().ar_kv4_workspace_init(used.ptr, None)
+        torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("warm", [True, False])
+def test_a_graph_with_parallel_branches(warm):
+    """Two streams of one capture attend at the same time, over long requests whose parts are joined."""
+    tda = _tda()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    cases = []
+    for seed, n, G in ((71, 9001, 8), (73, 7003, 4)):
+        q, pool, K, V, table, cu = _attend_case(seed, 2, [n, 333], [1, 1], 2, G, 128, 64, "bf16")
+        cases.append((q.cuda(), pool.cuda(), _i32(table), _i32([n, 333])))
+    want = [tda.kv4_attend(*c) for c in cases]
+    if warm:
+        for s, c in zip((main, side), cases):
+            tda.kv4_attend(*c, stream=s)
+    torch.cuda.synchronize()
+    graph, got = torch.cuda.CUDAGraph(), [[], []]
+    with torch.cuda.stream(main), torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        for _ in range(10):
+            with torch.cuda.stream(side):
+                got[1].append(tda.kv4_attend(*cases[1]))
+            got[0].append(tda.kv4_attend(*cases[0]))
+        with torch.cuda.stream(side):
+            second = tda.kv4_workspace()
+        assert tda.kv4_workspace() is not second
+        main.wait_stream(side)
+    for _ in range(5):
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(x, w) for x in g)
+            for x in g:
+                x.zero_()
+
+
+def test_replays_beside_calls_on_the_captured_stream():
+    """The usual warm-up, then a capture on the same stream: replays on another stream overlap with its calls."""
+    tda = _tda()
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    q, pool, K, V, table, cu = _attend_case(79, 2, [9001, 333], [1, 1], 2, 8, 128, 64, "bf16")
+    args = q.cuda(), pool.cuda(), _i32(table), _i32([9001, 333])
+    want = tda.kv4_attend(*args, stream=s)
+    graph, got = torch.cuda.CUDAGraph(), []
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s), torch.cuda.graph(graph, stream=s):
+        for _ in range(20):
+            got.append(tda.kv4_attend(*args))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        graph.replay()
+    got += [tda.kv4_attend(*args, stream=s) for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in got)
+
+
+def test_a_capture_of_more_streams_than_workspaces_is_refused(monkeypatch):
+    tda = _tda()
+    args = _small_call()
+    tda.kv4_attend(*args)
+    dev = torch.cuda.current_device()
+    monkeypatch.setitem(tda.ops._captured, dev, tda.ops._captured[dev][:2])
+    main, *sides = [torch.cuda.Stream() for _ in range(4)]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main), torch.cuda.graph(graph, stream=main):
+        for s in sides:
+            s.wait_stream(main)
+        with pytest.raises(RuntimeError, match="captured on more streams"):
+            for s in sides:
+                tda.kv4_attend(*args, stream=s)
+        for s in sides:
+            main.wait_stream(s)
