@@ -101,6 +101,15 @@ def _on(stream, dev):
     return stream
 
 
+def _index(device) -> int:
+    """The index of a CUDA device; "cuda" and None are the current one."""
+    import torch
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError(f"device: {device} is not a CUDA device")
+    return torch.cuda.current_device() if device.index is None else device.index
+
+
 def _under(stream, call, *args, **kwargs):
     """The call with `stream` as the current one."""
     import torch
@@ -188,12 +197,12 @@ class Kv4Workspace:
         import torch
         if stream is not None:
             return _under(stream, self.__init__, device)
-        dev = torch.cuda.current_device() if device is None else torch.device(device).index
+        dev = _index(device)
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("a kv4_attend workspace cannot be made while a CUDA graph is captured: "
                                "make it (or call kv4_attend once on this stream) before")
         L = _lib or _ops()
-        self.buffer = torch.empty(L.ar_kv4_workspace_bytes(), dtype=torch.uint8, device=dev)
+        self.buffer = torch.empty(L.ar_kv4_workspace_bytes(), dtype=torch.uint8, device=torch.device("cuda", dev))
         self.device, self.ptr = dev, self.buffer.data_ptr()
         rc = L.ar_kv4_workspace_init(self.ptr, torch.cuda.current_stream(dev).cuda_stream)
         if rc:
@@ -221,7 +230,7 @@ def kv4_workspace(device=None, stream=None) -> Kv4Workspace:
     import torch
     if stream is not None:
         return _under(stream, kv4_workspace, device)
-    dev = torch.cuda.current_device() if device is None else torch.device(device).index
+    dev = _index(device)
     key = dev, torch.cuda.current_stream(dev).cuda_stream
     capture = _binding().capture_id(key[1])
     with _workspace_lock:
@@ -247,7 +256,7 @@ def kv4_workspaces(device=None) -> list:
     """All workspaces kept for kv4_attend on a device, its streams' and those of captured calls, for their
     ``check()`` after a step (synchronise with its calls and replays first)."""
     import torch
-    dev = torch.cuda.current_device() if device is None else torch.device(device).index
+    dev = _index(device)
     with _workspace_lock:
         return [ws for (d, _), ws in _workspaces.items() if d == dev] + _captured.get(dev, [])
 

@@ -196,3 +196,13 @@ def test_a_capture_of_more_streams_than_workspaces_is_refused(monkeypatch):
                 tda.kv4_attend(*args, stream=s)
         for s in sides:
             main.wait_stream(s)
+
+
+@pytest.mark.parametrize("device", ["cuda", torch.device("cuda"), "cuda:0", 0])
+def test_workspaces_by_the_name_of_their_device(device):
+    tda = _tda()
+    ws = tda.Kv4Workspace(device)
+    assert ws.buffer.device == torch.device("cuda", 0) and ws.device == 0 and ws.status() == 0
+    args = _small_call()
+    assert torch.equal(tda.kv4_attend(*args, workspace=ws), tda.kv4_attend(*args))
+    assert tda.kv4_workspace(device) is tda.kv4_workspace() and tda.kv4_workspaces(device) == tda.kv4_workspaces()
