@@ -176,7 +176,7 @@ Pool pool_of(const Tensor &p, int dev) {
 
 // ------------------------------------------------------------------ operators
 
-// plan(lens, new, table, free_pages, free_used, page, max_tokens, out | None) -> 7 tensors
+// plan(lens, new, table, free_pages, free_used, page, max_tokens, out | None) -> (stream handle, 7 tensors or out)
 PyObject *plan(PyObject *const *o) {
     const Tensor &lens = tensor("lens", o[0]), &fresh = tensor("new", o[1]), &table = tensor("table", o[2]), &pages = tensor("free_pages", o[3]),
                  &used = tensor("free_used", o[4]);
@@ -216,10 +216,12 @@ PyObject *plan(PyObject *const *o) {
     a.status = p(out[5]); a.slots = static_cast<int64_t *>(out[6].data_ptr());
     a.table_stride = B > 1 ? table.stride(0) : table.size(1);
     a.free_count = pages.size(0); a.requests = (int32_t)B; a.table_width = (int32_t)table.size(1); a.page = (int32_t)page; a.max_tokens = (int32_t)cap;
-    const int rc = ar_kv_plan(&a, stream_of(dev));
+    const ar_stream_t stream = stream_of(dev);
+    const int rc = ar_kv_plan(&a, stream);
     if (rc) return fail(rc, "ar_kv_plan");
-    if (o[7] != Py_None) return Py_INCREF(o[7]), o[7];
-    return tuple_of({&out[0], &out[1], &out[2], &out[3], &out[4], &out[5], &out[6]});
+    PyObject *made = o[7] != Py_None ? (Py_INCREF(o[7]), o[7])
+                                     : tuple_of({&out[0], &out[1], &out[2], &out[3], &out[4], &out[5], &out[6]});
+    return made ? Py_BuildValue("KN", (unsigned long long)(uintptr_t)stream, made) : nullptr;
 }
 
 int rows(bool append, const Tensor &k, const Tensor &v, const Tensor &pool, const Pool &dims, const Tensor &slots, int dev) {

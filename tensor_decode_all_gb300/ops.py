@@ -119,8 +119,7 @@ def _under(stream, call, *args, **kwargs):
 
 # --------------------------------------------------------------------- plan
 
-class KvPlan(NamedTuple):
-    """What kv_plan writes (see ar_kv_plan in ar_ops.h)."""
+class _KvPlanFields(NamedTuple):
     lens: object        # int32 [requests]: tokens with the new ones
     cu: object          # int32 [requests + 1]: where each request's new tokens begin
     request: object     # int32 [max_tokens]
@@ -129,8 +128,25 @@ class KvPlan(NamedTuple):
     status: object      # int32 [1]: an AR_* code
     slots: object       # int64 [max_tokens]
 
+
+class KvPlan(_KvPlanFields):
+    """What kv_plan writes (see ar_kv_plan in ar_ops.h)."""
+
+    _stream = None      # the handle of the stream that it is made on
+
+    def _replace(self, **fields):
+        plan = super()._replace(**fields)
+        plan._stream = self._stream
+        return plan
+
     def check(self):
-        """Raise ArError if nothing was handed out (waits for the plan)."""
+        """Raise ArError if nothing was handed out.  Waits for the plan, on whatever stream it is made (which has
+        to exist still); of a plan in a graph, for replays on the current stream."""
+        import torch
+        if self._stream is not None:
+            here = torch.cuda.current_stream(self.status.device)
+            if here.cuda_stream != self._stream:
+                here.wait_stream(_on(self._stream, self.status.device))
         code = int(self.status.item())
         if code:
             raise ArError(code, "kv_plan")
@@ -148,8 +164,11 @@ def kv_plan(lens, new, table, free_pages, free_used, *, page, max_tokens, out=No
     """
     if stream is not None:
         return _under(stream, kv_plan, lens, new, table, free_pages, free_used, page=page, max_tokens=max_tokens, out=out)
-    made = (_native or _binding()).plan(lens, new, table, free_pages, free_used, page, max_tokens, out)
-    return out if out is not None else KvPlan._make(made)
+    handle, made = (_native or _binding()).plan(lens, new, table, free_pages, free_used, page, max_tokens, out)
+    plan = KvPlan._make(made) if out is None else out
+    if isinstance(plan, KvPlan):
+        plan._stream = handle
+    return plan
 
 
 # -------------------------------------------------------------------- cache

@@ -206,3 +206,31 @@ def test_workspaces_by_the_name_of_their_device(device):
     args = _small_call()
     assert torch.equal(tda.kv4_attend(*args, workspace=ws), tda.kv4_attend(*args))
     assert tda.kv4_workspace(device) is tda.kv4_workspace() and tda.kv4_workspaces(device) == tda.kv4_workspaces()
+
+
+# --------------------------------------------------------------------- plan
+
+@pytest.mark.parametrize("how", ["stream=", "current", "handle", "out"])
+def test_plan_check_waits_for_the_stream_of_the_plan(how):
+    """A refused plan on a busy stream that is not the current one when its check is called."""
+    tda = _tda()
+    s = torch.cuda.Stream()
+    lens, new, table, free, used = _i32([3]), _i32([40]), _i32([[5, -1]]), _i32([7, 8]), _i32([0])
+    args, kw = (lens, new, table, free, used), dict(page=16, max_tokens=64)
+    out = None
+    if how == "out":
+        out = tda.kv_plan(lens, _i32([1]), table, free, used, **kw)
+        out.check()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    if how == "current":
+        with torch.cuda.stream(s):
+            plan = tda.kv_plan(*args, **kw)
+    else:
+        plan = tda.kv_plan(*args, **kw, out=out, stream=s.cuda_stream if how == "handle" else s)
+    plan = plan._replace(lens=plan.lens)
+    with pytest.raises(tda.ArError) as e:
+        plan.check()
+    assert e.value.code == tda.ar.AR_ETOOBIG
+    assert isinstance(plan, tuple) and len(plan) == 7 and plan._fields[0] == "lens"
