@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) norm_rows_kernel(const ar
         const int at = i * blockDim.x + threadIdx.x;
         const float m = lanes ? top[i] : most;
         float scale = m * inv * (1.0f / 448.0f), q = __fdividef(448.0f, m);       // h * q: within 2 units of the last place of y / scale
-        if (!(m > 0x1p-60f && m < 0x1p100f)) {
-            // zeros, the ends of the range, infinities
+        if (!(m > 0x1p-60f && m < 0x1p100f && inv > 0)) {
+            // zeros, the ends of the range, infinities; rows whose sum of squares is infinite: y = 0
             scale = m * inv == 0 ? 1.0f : __fdiv_rn(m * inv, 448.0f);
             q = __fdiv_rn(inv, scale);
         }

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from tests import ops_helpers as H
-from tests.test_gpu_ops import _attend_case, _check_attend, _gen, _i32, _tda
+from tests.test_gpu_ops import _attend_case, _check_attend, _check_norm, _gen, _i32, _tda
 
 pytestmark = pytest.mark.gpu
 
@@ -234,3 +234,29 @@ def test_plan_check_waits_for_the_stream_of_the_plan(how):
         plan.check()
     assert e.value.code == tda.ar.AR_ETOOBIG
     assert isinstance(plan, tuple) and len(plan) == 7 and plan._fields[0] == "lens"
+
+
+# --------------------------------------------------------------------- norm
+
+def _shifted(x, shift):
+    """x on the GPU, its rows `shift` elements off 16 bytes (each shift takes another kernel)."""
+    room = torch.zeros(x.shape[0], x.shape[1] + 8, dtype=x.dtype, device="cuda")
+    view = room[:, shift:shift + x.shape[1]]
+    view.copy_(x)
+    return view
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("group", [0, 128])
+def test_norm_of_rows_whose_squares_overflow(group, shift):
+    """An infinity in the row, or finite values whose squares pass binary32: y is 0 (scale 1) wherever h is finite, and
+    NaN in the infinity's group."""
+    d = 1024
+    x = torch.randn(4, d, generator=_gen(1)).to(torch.bfloat16)
+    x[0, 9], x[1, 9], x[2, 9] = math.inf, -math.inf, 1e20
+    out, scales, _ = _tda().add_norm_fp8(_shifted(x, shift), torch.ones(d, dtype=torch.bfloat16, device="cuda"), group=group)
+    f = out.float().cpu()
+    assert (f[2] == 0).all() and (scales[2] == 1).all()
+    assert f[:2, :group or d].isnan().all() and scales[:2, 0].isnan().all()
+    assert (f[:2, group or d:] == 0).all() and (scales[:2, 1:] == 1).all()
+    _check_norm(x[3:], None, torch.ones(d, dtype=torch.bfloat16), 1e-6, group, out[3:], scales[3:], None)
