@@ -178,6 +178,7 @@ AR_API int ar_kv4_status(const void *workspace);
  * Per row: h = x + residual (binary32; residual NULL: h = x), y = h / sqrt(mean(h^2) +
  * eps) * weight; per group of `group` channels (0: the row; the last group may
  * be short): scale = max|y| / 448 (1 if that is 0), out = e4m3(y / scale).
+ * (A NaN is the largest: it is its group's scale, and out is NaN.)
  * A row whose sum of squares passes binary32 has y = 0 but where h is not finite; there y is NaN, and so are its
  * group's scale and out.
  * residual_out (may be residual or x themselves, by their strides; no other overlap): h rounded to dtype;

@@ -37,7 +37,9 @@ __device__ __forceinline__ float block_sum(float v, float *buf) {
 
 // The larger of two magnitudes; a NaN wins.
 __device__ __forceinline__ float top_of(float a, float b) {
-    return __uint_as_float(max(__float_as_uint(a) & 0x7fffffffu, __float_as_uint(b) & 0x7fffffffu));
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
 }
 
 // Vectors of 8 channels, V to a thread: vector i * blockDim.x + threadIdx.x.  Lanes: threads that share a
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) norm_rows_kernel(const ar
             sum = fmaf(v.y, v.y, sum);
             h[i][2 * e] = v.x * w2.x;
             h[i][2 * e + 1] = v.y * w2.y;
-            top[i] = fmaxf(top[i], fmaxf(fabsf(h[i][2 * e]), fabsf(h[i][2 * e + 1])));
+            top[i] = top_of(top[i], top_of(h[i][2 * e], h[i][2 * e + 1]));
         }
         const int at = i * blockDim.x + threadIdx.x;
         if (a.residual_out && at < vecs)
@@ -98,16 +100,16 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) norm_rows_kernel(const ar
     float most = 0;
     if (lanes == 0) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) most = fmaxf(most, top[i]);
+        for (int i = 0; i < V; ++i) most = top_of(most, top[i]);
     }
 #pragma unroll
     for (int d = 16; d; d /= 2) {
         sum += __shfl_xor_sync(~0u, sum, d);
         if (lanes == 0) {
-            most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
+            most = top_of(most, __shfl_xor_sync(~0u, most, d));
         } else if (d < lanes) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(~0u, top[i], d));
+            for (int i = 0; i < V; ++i) top[i] = top_of(top[i], __shfl_xor_sync(~0u, top[i], d));
         }
     }
     if (lane == 0) buf[warp] = make_float2(sum, most);
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) norm_rows_kernel(const ar
 #pragma unroll
     for (int d = 16; d; d /= 2) {
         sum += __shfl_xor_sync(~0u, sum, d);
-        most = fmaxf(most, __shfl_xor_sync(~0u, most, d));
+        most = top_of(most, __shfl_xor_sync(~0u, most, d));
     }
     const float inv = rsqrtf(__fdiv_rn(sum, (float)a.dim) + a.eps);
     uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + row * a.dim);

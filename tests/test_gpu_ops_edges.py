@@ -260,3 +260,19 @@ def test_norm_of_rows_whose_squares_overflow(group, shift):
     assert f[:2, :group or d].isnan().all() and scales[:2, 0].isnan().all()
     assert (f[:2, group or d:] == 0).all() and (scales[:2, 1:] == 1).all()
     _check_norm(x[3:], None, torch.ones(d, dtype=torch.bfloat16), 1e-6, group, out[3:], scales[3:], None)
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("d", [1024, 6144])
+def test_norm_with_a_nan_in_the_weight(d, group, shift):
+    """It spoils the scale and output of its own group, in every row, whichever kernel the rows take."""
+    x = torch.randn(3, d, generator=_gen(1)).to(torch.bfloat16)
+    w = torch.ones(d, dtype=torch.bfloat16)
+    w[d // 2 + 3] = math.nan
+    out, scales, _ = _tda().add_norm_fp8(_shifted(x, shift), w.cuda(), group=group)
+    n = group or d
+    bad = torch.arange(d) // n == (d // 2 + 3) // n
+    f = out.float().cpu()
+    assert f[:, bad].isnan().all() and not f[:, ~bad].isnan().any()
+    assert torch.equal(scales.cpu().isnan(), bad.view(1, -1, n)[..., 0].expand(3, -1))
