@@ -166,8 +166,8 @@ __device__ __forceinline__ uint32_t quantise(const uint32_t (&pairs)[N / 2], flo
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float f = rintf(__fdiv_rn(e ? v.y : v.x, s));
-                // fmax and fmin turn NaN into a bound, so NaN (and 0 / 0) is asked for first
-                const uint32_t n = (uint32_t)(f == f ? (int)fminf(fmaxf(f, -7.0f), 7.0f) + 8 : 8);
+                // fmax and fmin turn NaN into a bound, so NaN is asked for first; a scale that rounded to 0 has n = 0
+                const uint32_t n = (uint32_t)(f == f && s != 0 ? (int)fminf(fmaxf(f, -7.0f), 7.0f) + 8 : 8);
                 w = w >> 4 | n << (4 * N - 4);
             }
 #pragma unroll

@@ -276,3 +276,24 @@ def test_norm_with_a_nan_in_the_weight(d, group, shift):
     f = out.float().cpu()
     assert f[:, bad].isnan().all() and not f[:, ~bad].isnan().any()
     assert torch.equal(scales.cpu().isnan(), bad.view(1, -1, n)[..., 0].expand(3, -1))
+
+
+# -------------------------------------------------------------------- cache
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_append_of_groups_whose_scale_rounds_to_zero(D):
+    """max|x| / 7 of bfloat16 values below 4 x 2^-133 is no bfloat16 number but 0: n = 0, not a quotient by 0."""
+    tda = _tda()
+    rows = torch.zeros(5, 1, D, dtype=torch.bfloat16)
+    for i in range(5):
+        rows[i, 0, ::3], rows[i, 0, 1::3] = 2.0 ** -133 * i, -(2.0 ** -133) * i
+    pool = torch.full((1, 1, 1, 18 * D), 0xa5, dtype=torch.uint8, device="cuda")
+    slots = torch.arange(5, device="cuda")
+    tda.kv4_append(rows.cuda(), rows.flip(0).cuda(), pool, slots)
+    kn, ks, vn, vs = (x[0, 0, 0, :5] for x in H.unpack(pool.cpu()))
+    assert (kn[:4] == 0).all() and (ks[:4] == 0).all() and (vn[1:] == 0).all() and (vs[1:] == 0).all()
+    # 4 x 2^-133 / 7 rounds to 2^-133, and x / scale is 4
+    want = rows[4, 0].double() * 2.0 ** 133
+    assert (ks[4] == 2.0 ** -133).all() and torch.equal(kn[4], want) and torch.equal(vn[0], want)
+    k, v = tda.kv4_load(pool, slots)
+    assert (k[:4] == 0).all() and torch.equal(k[4], rows[4].cuda()) and torch.equal(v[0], rows[4].cuda())
