@@ -594,7 +594,11 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) y[ct][n][i] = exp2_approx(y[ct][n][i]);
+                for (int i = 0; i < 4; ++i) {
+                    // (what a row does not see is known by a negative zero from a weight too small to hold)
+                    const bool hidden = !Full && y[ct][n][i] == -INFINITY;
+                    y[ct][n][i] = hidden ? -0.0f : exp2_approx(y[ct][n][i]);
+                }
                 l[n][0] += y[ct][n][0] + y[ct][n][2];
                 l[n][1] += y[ct][n][1] + y[ct][n][3];
             }
@@ -612,7 +616,7 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
                     if constexpr (!Full) {
                         // a scale that a row does not see can be anything
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) p[i] = y[ct][n][i] == 0 ? 0 : p[i];
+                        for (int i = 0; i < 4; ++i) p[i] = __float_as_uint(y[ct][n][i]) == 0x80000000u ? 0 : p[i];
                     }
                     const uint32_t b0 = transpose8x8(pack_half(p[0], p[1])), b1 = transpose8x8(pack_half(p[2], p[3]));
                     mma16816(o[2 * j][n], a0, b0, b1);

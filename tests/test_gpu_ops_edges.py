@@ -81,6 +81,24 @@ def test_attend_large_channels_in_k(dtype, D, G, max_new):
     _check_attend(q, K, V, table, lens, cu, 0, 0, D ** -0.5, out, lse)
 
 
+@pytest.mark.parametrize("n,new,max_new", [(64, 1, 1), (50, 1, 1), (64, 1, 2), (50, 3, 3)])
+def test_attend_nan_in_v_under_a_vanishing_weight(n, new, max_new):
+    """A token whose weight is below binary32's smallest number still has its NaN seen, in a tile that some rows see
+    in part as in a whole one."""
+    tda = _tda()
+    D, page = 128, 16
+    q, pool, K, V, table, cu = _attend_case(67, 1, [n], [new], 1, 8, D, page, "f16")
+    kn, ks, vn, vs = H.unpack(pool)
+    q[:] = 1
+    pid = table[0][0]
+    kn[pid, 0, 0, 3], ks[pid, 0, 0, 3] = -7, 8.0      # a score of -7 x 8 x sqrt(128), -634
+    vs[pid, 0, 0, 3, 64:96] = math.nan
+    pool = H.pack(kn, ks[..., ::32].to(torch.bfloat16), vn, vs[..., ::32].to(torch.bfloat16))
+    out = tda.kv4_attend(q.cuda(), pool.cuda(), _i32(table), _i32([n]), _i32(cu), max_new=max_new)
+    assert out[:, :, 64:96].isnan().all()
+    assert not out[:, :, :64].isnan().any() and not out[:, :, 96:].isnan().any()
+
+
 # --------------------------------------------------------------- workspaces
 
 def test_a_workspace_is_ready_on_every_stream():
