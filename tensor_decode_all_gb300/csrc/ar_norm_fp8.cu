@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const ar_add_norm_fp
     }
     sum = block_sum(sum, buf);
     const float inv = rsqrtf(__fdiv_rn(sum, (float)a.dim) + a.eps);
-    const int group = a.group ? a.group : a.dim, groups = (a.dim + group - 1) / group;
+    const int group = a.group ? a.group : a.dim, groups = group ? (a.dim + group - 1) / group : 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (groups == 1) {
         float top = 0;
@@ -207,7 +207,7 @@ template <typename T>
 cudaError_t start(const ar_add_norm_fp8_args &a, cudaStream_t s) {
     // Threads that share a group of the vector kernel; -1: it cannot take the call.
     int lanes = -1;
-    if (a.dim % 8 == 0 && aligned16(a.x, a.x_stride) && aligned16(a.residual, a.residual_stride) && aligned16(a.weight, 0) &&
+    if (a.dim > 0 && a.dim % 8 == 0 && aligned16(a.x, a.x_stride) && aligned16(a.residual, a.residual_stride) && aligned16(a.weight, 0) &&
         aligned16(a.residual_out, a.residual_out_stride) && !misaligned(a.out, 8)) {
         if (a.group == 0 || a.group == a.dim) lanes = 0;
         else if (a.group == 8 || a.group == 16 || a.group == 32 || a.group == 64 || a.group == 128 || a.group == 256) lanes = a.group / 8;
@@ -242,8 +242,8 @@ extern "C" AR_API int ar_add_norm_fp8(const ar_add_norm_fp8_args *args, ar_strea
     if (a.dtype != AR_F16 && a.dtype != AR_BF16) return AR_EINVAL;
     if (a.rows < 0 || a.dim < 0 || a.group < 0 || a.group > a.dim || !(a.eps >= 0)) return AR_EINVAL;
     if (a.dim > kNormDim || a.rows > 0x7fffffff) return AR_ETOOBIG;
-    if (a.rows == 0 || a.dim == 0) return AR_OK;
-    if (!a.x || !a.weight || !a.out || !a.scales) return AR_EINVAL;
+    if (a.rows == 0) return AR_OK;
+    if (!a.scales || (a.dim > 0 && (!a.x || !a.weight || !a.out))) return AR_EINVAL;
     if (misaligned(a.x, 2) || misaligned(a.residual, 2) || misaligned(a.weight, 2) || misaligned(a.residual_out, 2) ||
         misaligned(a.scales, 4))
         return AR_EINVAL;

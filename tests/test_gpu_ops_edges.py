@@ -296,6 +296,15 @@ def test_norm_with_a_nan_in_the_weight(d, group, shift):
     assert torch.equal(scales.cpu().isnan(), bad.view(1, -1, n)[..., 0].expand(3, -1))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_norm_of_rows_without_channels(dtype):
+    """Their scale is 1, as of any row whose largest |y| is 0; it is written."""
+    x = torch.empty(5, 0, dtype=H.DT[dtype], device="cuda")
+    scales = torch.full((5, 1), 7.0, device="cuda")
+    out, same, _ = _tda().add_norm_fp8(x, x[0], scales=scales)
+    assert same is scales and (scales == 1).all() and out.shape == (5, 0)
+
+
 # -------------------------------------------------------------------- cache
 
 @pytest.mark.parametrize("D", [64, 128, 256])
