@@ -374,7 +374,7 @@ PyObject *norm(PyObject *const *o) {
         after = tensor("residual_out", o[7]);
         check("residual_out", after, dev, type, 2, false);
         check_shape("residual_out", after, x.sizes());
-    } else if (a.residual) {
+    } else if (o[2] != Py_None) {      // (an empty residual has no address)
         after = make(x.sizes(), type, x);
     }
     if (o[5] != Py_None) {

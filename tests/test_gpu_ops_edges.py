@@ -305,6 +305,15 @@ def test_norm_of_rows_without_channels(dtype):
     assert same is scales and (scales == 1).all() and out.shape == (5, 0)
 
 
+@pytest.mark.parametrize("shape", [(0, 64), (5, 0), (0, 0)])
+def test_norm_of_nothing_with_a_residual(shape):
+    """An empty step gives empty tensors, the sum with the residual among them."""
+    x = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(shape[1], dtype=torch.bfloat16, device="cuda")
+    out, scales, h = _tda().add_norm_fp8(x, w, residual=x)
+    assert out.shape == h.shape == shape and h.dtype == x.dtype and scales.shape == (shape[0], 1)
+
+
 # -------------------------------------------------------------------- cache
 
 @pytest.mark.parametrize("D", [64, 128, 256])
