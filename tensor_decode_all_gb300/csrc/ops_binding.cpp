@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/MemoryOverlap.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -79,6 +80,11 @@ void check(const char *what, const Tensor &t, int dev, at::ScalarType type, int6
     if (t.dim() != rank) refuse(what, std::to_string(t.dim()) + " dimensions, not " + std::to_string(rank));
     if (dense ? !t.is_contiguous() : t.size(-1) > 1 && t.stride(-1) != 1)
         refuse(what, dense ? "not contiguous" : "its last dimension is not contiguous");
+}
+
+// A tensor that is written by its strides: an expanded one has several writers to an element.
+void check_written(const char *what, const Tensor &t) {
+    if (at::has_internal_overlap(t) == at::MemOverlap::Yes) refuse(what, "its elements overlap (an expanded tensor?)");
 }
 
 void check_shape(const char *what, const Tensor &t, at::IntArrayRef shape) {
@@ -231,6 +237,10 @@ int rows(bool append, const Tensor &k, const Tensor &v, const Tensor &pool, cons
     check_shape("k", k, {n, dims.heads, dims.dim});
     check("v", v, dev, k.scalar_type(), 3, false);
     check_shape("v", v, {n, dims.heads, dims.dim});
+    if (!append) {
+        check_written("out", k);
+        check_written("out", v);
+    }
     ar_kv4_rows_args a = {};
     a.k = k.data_ptr(); a.v = v.data_ptr(); a.pool = pool.data_ptr(); a.slots = static_cast<int64_t *>(slots.data_ptr());
     a.k_token_stride = k.stride(0); a.k_head_stride = k.stride(1); a.v_token_stride = v.stride(0); a.v_head_stride = v.stride(1);
@@ -324,6 +334,7 @@ PyObject *attend(PyObject *const *o) {
         out = tensor("out", o[9]);
         check("out", out, dev, q.scalar_type(), 3, false);
         check_shape("out", out, q.sizes());
+        check_written("out", out);
     }
     if (o[10] != Py_None) {
         lse = tensor("lse", o[10]);
@@ -374,6 +385,7 @@ PyObject *norm(PyObject *const *o) {
         after = tensor("residual_out", o[7]);
         check("residual_out", after, dev, type, 2, false);
         check_shape("residual_out", after, x.sizes());
+        check_written("residual_out", after);
     } else if (o[2] != Py_None) {      // (an empty residual has no address)
         after = make(x.sizes(), type, x);
     }

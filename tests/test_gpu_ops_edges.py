@@ -333,3 +333,26 @@ def test_append_of_groups_whose_scale_rounds_to_zero(D):
     assert (ks[4] == 2.0 ** -133).all() and torch.equal(kn[4], want) and torch.equal(vn[0], want)
     k, v = tda.kv4_load(pool, slots)
     assert (k[:4] == 0).all() and torch.equal(k[4], rows[4].cuda()) and torch.equal(v[0], rows[4].cuda())
+
+
+# ----------------------------------------------------------------- refusals
+
+def test_written_tensors_whose_elements_overlap_are_refused():
+    """As everywhere in torch; read ones may be expanded."""
+    tda = _tda()
+    q, pool, table, lens = _small_call()
+    x = torch.ones(4, 64, dtype=torch.bfloat16, device="cuda")
+    slots = torch.arange(2, device="cuda")
+    k, v = tda.kv4_load(pool, slots)
+    bad = [lambda: tda.add_norm_fp8(x, x[0], residual_out=x[:1].expand(4, 64)),
+           lambda: tda.kv4_attend(q, pool, table, lens, out=torch.zeros_like(q[:1]).expand_as(q)),
+           lambda: tda.kv4_load(pool, slots, out=(k[:1].expand_as(k), v)),
+           lambda: tda.kv4_load(pool, slots, out=(k, v[:1].expand_as(v)))]
+    for f in bad:
+        with pytest.raises(ValueError, match="out: its elements overlap"):
+            f()
+    same = tda.add_norm_fp8(x, x[0], residual=x[:1].expand(4, 64))
+    assert (same[2] == 2).all()
+    tda.kv4_append(k[:1].expand_as(k), v[:1].expand_as(v), pool, slots)
+    again = tda.kv4_load(pool, slots)
+    assert torch.equal(again[0][1], again[0][0]) and torch.equal(again[1][1], again[1][0])
