@@ -69,7 +69,8 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) norm_rows_kernel(const ar
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int at = i * blockDim.x + threadIdx.x;
-        wv[i].v = at < vecs ? __ldg(static_cast<const uint4 *>(a.weight) + at) : make_uint4(0, 0, 0, 0);
+        // (an ordinary load: this kernel may have begun before the one that writes the weight has ended)
+        wv[i].v = at < vecs ? static_cast<const uint4 *>(a.weight)[at] : make_uint4(0, 0, 0, 0);
     }
     const int groups = lanes ? (vecs + lanes - 1) / lanes : 1;
     float h[V][8], top[V], sum = 0;

@@ -314,6 +314,23 @@ def test_norm_of_nothing_with_a_residual(shape):
     assert out.shape == h.shape == shape and h.dtype == x.dtype and scales.shape == (shape[0], 1)
 
 
+def test_norm_with_a_weight_from_the_call_before():
+    """A weight that the call before writes, again and again at the same place, in one row after another's reads."""
+    tda = _tda()
+    d = 2048
+    g = _gen(5)
+    x = torch.randn(300, d, generator=g).to(torch.bfloat16).cuda()
+    ws = [(1 + 0.2 * torch.randn(1, d, generator=g)).to(torch.bfloat16).cuda() for _ in range(40)]
+    want = [tda.add_norm_fp8(x, w[0])[0].view(torch.uint8) for w in ws]
+    zero, weight = torch.zeros(1, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, d, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    got = []
+    for w in ws:
+        tda.add_norm_fp8(w, w[0], residual=zero, residual_out=weight)
+        got.append(tda.add_norm_fp8(x, weight[0])[0])
+    assert all(torch.equal(a.view(torch.uint8), b) for a, b in zip(got, want))
+
+
 # -------------------------------------------------------------------- cache
 
 @pytest.mark.parametrize("D", [64, 128, 256])
