@@ -136,7 +136,7 @@ AR_API int ar_kv4_load(const ar_kv4_rows_args *args, ar_stream_t stream);
  * Its status (ar_kv4_status) says AR_EINVAL after a call that met a page id
  * outside the pool, a length past the table, or rows outside q in cu (the call
  * stays inside the buffers; outputs of such requests are undefined), and AR_ETIMEOUT
- * after a copy into shared memory that did not arrive.
+ * after a copy into shared memory that did not arrive (the call ends, its outputs are undefined).
  * Results do not depend on the order in which blocks run.
  * out must not overlap q (AR_EINVAL for the same address).
  * Errors: AR_EINVAL, AR_ETOOBIG (requests > 8192, tokens * query heads of a kv

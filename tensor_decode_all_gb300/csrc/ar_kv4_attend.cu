@@ -324,7 +324,6 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
     const uint32_t ring_addr = smem_addr(ring), bar_addr = smem_addr(&bars[warp * S]);
     const int tiles_page = a.page / kTileTokens;
     constexpr int kBatch = 32 / CT;
-    bool late = false;
     uint32_t filled = 0, used = 0;       // stages filled and used, over all segments
     int walked = 0;                      // segments walked to
     // Of the segment walked to last: its chunks and how many of them are sent.  Lane l has the address of tile
@@ -638,7 +637,13 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
 #pragma unroll 1
         while (next < end) {
             const uint32_t stage = used % S;
-            if (!late) late = !bar_wait(bar_addr + 8 * stage, (used / S) & 1, status);
+            if (__any_sync(~0u, !bar_wait(bar_addr + 8 * stage, (used / S) & 1, status))) {
+                // A copy that does not come: the warp waits for its others (with the same limit), so that none
+                // lands in a stage that is filled anew or after the block has gone, and leaves its share undone.
+#pragma unroll 1
+                for (uint32_t k = used; k != filled; ++k) (void)bar_wait(bar_addr + 8 * (k % S), (k / S) & 1, status);
+                return;
+            }
             const uint8_t *data = ring + stage * C::Stage;
             if (next < full0 || (next >= full1 && next < full2)) {
 #pragma unroll 1
