@@ -127,7 +127,8 @@ AR_API int ar_kv4_load(const ar_kv4_rows_args *args, ar_stream_t stream);
  * position p sees token j if 0 <= j <= p and (window == 0 or j > p - window or
  * j < sinks).  With s_j = scale * q . k_j over those tokens:
  *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = ln sum_j exp(s_j);
- * a row that sees no token gets out = 0 and lse = -infinity.
+ * a row that sees no token gets out = 0 and lse = -infinity.  Rows of no request (before cu[0], from cu[requests]
+ * on: all of them after a plan that was refused) are not written, so that calls may share out and lse by requests.
  * Products take fp16 operands (q scaled by a power of two of its row's so that
  * nothing is lost, K and V as the whole numbers they are, each exp(s_j) times
  * its V scale rounded once), sums and statistics are binary32, out is rounded once.

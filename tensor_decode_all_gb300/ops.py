@@ -289,6 +289,8 @@ def kv4_attend(q, pool, table, lens, cu=None, *, max_new=None, window=0, sinks=0
     [requests + 1]) request b's tokens are rows cu[b] .. cu[b + 1] - 1, and `max_new`, the most of
     any request (default: all of them), picks the kernel's shape.  `window` > 0 limits a token to
     the last `window` ones, itself included, and the first `sinks`.  `scale` defaults to head_dim ** -0.5.
+    Rows of no request (past cu[requests], as in a padded step) are not written: in an `out` that the call
+    makes they hold whatever the memory held.
     Returns `out`, or (out, lse) with `return_lse` or an `lse` (float32 [tokens, q_heads]) of the caller's.
     """
     if stream is not None:

@@ -99,6 +99,27 @@ def test_attend_nan_in_v_under_a_vanishing_weight(n, new, max_new):
     assert not out[:, :, :64].isnan().any() and not out[:, :, 96:].isnan().any()
 
 
+@pytest.mark.parametrize("D,G,max_new", [(128, 8, 1), (64, 8, 3)])
+def test_attend_leaves_rows_of_no_request_alone(D, G, max_new):
+    """Two calls that share q, out and lse, each over its part of the requests, with rows of padding behind both;
+    and a call after a refused plan, whose cu is all 0."""
+    tda = _tda()
+    lens, new, page = [70, 1, 333, 40], [3, 1, 2, 1], 16
+    q, pool, K, V, table, cu = _attend_case(83, 4, lens, new, 2, G, D, page, "bf16")
+    pad = 5
+    qd = torch.cat((q, torch.full((pad, *q.shape[1:]), math.nan, dtype=q.dtype))).cuda()
+    out, lse = torch.full_like(qd, 5.0), torch.full(qd.shape[:2], 5.0, device="cuda")
+    pd, td, ld, cd = pool.cuda(), _i32(table), _i32(lens), _i32(cu)
+    tda.kv4_attend(qd, pd, td, ld, torch.zeros_like(cd), max_new=max_new, out=out, lse=lse)
+    assert (out == 5).all() and (lse == 5).all()
+    tda.kv4_attend(qd, pd, td[2:], ld[2:], cd[2:], max_new=max_new, out=out, lse=lse)
+    assert (out[:4] == 5).all() and (lse[:4] == 5).all()
+    tda.kv4_attend(qd, pd, td[:2], ld[:2], cd[:3], max_new=max_new, out=out, lse=lse)
+    assert (out[-pad:] == 5).all() and (lse[-pad:] == 5).all()
+    _check_attend(q, K, V, table, lens, cu, 0, 0, D ** -0.5, out[:-pad], lse[:-pad])
+    tda.kv4_workspace().check()
+
+
 # --------------------------------------------------------------- workspaces
 
 def test_a_workspace_is_ready_on_every_stream():
