@@ -12,6 +12,9 @@ outputs allocated and arguments marshalled in the extension module beside it
 enqueued, codes of the library ``ArError``.  ``stream`` (a torch stream, a raw
 handle, or None for the current stream) is where the call is enqueued; what it
 returns without an ``out`` of the caller's is allocated for that stream.
+
+For serving only: nothing here has a gradient.  Tensors that require one are taken as data, and
+no result requires one, as under ``torch.no_grad()``.
 """
 from __future__ import annotations
 

@@ -394,3 +394,16 @@ def test_written_tensors_whose_elements_overlap_are_refused():
     tda.kv4_append(k[:1].expand_as(k), v[:1].expand_as(v), pool, slots)
     again = tda.kv4_load(pool, slots)
     assert torch.equal(again[0][1], again[0][0]) and torch.equal(again[1][1], again[1][0])
+
+
+def test_nothing_has_a_gradient():
+    """Tensors that require one (a module's parameters) are data, in grad mode too; the same bits come out."""
+    tda = _tda()
+    q, pool, table, lens = _small_call()
+    x, w = torch.randn(4, 64, device="cuda").to(torch.bfloat16), torch.nn.Parameter(torch.ones(64, dtype=torch.bfloat16, device="cuda"))
+    with torch.enable_grad():
+        got = tda.add_norm_fp8(x, w, residual=x.clone().requires_grad_())
+        out = tda.kv4_attend(q.clone().requires_grad_(), pool, table, lens)
+    want = tda.add_norm_fp8(x, w.detach(), residual=x)
+    assert all(not t.requires_grad for t in (*got, out))
+    assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(out, tda.kv4_attend(q, pool, table, lens))
