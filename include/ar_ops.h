@@ -133,7 +133,8 @@ AR_API int ar_kv4_load(const ar_kv4_rows_args *args, ar_stream_t stream);
  * nothing is lost, K and V as the whole numbers they are, each exp(s_j) times
  * its V scale rounded once), sums and statistics are binary32, out is rounded once.
  * workspace: ar_kv4_workspace_bytes() bytes, 256-byte aligned, made ready once
- * by ar_kv4_workspace_init; calls that may overlap on the GPU need one each.
+ * by ar_kv4_workspace_init; calls that may overlap on the GPU need one each, and so do host threads that may
+ * enqueue calls on one stream at the same time (a call is two launches, which must stay next to each other).
  * Its status (ar_kv4_status) says AR_EINVAL after a call that met a page id
  * outside the pool, a length past the table, or rows outside q in cu (the call
  * stays inside the buffers; outputs of such requests are undefined), and AR_ETIMEOUT
