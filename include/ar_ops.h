@@ -129,9 +129,12 @@ AR_API int ar_kv4_load(const ar_kv4_rows_args *args, ar_stream_t stream);
  *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = ln sum_j exp(s_j);
  * a row that sees no token gets out = 0 and lse = -infinity.  Rows of no request (before cu[0], from cu[requests]
  * on: all of them after a plan that was refused) are not written, so that calls may share out and lse by requests.
- * Products take fp16 operands (q scaled by a power of two of its row's so that
- * nothing is lost, K and V as the whole numbers they are, each exp(s_j) times
- * its V scale rounded once), sums and statistics are binary32, out is rounded once.
+ * Products take fp16 operands, sums and statistics are binary32, out is rounded once.  K and V enter as the whole
+ * numbers they are.  bfloat16 q enters divided by the power of two that takes its row's largest value to [1, 2):
+ * exact down to 2^-17 of that value, off by up to 2^-25 of it below.  Each exp(s_j) times its V scale is rounded
+ * once: to 11 bits, or, where it is small, to 2^-33 of the largest V scale that the request's rows see (at least
+ * 2^-80), so that groups of channels below 2^-22 of the largest have fewer.  Where V scales reach 2^k, k > 100, tokens
+ * whose exp(s_j) is below 2^(k - 134) of the largest count as 0.
  * workspace: ar_kv4_workspace_bytes() bytes, 256-byte aligned, made ready once
  * by ar_kv4_workspace_init; calls that may overlap on the GPU need one each, and so do host threads that may
  * enqueue calls on one stream at the same time (a call is two launches, which must stay next to each other).

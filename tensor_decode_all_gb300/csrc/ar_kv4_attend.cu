@@ -18,8 +18,8 @@
 //
 // Softmax runs in base 2 under a reference M per row, common to a warp, that moves only when a score passes it
 // by 2^6: p = 2^(s - M), and the usual step costs a vote in place of a reduction.  M also holds the exponent
-// of the largest V scale seen, so that a weight p * scale stays within fp16 with 2^-14 of it still a normal
-// number, whatever the scales.
+// of the largest V scale seen, so that a weight p * scale stays below fp16's largest number, and is a normal one
+// down to 2^-22 of the largest scale (a smaller one is off by 2^-33 of that, where the largest p is 1).
 //
 // Each warp reads its tokens on its own: a ring of stages in shared memory, filled by bulk copies (a tile is
 // 18 D contiguous bytes) a stage ahead, the next segment's first stages before the last one's results are
@@ -97,7 +97,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     return y;
 }
 
-// The 8 nibbles of w as fp16 pairs u - 8: nibbles (0, 4), (1, 5), (2, 6), (3, 7).
+// The 8 nibbles of w as fp16 pairs u - 8: nibbles (0, 4), (1, 5), (2, 6), (3, 7).  A whole number under the exponent
+// of 2^10 is 1024 + itself, so one logical instruction makes a pair and one exact operation takes the rest off
+// (Y. J. Kim, R. Henry, R. Fahim, H. H. Awadalla, "Who Says Elephants Can't Run: Bringing Large Scale MoE Models into
+// Cloud Scale Production", 2022).
 __device__ __forceinline__ void nibbles_to_half(uint32_t w, uint32_t (&h)[4]) {
     const uint32_t k1024 = 0x64006400u;
     const __half2 m1032 = __half2half2(__ushort_as_half(0xe408));   // -1032

@@ -81,6 +81,26 @@ def test_attend_large_channels_in_k(dtype, D, G, max_new):
     _check_attend(q, K, V, table, lens, cu, 0, 0, D ** -0.5, out, lse)
 
 
+@pytest.mark.parametrize("D,G,max_new", [(128, 8, 1), (64, 8, 2), (256, 4, 1)])
+@pytest.mark.parametrize("small", [10, 18, 26])
+def test_attend_small_channels_beside_large_ones(D, G, max_new, small):
+    """Groups of V at 2^-small of the others: a weight is off by 2^-11 of itself, or by 2^-33 of the largest scale where
+    it is small, so a channel by n x 7 of those at most, beside what the other bounds allow."""
+    tda = _tda()
+    lens, page = [400, 33, 3000], 16
+    q, pool, K, V, table, cu = _attend_case(89, 3, lens, [1] * 3, 1, G, D, page, "f16")
+    kn, ks, vn, vs = H.unpack(pool)
+    vs[..., 32:64] *= 2.0 ** -small
+    pool = H.pack(kn, ks[..., ::32].to(torch.bfloat16), vn, vs[..., ::32].to(torch.bfloat16))
+    V = (vn * vs).reshape(V.shape)
+    out, lse = tda.kv4_attend(q.cuda(), pool.cuda(), _i32(table), _i32(lens), max_new=max_new, return_lse=True)
+    want, wl, mag, big, _ = H.attend(q, K, V, table, lens, cu, 0, 0, D ** -0.5)
+    none = torch.zeros(want.shape[:2], dtype=torch.float64)
+    bound = H.attend_bounds(want, wl, mag, big, none, D ** -0.5, q.dtype, max(lens))[0]
+    bound += torch.tensor(lens).view(-1, 1, 1) * 7 * 2.0 ** -33 * vs.max()
+    assert ((out.cpu().double() - want).abs() <= bound).all()
+
+
 @pytest.mark.parametrize("n,new,max_new", [(64, 1, 1), (50, 1, 1), (64, 1, 2), (50, 3, 3)])
 def test_attend_nan_in_v_under_a_vanishing_weight(n, new, max_new):
     """A token whose weight is below binary32's smallest number still has its NaN seen, in a tile that some rows see
