@@ -1258,6 +1258,11 @@ def main():
         else:
             line = run_ours(args, dist)
         if line is not None and dist.rank == 0:
+            # The one line on stdout stays short enough for whoever reads it from a pipe or a log's tail (with the
+            # details of every workload it was 27 KB); they go to stderr, their summary stays.
+            details = line.pop("workloads", None)
+            if details is not None:
+                print(json.dumps({"workloads": details}), file=sys.stderr, flush=True)
             print(json.dumps(line), flush=True)
     finally:
         dist.close()
