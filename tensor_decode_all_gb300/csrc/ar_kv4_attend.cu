@@ -569,13 +569,15 @@ __global__ void __launch_bounds__(kWarps * 32, C::Blocks) attend_kernel(const __
                     for (int d = 4; d < 32; d *= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
                     // the reference never falls: a lower one would let earlier weights overflow
                     const float now = top > kNoScore ? fmaxf(ref[n][i], top + (float)(vexp - kHead)) : ref[n][i];
-                    const float keep = exp2_approx(ref[n][i] - now);
+                    // With V's exponent the reference can move by more than binary32 has exponents (V of zeros before
+                    // V of 2^60), while the sums, far from 1 themselves, stay within: so by the factor's root, twice.
+                    const float root = exp2_approx((ref[n][i] - now) * 0.5f);
                     ref[n][i] = now;
-                    l[n][i] *= keep;
+                    l[n][i] = l[n][i] * root * root;
 #pragma unroll
                     for (int m = 0; m < D / 16; ++m) {
-                        o[m][n][i] *= keep;
-                        o[m][n][i + 2] *= keep;
+                        o[m][n][i] = o[m][n][i] * root * root;
+                        o[m][n][i + 2] = o[m][n][i + 2] * root * root;
                     }
 #pragma unroll
                     for (int ct = 0; ct < CI; ++ct)
@@ -784,11 +786,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         float m = kNoScore, sum = 0;
         float4 v = make_float4(0, 0, 0, 0);
         auto add = [&](float2 ml, float4 y) {
-            const float m2 = fmaxf(m, ml.x), f0 = exp2_approx(m - m2), f1 = exp2_approx(ml.x - m2);
+            // (factors by their roots: the references can be further apart than binary32 has exponents, the sums not)
+            const float m2 = fmaxf(m, ml.x), f0 = exp2_approx((m - m2) * 0.5f), f1 = exp2_approx((ml.x - m2) * 0.5f);
             m = m2;
-            sum = fmaf(sum, f0, ml.y * f1);
-            v.x = fmaf(v.x, f0, y.x * f1); v.y = fmaf(v.y, f0, y.y * f1);
-            v.z = fmaf(v.z, f0, y.z * f1); v.w = fmaf(v.w, f0, y.w * f1);
+            sum = fmaf(sum * f0, f0, ml.y * f1 * f1);
+            v.x = fmaf(v.x * f0, f0, y.x * f1 * f1); v.y = fmaf(v.y * f0, f0, y.y * f1 * f1);
+            v.z = fmaf(v.z * f0, f0, y.z * f1 * f1); v.w = fmaf(v.w * f0, f0, y.w * f1 * f1);
         };
         constexpr int kAtOnce = 8;
         for (int k = group; k < r.parts; k += kAtOnce * Groups) {

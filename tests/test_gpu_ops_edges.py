@@ -140,6 +140,27 @@ def test_attend_leaves_rows_of_no_request_alone(D, G, max_new):
     tda.kv4_workspace().check()
 
 
+@pytest.mark.parametrize("D,G,max_new", [(128, 8, 1), (64, 8, 2), (256, 4, 1)])
+@pytest.mark.parametrize("n", [200, 20011])
+@pytest.mark.parametrize("small,large", [(0.0, 2.0 ** 13), (2.0 ** -60, 2.0 ** 20), (0.0, 2.0 ** 60), (2.0 ** -90, 2.0 ** 90)])
+def test_attend_v_of_zeros_before_large_v(D, G, max_new, n, small, large):
+    """Early tokens with V far below the later ones' keep their weights in the sum, also where the parts are joined."""
+    tda = _tda()
+    page = 64
+    q, pool, K, V, table, cu = _attend_case(97, 1, [n], [1], 1, G, D, page, "bf16")
+    kn, ks, vn, vs = H.unpack(pool)
+    tok = torch.zeros(pool.shape[0], page, dtype=torch.float64)
+    for i, pid in enumerate(table[0][:-(-n // page)]):
+        tok[pid] = torch.arange(page) + i * page
+    size = torch.where(tok < n // 2 + 5, small, large).view(pool.shape[0], 1, page // 16, 16, 1)
+    vs = vs * size
+    pool = H.pack(kn, ks[..., ::32].to(torch.bfloat16), vn, vs[..., ::32].to(torch.bfloat16))
+    kn, ks, vn, vs = H.unpack(pool)
+    V = (vn * vs).reshape(V.shape)
+    out, lse = tda.kv4_attend(q.cuda(), pool.cuda(), _i32(table), _i32([n]), max_new=max_new, return_lse=True)
+    _check_attend(q, K, V, table, [n], cu, 0, 0, D ** -0.5, out, lse)
+
+
 # --------------------------------------------------------------- workspaces
 
 def test_a_workspace_is_ready_on_every_stream():
