@@ -785,15 +785,27 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         const int col = i / Quads, quad = i % Quads;
         float m = kNoScore, sum = 0;
         float4 v = make_float4(0, 0, 0, 0);
-        auto add = [&](float2 ml, float4 y) {
-            // (factors by their roots: the references can be further apart than binary32 has exponents, the sums not)
-            const float m2 = fmaxf(m, ml.x), f0 = exp2_approx((m - m2) * 0.5f), f1 = exp2_approx((ml.x - m2) * 0.5f);
-            m = m2;
-            sum = fmaf(sum * f0, f0, ml.y * f1 * f1);
-            v.x = fmaf(v.x * f0, f0, y.x * f1 * f1); v.y = fmaf(v.y * f0, f0, y.y * f1 * f1);
-            v.z = fmaf(v.z * f0, f0, y.z * f1 * f1); v.w = fmaf(v.w * f0, f0, y.w * f1 * f1);
-        };
         constexpr int kAtOnce = 8;
+        // The first `count` parts under one reference.  Factors by their roots, twice: the references can be further
+        // apart than binary32 has exponents, the sums not.
+        auto add = [&](const float2 (&ml)[kAtOnce], const float4 (&y)[kAtOnce], int count) {
+            float m2 = m;
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e)
+                if (e < count) m2 = fmaxf(m2, ml[e].x);
+            const float r0 = exp2_approx((m - m2) * 0.5f);
+            m = m2;
+            sum = sum * r0 * r0;
+            v.x = v.x * r0 * r0; v.y = v.y * r0 * r0; v.z = v.z * r0 * r0; v.w = v.w * r0 * r0;
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e) {
+                if (e >= count) break;
+                const float r = exp2_approx((ml[e].x - m2) * 0.5f);
+                sum = fmaf(ml[e].y * r, r, sum);
+                v.x = fmaf(y[e].x * r, r, v.x); v.y = fmaf(y[e].y * r, r, v.y);
+                v.z = fmaf(y[e].z * r, r, v.z); v.w = fmaf(y[e].w * r, r, v.w);
+            }
+        };
         for (int k = group; k < r.parts; k += kAtOnce * Groups) {
             float2 ml[kAtOnce];
             float4 y[kAtOnce];
@@ -806,9 +818,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
                     y[e] = __ldcg(reinterpret_cast<const float4 *>(p + col * D + 4 * quad));
                 }
             }
-#pragma unroll
-            for (int e = 0; e < kAtOnce; ++e)
-                if (k + e * Groups < r.parts) add(ml[e], y[e]);
+            add(ml, y, (r.parts - k + Groups - 1) / Groups);
         }
         if constexpr (Spread) {
             rows[group][quad] = v;
@@ -816,7 +826,18 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
             __syncthreads();
             if (group > 0) return;
 #pragma unroll
-            for (int k = 1; k < Groups; ++k) add(facts[k], rows[k][quad]);
+            for (int k = 1; k < Groups; k += kAtOnce) {
+                float2 ml[kAtOnce];
+                float4 y[kAtOnce];
+#pragma unroll
+                for (int e = 0; e < kAtOnce; ++e) {
+                    if (k + e < Groups) {
+                        ml[e] = facts[k + e];
+                        y[e] = rows[k + e][quad];
+                    }
+                }
+                add(ml, y, Groups - k);
+            }
         }
         const int row = r.row0 + col;
         store_row<T>(c, (long long)r.first + row / c.group, r.kv * c.group + row % c.group, 4 * quad, v, m, sum);
