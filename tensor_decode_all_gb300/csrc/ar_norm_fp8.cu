@@ -42,6 +42,13 @@ __device__ __forceinline__ float top_of(float a, float b) {
     return r;
 }
 
+// The same of a (0 or more already) and two others.
+__device__ __forceinline__ float top_of(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+    return r;
+}
+
 // Vectors of 8 channels, V to a thread: vector i * blockDim.x + threadIdx.x.  Lanes: threads that share a
 // group (a power of two up to 32; 0: the row is one group).
 template <typename T, int V>
@@ -92,7 +99,7 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) norm_rows_kernel(const ar
             sum = fmaf(v.y, v.y, sum);
             h[i][2 * e] = v.x * w2.x;
             h[i][2 * e + 1] = v.y * w2.y;
-            top[i] = top_of(top[i], top_of(h[i][2 * e], h[i][2 * e + 1]));
+            top[i] = top_of(top[i], h[i][2 * e], h[i][2 * e + 1]);
         }
         const int at = i * blockDim.x + threadIdx.x;
         if (a.residual_out && at < vecs)
