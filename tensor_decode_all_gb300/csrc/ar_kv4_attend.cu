@@ -11,8 +11,8 @@
 // instruction.  (tcgen05 has 64 rows at least, and wants its operands in shared memory: each nibble would be
 // written there at four times its size and read once.)  K and V enter as the whole numbers u - 8 that they are: a
 // nibble u in the mantissa of a power of two is that power plus u, and one exact instruction to a pair takes the
-// rest off.  (Taking K's out of the sums instead, by where the accumulators start, saves that instruction and
-// loses bits, up to 8 where most of a group is 0, and the product of an infinite scale with a sum that is 0.)  K's
+// rest off.  (Taking K's out of the sums instead, by where the accumulators start, loses bits, up to 8 where most
+// of a group is 0, and the product of an infinite scale with a sum that is 0; it was not faster: 69 us for 68.)  K's
 // scales multiply the sums of each group of 32 channels, V's the weights, both in binary32; weight x scale is
 // rounded once, to fp16.
 //
@@ -25,12 +25,12 @@
 // 18 D contiguous bytes) a stage ahead, the next segment's first stages before the last one's results are
 // written.
 //
-// Measured on a GB300 (graph replays): 64 requests of 16385 to 32768 tokens, 8 kv heads of 8, D 128: 308 us,
-// 5.9 TB/s of cache or 87% of what a plain copy reaches; 64 ragged ones of 517 to 8001: 69 us, 67%; 128 ragged
-// with a window of 1024 and D 64: 32 us; one of 1003 tokens and one kv head: 9.6 us.  The short ones are bound
-// by the instructions they issue: 308 for a tile of 16 tokens and one head of 128, 0.56 a cycle and scheduler,
-// two of five on the ALU pipe, which takes one every other cycle; DRAM carries 1.006 times the bytes that have
-// to be read, and the matrix instructions take a quarter of the time.  12 warps a multiprocessor: 16 with 126
+// Measured on a GB300 (graph replays): 64 requests of 16385 to 32768 tokens, 8 kv heads of 8, D 128: 306 us,
+// 6.0 TB/s of cache or 88% of what a plain copy reaches; 64 ragged ones of 517 to 8001: 68 us, 69%; 128 ragged
+// with a window of 1024 and D 64: 32 us; one of 1003 tokens and one kv head: 9.7 us.  The short ones are bound
+// by the instructions they issue: 318 for a tile of 16 tokens and one head of 128, 0.60 a cycle and scheduler,
+// two of five on the ALU pipe, which takes one every other cycle; DRAM carries the bytes that have to be read
+// and no more, and the matrix instructions take a quarter of the time.  12 warps a multiprocessor: 16 with 126
 // registers each were 12% slower.
 #include "ar_kv4.cuh"
 

@@ -5,7 +5,7 @@
 //
 // A warp takes 8 tokens of one head, K or V, its lanes as the tile's words lie, so that a run of tokens is
 // read and written in whole lines.  Measured on a GB300 (graph replays): 8191 tokens of 8 heads of 128, append
-// 14.5 us (43 MB), load 8.8; 64 tokens 3.2 and 2.6 us.  Bound by the rounding's instructions (0.64 a cycle and
+// 14.5 us (43 MB), load 8.7; 64 tokens 3.0 and 2.5 us.  Bound by the rounding's instructions (0.64 a cycle and
 // scheduler), not by its 6.3 us of memory: with a division to a value 32.6 us, with a scale made by every lane
 // 16.9.
 #include "ar_kv4.cuh"

@@ -6,8 +6,8 @@
 // cluster, whose barrier stands between the reads of lens and *free_used and their writes, so that both may be
 // updated in place.
 //
-// Bound by latency: 64 requests of a token each take 4.9 us on a GB300, 1000 requests with 23524 new tokens
-// 9.1 (graph replays; the second writes 0.4 MB).
+// Bound by latency: 64 requests of a token each take 4.8 us on a GB300, 1000 requests with 23524 new tokens
+// 9.0 (graph replays; the second writes 0.4 MB).
 #include "ar_kv4.cuh"
 
 namespace {

@@ -6,8 +6,8 @@
 // come out of one round through shared memory, and no value is read or computed twice.
 //
 // Bound by memory: 7 bytes an element (x, residual, h and the e4m3 output).  In
-// GB300 graph replays 8192 rows of 8192 take 70.6 us, 6.66 TB/s or 98% of what a plain
-// copy reaches; 8192 of 5120 with groups of 128 45.9 us, 6.4 TB/s; 8 rows of 8192 2.0 us.
+// GB300 graph replays 8192 rows of 8192 take 70.0 us, 6.7 TB/s or 99% of what a plain
+// copy reaches; 8192 of 5120 with groups of 128 45.9 us, 6.4 TB/s; 8 rows of 8192 2.1 us.
 // A block that went from row to row with the next row's loads ahead needed
 // 85 registers and was slower (82.9 us, or spilled); many short blocks do the same overlap.
 // Rows that do not lie on 16 bytes and groups that a warp's lanes do not divide take a
