@@ -139,8 +139,8 @@ def lib():
 
 
 def declared_symbols(header: str | None = None):
-    """Names of the entry points include/ar.h and ar_ops.h declare (or the given header)."""
-    headers = [header] if header else [os.path.join(_build.INCLUDE, f) for f in ("ar.h", "ar_ops.h")]
+    """Names of the entry points include/ar.h, ar_ops.h and ar_ffn.h declare (or the given header)."""
+    headers = [header] if header else [os.path.join(_build.INCLUDE, f) for f in ("ar.h", "ar_ops.h", "ar_ffn.h")]
     text = "".join(open(h).read() for h in headers)
     return sorted(set(re.findall(r"AR_API\s+[^;(]*?\b(ar_\w+)\s*\(", text)))
 

@@ -1,0 +1,123 @@
+// ar_matmul_fp8.cu -- ar_matmul_fp8: the checks of a call, the choice of its kernel, and the kernel that takes any alignment.
+#include <cuda_fp8.h>
+
+#include "ar_matmul_fp8.cuh"
+
+namespace {
+
+using namespace tda;
+
+// ---------------------------------------------------- rows of any alignment
+//
+// Tiles of 64 rows and 64 features, 4 warps.  Bytes go through registers to shared memory as fp16 (which holds every
+// e4m3 value), the products are mma.sync's: rows that are not on 16 bytes cannot be moved by bulk copies, and
+// no weight that is kept for its speed is laid out like that.
+
+constexpr int kSide = 64, kPitch = kBlock + 8;   // (8 more halves to a row: no two of a fragment's rows share banks)
+
+__device__ __forceinline__ void load_tile(__half (*to)[kPitch], const uint8_t *from, int k, int dim, bool there) {
+    // one row to two threads, 64 channels each
+    const int row = threadIdx.x >> 1, c0 = (threadIdx.x & 1) * 64;
+    for (int i = 0; i < 64; i += 2) {
+        const int c = k + c0 + i;
+        const uint32_t lo = there && c < dim ? from[c] : 0, hi = there && c + 1 < dim ? from[c + 1] : 0;
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(lo | hi << 8), __NV_E4M3);
+        *reinterpret_cast<__half2_raw *>(&to[row][c0 + i]) = h;
+    }
+}
+
+__global__ void __launch_bounds__(128) any_rows_kernel(const Product p) {
+    after_the_stream();
+    __shared__ __half xs[kSide][kPitch], ws[kSide][kPitch];
+    const ar_matmul_fp8_args &a = p.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const Rows rows = rows_of_tile(a, blockIdx.x, kSide);
+    if (rows.count == 0) return;
+    const int feature = blockIdx.y * kSide;
+    const uint8_t *x = static_cast<const uint8_t *>(a.x), *w = static_cast<const uint8_t *>(a.weight) + rows.expert * a.expert_stride;
+    const int mine = threadIdx.x >> 1;
+    const int64_t from = mine < rows.count ? source_row(a, rows.first + mine) : -1;
+    int64_t source[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = warp * 16 + g + 8 * h;
+        source[h] = r < rows.count ? source_row(a, rows.first + r) : -1;
+    }
+    const float *scale_w = a.weight_scales + ((int64_t)rows.expert * ((a.out_dim + kBlock - 1) / kBlock) + feature / kBlock) * p.groups;
+    float acc[8][4] = {};
+    for (int k = 0; k < p.groups; ++k) {
+        load_tile(xs, x + max(from, (int64_t)0) * a.x_stride, k * kBlock, a.dim, from >= 0);
+        load_tile(ws, w + (int64_t)(feature + mine) * a.weight_stride, k * kBlock, a.dim, feature + mine < a.out_dim);
+        __syncthreads();
+        float part[8][4] = {};
+#pragma unroll
+        for (int s = 0; s < kBlock; s += 16) {
+            uint32_t f[4];
+            const int r = warp * 16 + g;
+            f[0] = *reinterpret_cast<uint32_t *>(&xs[r][s + 2 * t]);
+            f[1] = *reinterpret_cast<uint32_t *>(&xs[r + 8][s + 2 * t]);
+            f[2] = *reinterpret_cast<uint32_t *>(&xs[r][s + 2 * t + 8]);
+            f[3] = *reinterpret_cast<uint32_t *>(&xs[r + 8][s + 2 * t + 8]);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const uint32_t b0 = *reinterpret_cast<uint32_t *>(&ws[n * 8 + g][s + 2 * t]), b1 = *reinterpret_cast<uint32_t *>(&ws[n * 8 + g][s + 2 * t + 8]);
+                asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                             : "+f"(part[n][0]), "+f"(part[n][1]), "+f"(part[n][2]), "+f"(part[n][3])
+                             : "r"(f[0]), "r"(f[1]), "r"(f[2]), "r"(f[3]), "r"(b0), "r"(b1));
+            }
+        }
+        const float sw = scale_w[k];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float s = source[h] >= 0 ? a.x_scales[source[h] * a.x_scales_stride + (a.x_row_scales ? 0 : k)] * sw : 0.0f;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                acc[n][2 * h] = fmaf(part[n][2 * h], s, acc[n][2 * h]);
+                acc[n][2 * h + 1] = fmaf(part[n][2 * h + 1], s, acc[n][2 * h + 1]);
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = warp * 16 + g + 8 * h;
+        if (r >= rows.count) continue;
+        const int64_t at = (rows.first + r) * a.out_stride;
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+            for (int e = 0; e < 2; ++e) {
+                const int c = feature + n * 8 + 2 * t + e;
+                if (c >= a.out_dim) continue;
+                const float v = source[h] >= 0 ? acc[n][2 * h + e] : 0.0f;
+                if (a.dtype == AR_F16) static_cast<__half *>(a.out)[at + c] = __float2half_rn(v);
+                else static_cast<__nv_bfloat16 *>(a.out)[at + c] = __float2bfloat16_rn(v);
+            }
+    }
+}
+
+cudaError_t start_any(const Product &p, cudaStream_t s) {
+    const int64_t tiles = most_tiles(p.a, kSide);
+    return launch_next(any_rows_kernel, dim3((unsigned)tiles, (unsigned)((p.a.out_dim + kSide - 1) / kSide)), 128, 0, s, 0, p);
+}
+
+}  // namespace
+
+extern "C" AR_API int ar_matmul_fp8(const ar_matmul_fp8_args *args, ar_stream_t stream) {
+    if (!args) return AR_EINVAL;
+    const ar_matmul_fp8_args &a = *args;
+    if (a.dtype != AR_F16 && a.dtype != AR_BF16) return AR_EINVAL;
+    if (a.rows < 0 || a.x_rows < 0 || a.out_dim < 0 || a.dim < 0 || a.experts < 1 || (a.x_row_scales & ~1)) return AR_EINVAL;
+    if ((!a.offsets && a.experts != 1) || (!a.row_of && a.x_rows != a.rows)) return AR_EINVAL;
+    constexpr int64_t most = 1 << 30;
+    if (a.rows > most || a.x_rows > most || a.dim > 1 << 20 || a.out_dim > 1 << 20 || a.experts > 1024) return AR_ETOOBIG;
+    if (a.rows == 0 || a.out_dim == 0) return AR_OK;
+    if (!a.out || (a.dim > 0 && (!a.weight || !a.weight_scales || (a.x_rows > 0 && (!a.x || !a.x_scales))))) return AR_EINVAL;
+    if (misaligned(a.x_scales, 4) || misaligned(a.weight_scales, 4) || misaligned(a.out, 2) || misaligned(a.offsets, 4) || misaligned(a.row_of, 4))
+        return AR_EINVAL;
+    Product p;
+    p.a = a;
+    p.groups = (a.dim + kBlock - 1) / kBlock;
+    return launch_status(start_any(p, stream));
+}
+
+extern "C" AR_API int ar_matmul_fp8_status(void) { return AR_OK; }

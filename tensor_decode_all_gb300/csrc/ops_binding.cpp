@@ -1,8 +1,8 @@
-// ops_binding.cpp -- Python binding of include/ar_ops.h as an extension module.
+// ops_binding.cpp -- Python binding of include/ar_ops.h and ar_ffn.h as an extension module.
 //
 // What ctypes does for the rest of the library costs a call of these small
 // operators more than their kernels run, so their tensors are checked, their outputs
-// allocated and their arguments marshalled here.  ops.py holds the public
+// allocated and their arguments marshalled here.  ops.py and ffn.py hold the public
 // functions, with the defaults and the documentation.
 #include <Python.h>
 
@@ -16,6 +16,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <exception>
 #include <initializer_list>
@@ -24,6 +25,7 @@
 #include <utility>
 #include <vector>
 
+#include "ar_ffn.h"
 #include "ar_ops.h"
 
 namespace {
@@ -415,6 +417,199 @@ PyObject *norm(PyObject *const *o) {
     return tuple_of({&out, &scales, after.defined() ? &after : nullptr});
 }
 
+// ------------------------------------------------- operators of ar_ffn.h
+
+// The type that a call's `dtype` asks for.
+at::ScalarType type_16(const char *what, PyObject *o) {
+    if (o == Py_None) return at::kBFloat16;
+    if (!THPDtype_Check(o)) refuse(what, "not a torch.dtype");
+    const at::ScalarType type = reinterpret_cast<THPDtype *>(o)->scalar_type;
+    if (type != at::kHalf && type != at::kBFloat16) refuse(what, name_of(type) + " is neither float16 nor bfloat16");
+    return type;
+}
+
+// Whether two tensors that are laid out in rows can have a byte in common.
+bool may_share(const Tensor &a, const Tensor &b) {
+    auto range = [](const Tensor &t) {
+        int64_t last = 0;
+        for (int64_t i = 0; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
+        const char *p = static_cast<const char *>(t.data_ptr());
+        return std::pair<const char *, const char *>(p, p + (last + 1) * (int64_t)t.element_size());
+    };
+    if (a.numel() == 0 || b.numel() == 0) return false;
+    const auto x = range(a), y = range(b);
+    return x.first < y.second && y.first < x.second;
+}
+
+// matmul(x, x_scales, weight, weight_scales, offsets | None, rows | None, out | None, dtype | None) -> out
+PyObject *matmul(PyObject *const *o) {
+    const Tensor &x = tensor("x", o[0]), &xs = tensor("x_scales", o[1]), &w = tensor("weight", o[2]), &ws = tensor("weight_scales", o[3]);
+    const int dev = device_of("x", x);
+    const bool experts = o[4] != Py_None;
+    check("x", x, dev, at::kFloat8_e4m3fn, 2, false);
+    const int64_t N = x.size(0), K = x.size(1), groups = (K + 127) / 128, lead = experts ? 1 : 0;
+    check("weight", w, dev, at::kFloat8_e4m3fn, 2 + lead, false);
+    const int64_t F = w.size(lead), E = experts ? w.size(0) : 1, blocks = (F + 127) / 128;
+    if (w.size(lead + 1) != K) refuse("weight", std::to_string(w.size(lead + 1)) + " channels, x has " + std::to_string(K));
+    check("x_scales", xs, dev, at::kFloat, 2, false);
+    const bool row_scales = xs.size(1) == 1 && groups != 1;
+    if (xs.size(0) != N || (xs.size(1) != groups && !row_scales))
+        refuse("x_scales", "shape " + name_of(xs.sizes()) + " is neither " + name_of({N, groups}) + " nor " + name_of({N, 1}));
+    check("weight_scales", ws, dev, at::kFloat, 2 + lead, true);
+    if (experts) check_shape("weight_scales", ws, {E, blocks, groups});
+    else check_shape("weight_scales", ws, {blocks, groups});
+    ar_matmul_fp8_args a = {};
+    int64_t rows = N;
+    if (experts) {
+        const Tensor &offsets = tensor("offsets", o[4]);
+        check("offsets", offsets, dev, at::kInt, 1, true);
+        check_shape("offsets", offsets, {E + 1});
+        if (E < 1) refuse("weight", "no experts");
+        a.offsets = static_cast<int32_t *>(offsets.data_ptr());
+    }
+    if (o[5] != Py_None) {
+        const Tensor &of = tensor("rows", o[5]);
+        check("rows", of, dev, at::kInt, 1, true);
+        rows = of.size(0);
+        a.row_of = static_cast<int32_t *>(of.data_ptr());
+    }
+    Tensor out;
+    if (o[6] == Py_None) {
+        out = make({rows, F}, type_16("dtype", o[7]), x);
+    } else {
+        out = tensor("out", o[6]);
+        check("out", out, dev, kAny, 2, false);
+        (void)code_16("out", out);
+        if (o[7] != Py_None && out.scalar_type() != type_16("dtype", o[7]))
+            refuse("out", "dtype " + name_of(out.scalar_type()) + ", not " + name_of(type_16("dtype", o[7])));
+        check_shape("out", out, {rows, F});
+        check_written("out", out);
+        if (may_share(out, x) || may_share(out, xs) || may_share(out, w) || may_share(out, ws)) refuse("out", "overlaps an input");
+    }
+    if (K > kInt || F > kInt) refuse("weight", "too large");
+    a.x = x.data_ptr(); a.x_scales = static_cast<float *>(xs.data_ptr()); a.weight = w.data_ptr();
+    a.weight_scales = static_cast<float *>(ws.data_ptr()); a.out = out.data_ptr();
+    a.x_stride = x.stride(0); a.x_scales_stride = xs.stride(0); a.weight_stride = w.stride(lead); a.expert_stride = experts ? w.stride(0) : 0;
+    a.out_stride = out.stride(0); a.rows = rows; a.x_rows = N; a.dtype = code_16("out", out); a.out_dim = (int32_t)F; a.dim = (int32_t)K;
+    a.experts = (int32_t)std::min(E, kInt); a.x_row_scales = row_scales;
+    const int rc = ar_matmul_fp8(&a, stream_of(dev));
+    if (rc) return fail(rc, "ar_matmul_fp8");
+    return o[6] != Py_None ? (Py_INCREF(o[6]), o[6]) : THPVariable_Wrap(out);
+}
+
+// route(logits, k, normalize, out | None) -> (weights, experts, offsets, rows, place) or out
+PyObject *route(PyObject *const *o) {
+    const Tensor &logits = tensor("logits", o[0]);
+    const int dev = device_of("logits", logits);
+    check("logits", logits, dev, kAny, 2, false);
+    const at::ScalarType type = logits.scalar_type();
+    if (type != at::kFloat && type != at::kHalf && type != at::kBFloat16) refuse("logits", "dtype " + name_of(type) + " is none of float32, float16 and bfloat16");
+    const int64_t T = logits.size(0), E = logits.size(1);
+    if (E < 1) refuse("logits", "no experts");
+    const int64_t k = whole("k", o[1], 1, E);
+    const int normalize = PyObject_IsTrue(o[2]);
+    if (normalize < 0) return nullptr;
+    if (T > (int64_t(1) << 30) / k) return fail(AR_ETOOBIG, "ar_route_experts");
+    static const char *const names[5] = {"out.weights", "out.experts", "out.offsets", "out.rows", "out.place"};
+    Tensor out[5], room;
+    if (o[3] != Py_None && (!PyTuple_Check(o[3]) || PyTuple_GET_SIZE(o[3]) != 5)) refuse("out", "not Routes");
+    const int64_t n = T * k, sizes[5] = {n, n, E + 1, n, n};
+    if (o[3] == Py_None) room = make({4 * n + E + 1}, at::kInt, logits);
+    int64_t at = 0;
+    for (int i = 0; i < 5; ++i) {
+        const at::ScalarType t = i == 0 ? at::kFloat : at::kInt;
+        const bool pairs = i == 0 || i == 1 || i == 4;
+        if (o[3] == Py_None) {
+            out[i] = part_of(room, t, 4 * at, sizes[i]);
+            if (pairs) out[i].unsafeGetTensorImpl()->set_sizes_contiguous({T, k});
+            at += sizes[i];
+        } else {
+            out[i] = tensor(names[i], PyTuple_GET_ITEM(o[3], i));
+            check(names[i], out[i], dev, t, pairs ? 2 : 1, true);
+            if (pairs) check_shape(names[i], out[i], {T, k});
+            else check_shape(names[i], out[i], {sizes[i]});
+            for (int j = 0; j < i; ++j)
+                if (may_share(out[i], out[j])) refuse(names[i], std::string("overlaps ") + names[j]);
+            if (may_share(out[i], logits)) refuse(names[i], "overlaps logits");
+        }
+    }
+    ar_route_experts_args a = {};
+    auto p = [](const Tensor &t) { return static_cast<int32_t *>(t.data_ptr()); };
+    a.logits = logits.data_ptr(); a.weights = static_cast<float *>(out[0].data_ptr()); a.expert_ids = p(out[1]); a.offsets = p(out[2]);
+    a.rows = p(out[3]); a.place = p(out[4]); a.logits_stride = logits.stride(0); a.tokens = T;
+    a.dtype = type == at::kFloat ? AR_F32 : code_16("logits", logits); a.experts = (int32_t)std::min(E, kInt); a.chosen = (int32_t)k; a.normalize = normalize;
+    const int rc = ar_route_experts(&a, stream_of(dev));
+    if (rc) return fail(rc, "ar_route_experts");
+    return o[3] != Py_None ? (Py_INCREF(o[3]), o[3]) : tuple_of({&out[0], &out[1], &out[2], &out[3], &out[4]});
+}
+
+// silu(x, group, out | None, scales | None) -> (out, scales)
+PyObject *silu(PyObject *const *o) {
+    const Tensor &x = tensor("x", o[0]);
+    const int dev = device_of("x", x);
+    check("x", x, dev, kAny, 2, false);
+    const int code = code_16("x", x);
+    const int64_t N = x.size(0), d = x.size(1) / 2;
+    if (x.size(1) % 2) refuse("x", std::to_string(x.size(1)) + " channels are not gates and as many factors");
+    if (d > kInt) refuse("x", "rows too long");
+    const int64_t group = whole("group", o[1], 0, kInt);
+    // (a group of 128 is the default, and the whole row where that is shorter)
+    const int64_t used = std::min(group, d), groups = used ? (d + used - 1) / used : 1;
+    Tensor out, scales;
+    if (o[2] != Py_None) {
+        out = tensor("out", o[2]);
+        check("out", out, dev, at::kFloat8_e4m3fn, 2, true);
+        check_shape("out", out, {N, d});
+        if (may_share(out, x)) refuse("out", "overlaps x");
+    } else {
+        out = make({N, d}, at::kFloat8_e4m3fn, x);
+    }
+    if (o[3] != Py_None) {
+        scales = tensor("scales", o[3]);
+        check("scales", scales, dev, at::kFloat, 2, true);
+        check_shape("scales", scales, {N, groups});
+        if (may_share(scales, x)) refuse("scales", "overlaps x");
+        if (may_share(scales, out)) refuse("scales", "overlaps out");
+    } else {
+        scales = make({N, groups}, at::kFloat, x);
+    }
+    ar_silu_mul_fp8_args a = {};
+    a.x = x.data_ptr(); a.out = out.data_ptr(); a.scales = static_cast<float *>(scales.data_ptr()); a.x_stride = x.stride(0); a.rows = N;
+    a.dtype = code; a.dim = (int32_t)d; a.group = (int32_t)used;
+    const int rc = ar_silu_mul_fp8(&a, stream_of(dev));
+    if (rc) return fail(rc, "ar_silu_mul_fp8");
+    return tuple_of({&out, &scales});
+}
+
+// weighted(x, weights, place, out | None) -> out
+PyObject *weighted(PyObject *const *o) {
+    const Tensor &x = tensor("x", o[0]), &w = tensor("weights", o[1]), &place = tensor("place", o[2]);
+    const int dev = device_of("x", x);
+    check("x", x, dev, kAny, 2, false);
+    const int code = code_16("x", x);
+    check("weights", w, dev, at::kFloat, 2, true);
+    check("place", place, dev, at::kInt, 2, true);
+    check_shape("place", place, w.sizes());
+    const int64_t T = w.size(0), k = w.size(1), d = x.size(1);
+    if (d > kInt || k > kInt) refuse("x", "rows too long");
+    Tensor out;
+    if (o[3] != Py_None) {
+        out = tensor("out", o[3]);
+        check("out", out, dev, x.scalar_type(), 2, false);
+        check_shape("out", out, {T, d});
+        check_written("out", out);
+        if (may_share(out, x) || may_share(out, w) || may_share(out, place)) refuse("out", "overlaps an input");
+    } else {
+        out = make({T, d}, x.scalar_type(), x);
+    }
+    ar_experts_sum_args a = {};
+    a.x = x.data_ptr(); a.weights = static_cast<float *>(w.data_ptr()); a.place = static_cast<int32_t *>(place.data_ptr()); a.out = out.data_ptr();
+    a.x_stride = x.stride(0); a.out_stride = out.stride(0); a.rows = x.size(0); a.tokens = T; a.dtype = code; a.dim = (int32_t)d; a.chosen = (int32_t)k;
+    const int rc = ar_experts_sum(&a, stream_of(dev));
+    if (rc) return fail(rc, "ar_experts_sum");
+    return o[3] != Py_None ? (Py_INCREF(o[3]), o[3]) : THPVariable_Wrap(out);
+}
+
 // set_workspace(dev, stream, address): the workspace of a stream from now on
 PyObject *set_workspace(PyObject *const *o) {
     const int dev = (int)whole("device", o[0], 0, kInt);
@@ -466,7 +661,8 @@ PyMethodDef method(const char *name) {
 }
 
 PyMethodDef g_methods[] = {method<plan, 8>("plan"), method<append, 4>("append"), method<load, 4>("load"), method<attend, 13>("attend"),
-                           method<norm, 8>("norm"), method<set_workspace, 3>("set_workspace"), method<capture_id, 1>("capture_id"),
+                           method<norm, 8>("norm"),
+                           method<matmul, 8>("matmul"), method<route, 4>("route"), method<silu, 4>("silu"), method<weighted, 4>("weighted"), method<set_workspace, 3>("set_workspace"), method<capture_id, 1>("capture_id"),
                            method<set_error, 1>("set_error"), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_ops_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
