@@ -100,7 +100,71 @@ cudaError_t start_any(const Product &p, cudaStream_t s) {
     return launch_next(any_rows_kernel, dim3((unsigned)tiles, (unsigned)((p.a.out_dim + kSide - 1) / kSide)), 128, 0, s, 0, p);
 }
 
+// ------------------------------------------------- what the copy engine sees
+
+using Encode = decltype(&cuTensorMapEncodeTiled);
+
+// The driver's function; nullptr where there is none.
+Encode encoder() {
+    static Encode f = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess || found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        (void)cudaGetLastError();
+        return reinterpret_cast<Encode>(p);
+    }();
+    return f;
+}
+
+bool encode(CUtensorMap *m, const void *at, int rank, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
+    static const cuuint32_t ones[3] = {1, 1, 1};
+    const Encode f = encoder();
+    return f && f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(at), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether the copy engine can take these rows: on 16 bytes, one after another.
+bool copyable(const void *at, int64_t rows, int64_t stride, int64_t dim) {
+    return !misaligned(at, 16) && (rows == 1 || (stride % 16 == 0 && stride >= dim && stride < (int64_t)1 << 39));
+}
+
+bool fast(const Product &p) {
+    const ar_matmul_fp8_args &a = p.a;
+    return a.dim > 0 && a.x_rows > 0 && copyable(a.x, a.x_rows, a.x_stride, a.dim) && copyable(a.weight, a.out_dim, a.weight_stride, a.dim) &&
+           copyable(a.weight, a.experts, a.expert_stride, a.dim) && encoder();
+}
+
+int multiprocessors_of_device() {
+    static int known[64] = {};
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 64 && (n = *(volatile int *)&known[dev])) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (dev < 64) *(volatile int *)&known[dev] = n;
+    return n;
+}
+
 }  // namespace
+
+namespace tda {
+
+bool map_weight(CUtensorMap *m, const ar_matmul_fp8_args &a, int box) {
+    // (strides that nothing is found by are any multiple of 16)
+    const int64_t row = a.out_dim > 1 ? a.weight_stride : (a.dim + 15) / 16 * 16, expert = a.experts > 1 ? a.expert_stride : row * a.out_dim;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.dim, (cuuint64_t)a.out_dim, (cuuint64_t)a.experts}, strides[2] = {(cuuint64_t)row, (cuuint64_t)expert};
+    const cuuint32_t boxes[3] = {kBlock, (cuuint32_t)box, 1};
+    return encode(m, a.weight, 3, dims, strides, boxes);
+}
+
+bool map_rows(CUtensorMap *m, const ar_matmul_fp8_args &a, int box) {
+    const int64_t row = a.x_rows > 1 ? a.x_stride : (a.dim + 15) / 16 * 16;
+    const cuuint64_t dims[2] = {(cuuint64_t)a.dim, (cuuint64_t)a.x_rows}, strides[1] = {(cuuint64_t)row};
+    const cuuint32_t boxes[2] = {kBlock, a.row_of ? 1u : (cuuint32_t)box};
+    return encode(m, a.x, 2, dims, strides, boxes);
+}
+
+}  // namespace tda
 
 extern "C" AR_API int ar_matmul_fp8(const ar_matmul_fp8_args *args, ar_stream_t stream) {
     if (!args) return AR_EINVAL;
@@ -117,7 +181,12 @@ extern "C" AR_API int ar_matmul_fp8(const ar_matmul_fp8_args *args, ar_stream_t 
     Product p;
     p.a = a;
     p.groups = (a.dim + kBlock - 1) / kBlock;
-    return launch_status(start_any(p, stream));
+    if (!fast(p)) return launch_status(start_any(p, stream));
+    return launch_status(start_few(p, stream, multiprocessors_of_device()));
 }
 
-extern "C" AR_API int ar_matmul_fp8_status(void) { return AR_OK; }
+extern "C" AR_API int ar_matmul_fp8_status(void) {
+    int code = AR_OK;
+    const int rc = take_few_status(&code);
+    return rc ? rc : code;
+}

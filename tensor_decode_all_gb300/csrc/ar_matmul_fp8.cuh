@@ -2,6 +2,8 @@
 // weights a tile of it takes.
 #pragma once
 
+#include <cuda.h>
+
 #include "ar_ffn.h"
 #include "ar_kv4.cuh"
 
@@ -68,5 +70,14 @@ __device__ __forceinline__ int64_t source_row(const ar_matmul_fp8_args &a, int64
     const int r = a.row_of[row];
     return r >= 0 && r < a.x_rows ? r : -1;
 }
+
+// How the copy engine sees the weight, a box of `box` features of a group; and the rows of x, a box of `box` rows,
+// or one where they are picked by number.  False: it cannot (the addresses and strides are checked before).
+bool map_weight(CUtensorMap *m, const ar_matmul_fp8_args &a, int box);
+bool map_rows(CUtensorMap *m, const ar_matmul_fp8_args &a, int box);
+
+// The kernels for rows on 16 bytes, and the first error that each has recorded (and forgets).
+cudaError_t start_few(const Product &p, cudaStream_t s, int multiprocessors);
+int take_few_status(int *code);
 
 }  // namespace tda
