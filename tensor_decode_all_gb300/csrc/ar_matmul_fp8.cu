@@ -182,11 +182,14 @@ extern "C" AR_API int ar_matmul_fp8(const ar_matmul_fp8_args *args, ar_stream_t 
     p.a = a;
     p.groups = (a.dim + kBlock - 1) / kBlock;
     if (!fast(p)) return launch_status(start_any(p, stream));
-    return launch_status(start_few(p, stream, multiprocessors_of_device()));
+    const int multiprocessors = multiprocessors_of_device();
+    if (multiprocessors < 2) return AR_ECUDA;
+    if ((a.offsets ? a.rows / a.experts : a.rows) > 256) return launch_status(start_many(p, stream, multiprocessors));
+    return launch_status(start_few(p, stream, multiprocessors));
 }
 
 extern "C" AR_API int ar_matmul_fp8_status(void) {
-    int code = AR_OK;
-    const int rc = take_few_status(&code);
-    return rc ? rc : code;
+    int few = AR_OK, many = AR_OK;
+    const int rc = take_few_status(&few), other = take_many_status(&many);
+    return rc ? rc : other ? other : few ? few : many;
 }

@@ -79,5 +79,7 @@ bool map_rows(CUtensorMap *m, const ar_matmul_fp8_args &a, int box);
 // The kernels for rows on 16 bytes, and the first error that each has recorded (and forgets).
 cudaError_t start_few(const Product &p, cudaStream_t s, int multiprocessors);
 int take_few_status(int *code);
+cudaError_t start_many(const Product &p, cudaStream_t s, int multiprocessors);
+int take_many_status(int *code);
 
 }  // namespace tda

@@ -185,12 +185,13 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_consta
             if (!fine) break;
             if (cluster > 1) {
                 // (one tile to a cluster: nothing follows in the stages' memory)
-                tmem_before_sync();
+                __syncwarp();
                 cluster_sync_all();
                 const int each = TOK / cluster;
 #pragma unroll
                 for (int j = 0; j < TOK; ++j)
                     cluster_store(cluster_address(base + ((rank * each + j % each) * kBlock + mine) * 4, j / each), sum[j]);
+                __syncwarp();
                 cluster_sync_all();
                 const float *parts = reinterpret_cast<const float *>(shared);
 #pragma unroll 1
@@ -225,6 +226,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_consta
     }
     if (!fine && lane == 0) atomicCAS(&g_few_status, 0, AR_ETIMEOUT);
     if (cluster > 1 && any && !joined) {
+        __syncwarp();
         cluster_sync_all();
         cluster_sync_all();
     }
