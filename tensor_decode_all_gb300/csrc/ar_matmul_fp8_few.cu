@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_consta
                 for (int j = 0; j < TOK; j += W) {
                     float v[W];
                     tmem_load(tmem + ((uint32_t)(quarter * 32) << 16) + b * TOK + j, v);
-                    tmem_wait_loads();
+                    tmem_wait_loads(v);
 #pragma unroll
                     for (int i = 0; i < W; i += 4) {
                         const float4 sx = *reinterpret_cast<const float4 *>(words + j + i);

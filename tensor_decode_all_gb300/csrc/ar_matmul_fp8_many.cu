@@ -17,7 +17,9 @@ namespace {
 
 __device__ int g_many_status;
 
-constexpr int kManyThreads = 320;             // copies, instructions, eight warps that add up
+constexpr int kManyThreads = 384;             // a warpgroup for copies and instructions (two of its warps idle), two that add up
+// Registers a thread: 168 at the start, 384 * 168 = 128 * 72 + 256 * 216.
+constexpr int kRegistersMoving = 72, kRegistersAdding = 216;
 constexpr int kTileRows = 256, kTileFeatures = 256;
 constexpr int kManyStages = 6, kOperandBytes = kBlock * kBlock, kManyScaleBytes = (kBlock + 4) * 4;
 constexpr int kManyStageBytes = 2 * kOperandBytes + kManyScaleBytes, kOutBytes = 32 * 64;
@@ -93,6 +95,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
     bool fine = true;
     int feature = 0;
 
+    if (warp < 4) {
+    registers_down<kRegistersMoving>();
     if (warp == 0) {
         const uint32_t full_of_0 = cluster_address(full, 0);
         int issued = 0;
@@ -161,10 +165,12 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
             if (!fine)
                 for (int i = max(n - 2, 0); i < n; ++i) (void)bar_wait_warp(sums_full + 8 * (i & 1), i >> 1 & 1);
         }
+    }
     } else {
-        const int quarter = warp & 3, half = (warp - 2) >> 2, mine = quarter * 32 + lane;
+        registers_up<kRegistersAdding>();
+        const int quarter = warp & 3, half = (warp - 4) >> 2, mine = quarter * 32 + lane;
         const uint32_t empty_of_0 = cluster_address(sums_empty, 0), from = tmem + ((uint32_t)(quarter * 32) << 16) + half * kBlock;
-        const uint32_t out_words = out_at + (warp - 2) * kOutBytes;
+        const uint32_t out_words = out_at + (warp - 4) * kOutBytes;
         const bool vectors = !(reinterpret_cast<uintptr_t>(a.out) & 15) && a.out_stride % 8 == 0;
         int n = 0;
         for (int64_t u = blockIdx.x / 2; fine; u += step) {
@@ -183,14 +189,17 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
                 __syncwarp();
                 if (lane == 0) bar_arrive(empty + 8 * s);      // (the sums are there: nothing reads the stage any more)
                 const unsigned long long ff = pair_of_floats(f, f);
+                // (16 columns are on their way while the 16 before are added)
+                float v[2][16];
+                tmem_load(from + b * kTileFeatures, v[0]);
+                tmem_wait_loads(v[0]);
 #pragma unroll
-                for (int j = 0; j < kBlock; j += 32) {
-                    float v[32];
-                    tmem_load(from + b * kTileFeatures + j, v);
-                    tmem_wait_loads();
+                for (int j = 0; j < 8; ++j) {
+                    if (j < 7) tmem_load(from + b * kTileFeatures + (j + 1) * 16, v[(j + 1) & 1]);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2)
-                        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum[(j + i) / 2]) : "l"(pair_of_floats(v[i], v[i + 1])), "l"(ff));
+                    for (int i = 0; i < 16; i += 2)
+                        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum[j * 8 + i / 2]) : "l"(pair_of_floats(v[j & 1][i], v[j & 1][i + 1])), "l"(ff));
+                    if (j < 7) tmem_wait_loads(v[(j + 1) & 1]);
                 }
                 tmem_before_sync();
                 __syncwarp();
