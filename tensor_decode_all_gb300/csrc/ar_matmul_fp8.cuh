@@ -58,6 +58,17 @@ __device__ __forceinline__ Rows rows_of_tile(const ar_matmul_fp8_args &a, int64_
     return Rows{0, 0, 0};
 }
 
+// How many tiles of `size` rows there are; the whole warp calls it.
+__device__ __forceinline__ int64_t tiles_of_rows(const ar_matmul_fp8_args &a, int size) {
+    if (!a.offsets) return (a.rows + size - 1) / size;
+    int64_t n = 0;
+    for (int e = threadIdx.x & 31; e < a.experts; e += 32)
+        n += (max(clamp_row(a.offsets[e + 1], a.rows) - clamp_row(a.offsets[e], a.rows), 0) + size - 1) / size;
+#pragma unroll
+    for (int d = 16; d; d /= 2) n += __shfl_xor_sync(~0u, n, d);
+    return n;
+}
+
 // The most tiles of `size` rows that a call can have, whatever its offsets.
 inline int64_t most_tiles(const ar_matmul_fp8_args &a, int size) {
     const int64_t whole = (a.rows + size - 1) / size;

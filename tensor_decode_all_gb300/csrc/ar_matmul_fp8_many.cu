@@ -7,8 +7,13 @@
 // and 128 features to a thread, multiply by the two scales and add up in registers, while the next group's sums go to the
 // other half of tensor memory.
 //
-// Blocks stay and go from tile to tile; copies for the next tile are under way while one is stored.  Results leave by way of
-// shared memory, 64 bytes of a row at a time.
+// A tile of at most 128 rows (the end of an expert's) takes half the time: 64 rows to a block, whose features
+// lie on twice the lanes.  Where the last round of tiles would occupy half of the pairs or less, its tiles are cut in two.
+//
+// Blocks stay and go from tile to tile: a warp says which, the copies run ahead, and the next tile's first sums are
+// under way while one is stored, 32 bytes of a row at a time.
+#include <algorithm>
+
 #include "ar_matmul_fp8.cuh"
 #include "ar_tensor.cuh"
 
@@ -17,13 +22,13 @@ namespace {
 
 __device__ int g_many_status;
 
-constexpr int kManyThreads = 384;             // a warpgroup for copies and instructions (two of its warps idle), two that add up
+constexpr int kManyThreads = 384;             // a warpgroup for copies, instructions and tiles, two that add up
 // Registers a thread: 168 at the start, 384 * 168 = 128 * 72 + 256 * 216.
 constexpr int kRegistersMoving = 72, kRegistersAdding = 216;
 constexpr int kTileRows = 256, kTileFeatures = 256;
-constexpr int kManyStages = 6, kOperandBytes = kBlock * kBlock, kManyScaleBytes = (kBlock + 4) * 4;
-constexpr int kManyStageBytes = 2 * kOperandBytes + kManyScaleBytes, kOutBytes = 32 * 64;
-constexpr int kManySmem = kManyStages * kManyStageBytes + 8 * kOutBytes + (3 * kManyStages + 4) * 8 + 16 + 1024;
+constexpr int kManyStages = 6, kOperandBytes = kBlock * kBlock, kManyScaleBytes = (kBlock + 4) * 4, kTiles = 4;
+constexpr int kManyStageBytes = 2 * kOperandBytes + kManyScaleBytes;
+constexpr int kManySmem = kManyStages * kManyStageBytes + kTiles * 16 + (3 * kManyStages + 4 + 2 * kTiles) * 8 + 16 + 1024;
 constexpr int kRowTilesTogether = 8;
 
 __device__ __forceinline__ unsigned long long pair_of_floats(float a, float b) {
@@ -37,18 +42,25 @@ __device__ __forceinline__ float2 floats_of(unsigned long long v) {
     return r;
 }
 
+// What the pair does next: rows first .. first + count - 1 of the call (both blocks'), features from `feature` on.  Count 0: no more.
+struct Tile {
+    int expert, first, count, feature;
+};
+
 __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_constant__ Product p, const __grid_constant__ CUtensorMap weight,
-                                                               const __grid_constant__ CUtensorMap x, int row_tiles) {
+                                                               const __grid_constant__ CUtensorMap x) {
     constexpr int S = kManyStages;
     extern __shared__ uint8_t raw[];
     const ar_matmul_fp8_args &a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t base = (shared_address(raw) + 1023) & ~1023u;
-    const uint32_t rows_at = base, weights = rows_at + S * kOperandBytes, out_at = weights + S * kOperandBytes, scales = out_at + 8 * kOutBytes;
-    // full: block 0's, both blocks' operands; scaled: the scales; empty: a stage's; sums_full, sums_empty (block 0's): the halves of tensor memory
-    const uint32_t full = scales + S * kManyScaleBytes, scaled = full + S * 8, empty = scaled + S * 8, sums_full = empty + S * 8, sums_empty = sums_full + 16;
-    const uint32_t tmem_at = sums_empty + 16;
+    const uint32_t rows_at = base, weights = rows_at + S * kOperandBytes, scales = weights + S * kOperandBytes, tiles_at = scales + S * kManyScaleBytes;
+    // full: block 0's, both blocks' operands; scaled: the scales; empty: a stage's; sums_full, sums_empty (block 0's): the halves of
+    // tensor memory; known, used: the next tiles
+    const uint32_t full = tiles_at + kTiles * 16, scaled = full + S * 8, empty = scaled + S * 8, sums_full = empty + S * 8, sums_empty = sums_full + 16;
+    const uint32_t known = sums_empty + 16, used = known + kTiles * 8, tmem_at = used + kTiles * 8;
     uint8_t *const shared = raw + (base - shared_address(raw));
+    volatile Tile *const tiles = reinterpret_cast<volatile Tile *>(shared + (tiles_at - base));
     const int rank = (int)cluster_rank();
     if (warp == 0) {
         if (lane == 0) {
@@ -60,6 +72,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
             for (int i = 0; i < 2; ++i) {
                 bar_init(sums_full + 8 * i, 1);
                 bar_init(sums_empty + 8 * i, 16);
+            }
+            for (int i = 0; i < kTiles; ++i) {
+                bar_init(known + 8 * i, 1);
+                bar_init(used + 8 * i, 10);            // the copies' warp, the instructions' and the eight
             }
             bar_init_done();
             tensor_prefetch(&weight);
@@ -75,172 +91,222 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(shared + (tmem_at - base));
     after_the_stream();
 
-    const int wide = (a.out_dim + kTileFeatures - 1) / kTileFeatures, blocks = (a.out_dim + kBlock - 1) / kBlock;
-    const int64_t step = gridDim.x / 2;
-    // With one weight, 8 tiles of rows by all features, then the next 8: what the GPU works on at a time is a
-    // patch with few different rows and features, which L2 holds.  Rows and feature are the pair's.
-    auto tile_of = [&](int64_t u, int &feature) {
-        int64_t t;
-        if (row_tiles) {
-            const int64_t band = u / ((int64_t)kRowTilesTogether * wide), in = u - band * kRowTilesTogether * wide;
-            const int high = min(kRowTilesTogether, (int)max(row_tiles - band * kRowTilesTogether, (int64_t)1));
-            t = band * kRowTilesTogether + in % high;
-            feature = (int)(in / high) * kTileFeatures;
-        } else {
-            t = u / wide;
-            feature = (int)(u - t * wide) * kTileFeatures;
-        }
-        return feature < a.out_dim ? rows_of_tile(a, t, kTileRows) : Rows{0, 0, 0};
-    };
+    const int blocks = (a.out_dim + kBlock - 1) / kBlock;
     bool fine = true;
-    int feature = 0;
+    Ring<kTiles> next;
+    // The pair's next tile, for a warp that counts itself among `used`.
+    auto next_tile = [&]() {
+        if (!(fine = bar_wait_warp(known + 8 * next.at, next.parity))) return Tile{0, 0, 0, 0};
+        const volatile Tile &t = tiles[next.at];
+        const Tile tile = {t.expert, t.first, t.count, t.feature};
+        __syncwarp();
+        if (lane == 0) bar_arrive(used + 8 * next.at);
+        next.next();
+        return tile;
+    };
 
     if (warp < 4) {
-    registers_down<kRegistersMoving>();
-    if (warp == 0) {
-        const uint32_t full_of_0 = cluster_address(full, 0);
-        int issued = 0;
-        for (int64_t u = blockIdx.x / 2; fine; u += step) {
-            const Rows rows = tile_of(u, feature);
-            if (rows.count == 0) break;
-            const int first = rows.first + rank * kBlock, count = rows.count - rank * kBlock;
-            int picked[4] = {0, 0, 0, 0};
-            if (a.row_of) {
+        registers_down<kRegistersMoving>();
+        if (warp == 0) {
+            const uint32_t full_of_0 = cluster_address(full, 0);
+            Ring<S> stage;
+            int issued = 0;
+            while (fine) {
+                const Tile tile = next_tile();
+                if (tile.count == 0) break;
+                // (half of them are read twice where the tile is short)
+                const int own = tile.count <= kBlock ? kBlock / 2 : kBlock, first = tile.first + rank * own, count = min(tile.count - rank * own, own);
+                int picked[4] = {0, 0, 0, 0};
+                if (a.row_of) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = 4 * lane + i;
+                        picked[i] = j < count ? (int)max(source_row(a, first + j), (int64_t)0) : 0;
+                    }
+                }
+                const float *scale[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int j = 4 * lane + i;
-                    picked[i] = j < count ? (int)max(source_row(a, first + j), (int64_t)0) : 0;
+                    const int j = lane + 32 * i;
+                    const int64_t r = j < count ? source_row(a, first + j) : -1;
+                    scale[i] = r >= 0 ? a.x_scales + r * a.x_scales_stride : nullptr;
                 }
-            }
-            const float *scale[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = lane + 32 * i;
-                const int64_t r = j < count ? source_row(a, first + j) : -1;
-                scale[i] = r >= 0 ? a.x_scales + r * a.x_scales_stride : nullptr;
-            }
-            // the weight's scales of both halves, by two lanes
-            const int half = feature / kBlock + lane;
-            const float *weight_scale = lane < 2 && half < blocks ? a.weight_scales + ((int64_t)rows.expert * blocks + half) * p.groups : nullptr;
-            for (int k = 0; k < p.groups; ++k, ++issued) {
-                const int s = issued % S;
-                if (!(fine = bar_wait_warp(empty + 8 * s, (issued / S & 1) ^ 1))) break;
-                const uint32_t bar = full_of_0 + 8 * s, to = rows_at + s * kOperandBytes, words = scales + s * kManyScaleBytes;
-                if (lane == 0) {
-                    if (rank == 0) bar_expect(full + 8 * s, 4 * kOperandBytes);
-                    pair_tensor_load(weights + s * kOperandBytes, &weight, bar, k * kBlock, feature + rank * kBlock, rows.expert);
-                    if (!a.row_of) pair_tensor_load(to, &x, bar, k * kBlock, first);
-                }
-                if (a.row_of) pair_tensor_gather(to + lane * 4 * kBlock, &x, bar, k * kBlock, picked);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) copy_word(words + 4 * (lane + 32 * i), scale[i] ? scale[i] + (a.x_row_scales ? 0 : k) : a.x_scales, scale[i] != nullptr);
-                if (lane < 2) copy_word(words + 4 * (kBlock + lane), weight_scale ? weight_scale + k : a.weight_scales, weight_scale != nullptr);
-                bar_arrive_copies(scaled + 8 * s);
-                __syncwarp();
-            }
-        }
-        if (!fine) {                                   // what is under way has to land before the blocks may end
-            for (int i = max(issued - S, 0); i < issued; ++i) (void)bar_wait_warp(scaled + 8 * (i % S), i / S & 1);
-            if (rank == 0)
-                for (int i = max(issued - S, 0); i < issued; ++i) (void)bar_wait_warp(full + 8 * (i % S), i / S & 1);
-        }
-    } else if (warp == 1) {
-        if (rank == 0) {
-            int n = 0;
-            for (int64_t u = blockIdx.x / 2; fine; u += step) {
-                if (tile_of(u, feature).count == 0) break;
-                for (int k = 0; k < p.groups; ++k, ++n) {
-                    const int s = n % S, b = n & 1;
-                    if (!(fine = bar_wait_warp(sums_empty + 8 * b, (n >> 1 & 1) ^ 1) && bar_wait_warp(full + 8 * s, n / S & 1))) break;
-                    tmem_after_sync();
+                // the weight's scales of both halves, by two lanes
+                const int half = tile.feature / kBlock + lane;
+                const float *weight_scale = lane < 2 && half < blocks ? a.weight_scales + ((int64_t)tile.expert * blocks + half) * p.groups : nullptr;
+                for (int k = 0; k < p.groups; ++k, ++issued, stage.next()) {
+                    const uint32_t s = stage.at;
+                    if (!(fine = bar_wait_warp(empty + 8 * s, stage.parity ^ 1))) break;
+                    const uint32_t bar = full_of_0 + 8 * s, to = rows_at + s * kOperandBytes, words = scales + s * kManyScaleBytes;
                     if (lane == 0) {
-                        const uint64_t r = operand_of(rows_at + s * kOperandBytes), w = operand_of(weights + s * kOperandBytes);
+                        if (rank == 0) bar_expect(full + 8 * s, 4 * kOperandBytes);
+                        pair_tensor_load(weights + s * kOperandBytes, &weight, bar, k * kBlock, tile.feature + rank * kBlock, tile.expert);
+                        if (!a.row_of) pair_tensor_load(to, &x, bar, k * kBlock, first);
+                    }
+                    if (a.row_of) pair_tensor_gather(to + lane * 4 * kBlock, &x, bar, k * kBlock, picked);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) pair_mma_e4m3(tmem + b * kTileFeatures, r + 2 * i, w + 2 * i, product_shape(kTileRows, kTileFeatures), i > 0);
-                        pair_mma_commit(sums_full + 8 * b);
+                    for (int i = 0; i < 4; ++i) copy_word(words + 4 * (lane + 32 * i), scale[i] ? scale[i] + (a.x_row_scales ? 0 : k) : a.x_scales, scale[i] != nullptr);
+                    if (lane < 2) copy_word(words + 4 * (kBlock + lane), weight_scale ? weight_scale + k : a.weight_scales, weight_scale != nullptr);
+                    bar_arrive_copies(scaled + 8 * s);
+                    __syncwarp();
+                }
+            }
+            if (!fine) {                                   // what is under way has to land before the blocks may end
+                for (int i = max(issued - S, 0); i < issued; ++i) (void)bar_wait_warp(scaled + 8 * (i % S), i / S & 1);
+                if (rank == 0)
+                    for (int i = max(issued - S, 0); i < issued; ++i) (void)bar_wait_warp(full + 8 * (i % S), i / S & 1);
+            }
+        } else if (warp == 1) {
+            const uint64_t rows_operand = operand_of(rows_at), weights_operand = operand_of(weights);
+            const bool one = elected();
+            Ring<S> stage;
+            Ring<2> half;
+            int n = 0;
+            while (fine) {
+                const Tile tile = next_tile();
+                if (tile.count == 0) break;
+                if (rank != 0) continue;
+                const uint32_t shape = product_shape(tile.count <= kBlock ? kBlock : kTileRows, kTileFeatures);
+                // (the fewest instructions: a step of this loop has to be done before the matrix instructions of the last one are)
+                for (int k = 0; k < p.groups; ++k, ++n, stage.next(), half.next()) {
+                    if (!(fine = bar_wait_warp(full + 8 * stage.at, stage.parity, sums_empty + 8 * half.at, half.parity ^ 1))) break;
+                    tmem_after_sync();
+                    if (one) {
+                        const uint64_t r = rows_operand + stage.at * (kOperandBytes >> 4), w = weights_operand + stage.at * (kOperandBytes >> 4);
+                        const uint32_t to = tmem + half.at * kTileFeatures;
+                        pair_mma_e4m3(to, r, w, shape, false);
+                        pair_mma_e4m3(to, r + 2, w + 2, shape, true);
+                        pair_mma_e4m3(to, r + 4, w + 4, shape, true);
+                        pair_mma_e4m3(to, r + 6, w + 6, shape, true);
+                        pair_mma_commit(sums_full + 8 * half.at);
                     }
                     __syncwarp();
                 }
             }
             if (!fine)
                 for (int i = max(n - 2, 0); i < n; ++i) (void)bar_wait_warp(sums_full + 8 * (i & 1), i >> 1 & 1);
+        } else if (warp == 2) {
+            // Which tiles: with one weight, 8 tiles of rows by all features, then the next 8 (what the GPU works on at a time is
+            // a patch with few different rows and features, which L2 holds); else the experts' in their order.
+            const int wide = (a.out_dim + kTileFeatures - 1) / kTileFeatures, pairs = gridDim.x / 2;
+            const int64_t high = tiles_of_rows(a, kTileRows), whole = high * wide;
+            const int64_t last = whole % pairs, cut = 2 * last <= pairs ? whole - last : whole, all = whole + (whole - cut);
+            for (int64_t u = blockIdx.x / 2;; u += pairs) {
+                Tile tile = {0, 0, 0, 0};
+                if (u < all) {
+                    const int64_t v = u < cut ? u : cut + ((u - cut) >> 1);
+                    int64_t t;
+                    if (a.offsets) {
+                        t = v / wide;
+                        tile.feature = (int)(v - t * wide) * kTileFeatures;
+                    } else {
+                        const int64_t band = v / (kRowTilesTogether * wide);
+                        const int in = (int)(v - band * kRowTilesTogether * wide), h = (int)min((int64_t)kRowTilesTogether, high - band * kRowTilesTogether);
+                        t = band * kRowTilesTogether + in % h;
+                        tile.feature = in / h * kTileFeatures;
+                    }
+                    const Rows rows = rows_of_tile(a, t, kTileRows);
+                    tile.expert = rows.expert;
+                    tile.first = rows.first;
+                    tile.count = rows.count;
+                    if (u >= cut) {
+                        const int skip = (u - cut) & 1 ? kBlock : 0;
+                        tile.first += skip;
+                        tile.count = min(tile.count - skip, kBlock);
+                        if (tile.count <= 0) continue;
+                    }
+                }
+                if (!(fine = bar_wait_warp(used + 8 * next.at, next.parity ^ 1))) break;
+                if (lane == 0) {
+                    volatile Tile &t = tiles[next.at];
+                    t.expert = tile.expert;
+                    t.first = tile.first;
+                    t.count = tile.count;
+                    t.feature = tile.feature;
+                    bar_arrive(known + 8 * next.at);
+                }
+                next.next();
+                if (tile.count == 0) break;
+            }
         }
-    }
     } else {
         registers_up<kRegistersAdding>();
-        const int quarter = warp & 3, half = (warp - 4) >> 2, mine = quarter * 32 + lane;
-        const uint32_t empty_of_0 = cluster_address(sums_empty, 0), from = tmem + ((uint32_t)(quarter * 32) << 16) + half * kBlock;
-        const uint32_t out_words = out_at + (warp - 4) * kOutBytes;
-        const bool vectors = !(reinterpret_cast<uintptr_t>(a.out) & 15) && a.out_stride % 8 == 0;
-        int n = 0;
-        for (int64_t u = blockIdx.x / 2; fine; u += step) {
-            const Rows rows = tile_of(u, feature);
-            if (rows.count == 0) break;
-            const int first = rows.first + rank * kBlock, count = rows.count - rank * kBlock;
-            unsigned long long sum[kBlock / 2];
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const uint32_t empty_of_0 = cluster_address(sums_empty, 0);
+        // stores of 32, 16 and 2 bytes
+        const int wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride % 16 == 0 ? 16 : reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_stride % 8 == 0 ? 8 : 1;
+        Ring<S> stage;
+        Ring<2> sums;
+        // (written out for either width: one loop that asks which keeps its sums in registers a third as fast)
+        auto take = [&](const Tile &tile, auto short_tile) {
+            // A short tile's 64 rows lie on two quarters of the lanes, its other 128 features on the other two.
+            constexpr bool kShort = decltype(short_tile)::value;
+            constexpr int kOwn = kShort ? kBlock / 2 : kBlock;      // rows of the block, and features of the thread
+            const int first = tile.first + rank * kOwn, count = min(tile.count - rank * kOwn, kOwn);
+            const int mine = (kShort ? quarter & 1 : quarter) * 32 + lane, block = kShort ? quarter >> 1 : half;
+            const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + half * kOwn;
+            const int feature = tile.feature + block * kBlock + (kShort ? half * kOwn : 0);
+            const bool real = mine < count && source_row(a, first + mine) >= 0;
+            unsigned long long sum[kOwn / 2];
 #pragma unroll
-            for (int j = 0; j < kBlock / 2; ++j) sum[j] = 0;
-            for (int k = 0; k < p.groups; ++k, ++n) {
-                const int s = n % S, b = n & 1;
-                if (!(fine = bar_wait_warp(scaled + 8 * s, n / S & 1) && bar_wait_warp(sums_full + 8 * b, n >> 1 & 1))) break;
+            for (int j = 0; j < kOwn / 2; ++j) sum[j] = 0;
+            for (int k = 0; k < p.groups; ++k, stage.next(), sums.next()) {
+                if (!(fine = bar_wait_warp(scaled + 8 * stage.at, stage.parity))) return;
+                const float *words = reinterpret_cast<const float *>(shared + (scales - base)) + stage.at * (kManyScaleBytes / 4);
+                const float f = words[mine] * words[kBlock + block];
+                if (!(fine = bar_wait_warp(sums_full + 8 * sums.at, sums.parity))) return;
                 tmem_after_sync();
-                const float *words = reinterpret_cast<const float *>(shared + (scales - base) + s * kManyScaleBytes);
-                const float f = words[mine] * words[kBlock + half];
-                __syncwarp();
-                if (lane == 0) bar_arrive(empty + 8 * s);      // (the sums are there: nothing reads the stage any more)
-                const unsigned long long ff = pair_of_floats(f, f);
-                // (16 columns are on their way while the 16 before are added)
+                if (lane == 0) bar_arrive(empty + 8 * stage.at);      // (the sums are there: nothing reads the stage any more)
+                // 16 columns are on their way while the 16 before are multiplied and added
+                const unsigned long long both = pair_of_floats(f, f);
+                const uint32_t at = from + sums.at * kTileFeatures;
                 float v[2][16];
-                tmem_load(from + b * kTileFeatures, v[0]);
+                tmem_load(at, v[0]);
                 tmem_wait_loads(v[0]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (j < 7) tmem_load(from + b * kTileFeatures + (j + 1) * 16, v[(j + 1) & 1]);
+                for (int j = 0; j < kOwn / 16; ++j) {
+                    if (j < kOwn / 16 - 1) tmem_load(at + (j + 1) * 16, v[(j + 1) & 1]);
 #pragma unroll
                     for (int i = 0; i < 16; i += 2)
-                        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum[j * 8 + i / 2]) : "l"(pair_of_floats(v[j & 1][i], v[j & 1][i + 1])), "l"(ff));
-                    if (j < 7) tmem_wait_loads(v[(j + 1) & 1]);
+                        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum[j * 8 + i / 2]) : "l"(pair_of_floats(v[j & 1][i], v[j & 1][i + 1])), "l"(both));
+                    if (j < kOwn / 16 - 1) tmem_wait_loads(v[(j + 1) & 1]);
                 }
                 tmem_before_sync();
                 __syncwarp();
-                if (lane == 0) cluster_bar_arrive(empty_of_0 + 8 * b);
+                if (lane == 0) cluster_bar_arrive(empty_of_0 + 8 * sums.at);
             }
-            if (!fine) break;
-            const bool real = mine < count && source_row(a, first + mine) >= 0;
+            if (mine >= count) return;
+            uint16_t *const row = static_cast<uint16_t *>(a.out) + (int64_t)(first + mine) * a.out_stride + feature;
+            const int there = min(a.out_dim - feature, kOwn);
 #pragma unroll
-            for (int j = 0; j < kBlock; j += 32) {
-                // a row's 32 features (64 bytes) from a thread, in 16-byte pieces that two rows' order keeps apart
+            for (int j = 0; j < kOwn; j += 16) {
+                if (j >= there) break;
+                uint32_t w[8];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float2 v = floats_of(sum[j / 2 + c * 4 + e]);
-                        if (!real) v = make_float2(0, 0);
-                        w[e] = a.dtype == AR_F16 ? to_pair<__half>(v) : to_pair<__nv_bfloat16>(v);
-                    }
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(out_words + lane * 64 + ((c ^ (lane >> 1 & 3)) << 4)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+                for (int e = 0; e < 8; ++e) {
+                    float2 v = floats_of(sum[j / 2 + e]);
+                    if (!real) v = make_float2(0, 0);
+                    w[e] = a.dtype == AR_F16 ? to_pair<__half>(v) : to_pair<__nv_bfloat16>(v);
                 }
-                __syncwarp();
-                const int at = feature + half * kBlock + j + (lane & 3) * 8;
+                if (wide == 16 && j + 16 <= there) {
+                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + j), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                                 "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+                } else if (wide >= 8 && j + 16 <= there) {
+                    *reinterpret_cast<uint4 *>(row + j) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4 *>(row + j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = i * 8 + (lane >> 2), row = quarter * 32 + r;
-                    union { uint4 v; uint16_t h[8]; } w;
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.v.x), "=r"(w.v.y), "=r"(w.v.z), "=r"(w.v.w) : "r"(out_words + r * 64 + (((lane & 3) ^ (r >> 1 & 3)) << 4)) : "memory");
-                    if (row < count && at < a.out_dim) {
-                        uint16_t *to = static_cast<uint16_t *>(a.out) + (int64_t)(first + row) * a.out_stride + at;
-                        if (vectors && at + 8 <= a.out_dim) {
-                            *reinterpret_cast<uint4 *>(to) = w.v;
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (at + e < a.out_dim) to[e] = w.h[e];
-                        }
-                    }
+                    for (int e = 0; e < 16; ++e)
+                        if (j + e < there) row[j + e] = (uint16_t)(w[e / 2] >> (e & 1) * 16);
                 }
-                __syncwarp();
             }
+        };
+        while (fine) {
+            const Tile tile = next_tile();
+            if (tile.count == 0) break;
+            if (tile.count <= kBlock) take(tile, std::true_type());
+            else take(tile, std::false_type());
+            __syncwarp();
         }
     }
     if (!fine && lane == 0) atomicCAS(&g_many_status, 0, AR_ETIMEOUT);
@@ -265,8 +331,8 @@ cudaError_t start_many(const Product &p, cudaStream_t s, int multiprocessors) {
     if (e != cudaSuccess) return e;
     CUtensorMap weight, x;
     if (!map_weight(&weight, a, kBlock) || !map_rows(&x, a, kBlock)) return cudaErrorInvalidValue;
-    const int64_t tiles = most_tiles(a, kTileRows), units = tiles * ((a.out_dim + kTileFeatures - 1) / kTileFeatures), pairs = multiprocessors / 2;
-    return launch_next(many_kernel, dim3((unsigned)(2 * (units < pairs ? units : pairs))), kManyThreads, kManySmem, s, 2, p, weight, x, a.offsets ? 0 : (int)tiles);
+    const int64_t units = most_tiles(a, kTileRows) * ((a.out_dim + kTileFeatures - 1) / kTileFeatures), pairs = multiprocessors / 2;
+    return launch_next(many_kernel, dim3((unsigned)(2 * std::min(2 * units, pairs))), kManyThreads, kManySmem, s, 2, p, weight, x);
 }
 
 int take_many_status(int *code) {

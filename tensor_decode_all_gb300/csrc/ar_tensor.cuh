@@ -25,14 +25,16 @@ __device__ __forceinline__ void bar_arrive_copies(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ uint32_t bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done;
+}
 // The whole warp waits for the phase of that parity to end, four seconds at most: false after that, in all lanes.
-__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool bar_wait_long(uint32_t bar, uint32_t parity) {
     long long begun = 0;
     for (int i = 1;; ++i) {
-        uint32_t done;
-        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                     : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-        if (__all_sync(~0u, done)) return true;
+        if (__all_sync(~0u, bar_try(bar, parity))) return true;
         if (i % 256 == 0) {
             long long t;
             asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
@@ -42,6 +44,32 @@ __device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity) {
         }
     }
 }
+__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity) {
+    return __all_sync(~0u, bar_try(bar, parity)) || bar_wait_long(bar, parity);
+}
+// For both: their states are asked for together.
+__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, uint32_t other, uint32_t other_parity) {
+    const uint32_t done = bar_try(bar, parity), other_done = bar_try(other, other_parity);
+    return __all_sync(~0u, done & other_done) || (bar_wait_warp(bar, parity) && bar_wait_warp(other, other_parity));
+}
+
+// One lane of the warp, the same each time.
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+    return r;
+}
+
+// Where a warp stands in a ring of N stages: the stage, and the parity of its present round.
+template <int N> struct Ring {
+    uint32_t at = 0, parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) {
+            at = 0;
+            parity ^= 1;
+        }
+    }
+};
 
 // --------------------------------------------------------------------- copies
 
