@@ -88,12 +88,16 @@ typedef struct ar_route_experts_args {
     int32_t *offsets;
     int32_t *rows;
     int32_t *place;
+    int32_t *workspace;     /* ar_route_experts_workspace() bytes, this call's alone until it has run; NULL where that is 0 */
     int64_t logits_stride, tokens;
     int32_t dtype;          /* AR_F16, AR_BF16 or AR_F32 */
     int32_t experts, chosen;
     int32_t normalize;      /* 0 or 1 */
 } ar_route_experts_args;
 AR_API int ar_route_experts(const ar_route_experts_args *args, ar_stream_t stream);
+
+/* Bytes of working memory that a call of these sizes (tokens, experts, chosen) needs; what is in it does not matter. */
+AR_API size_t ar_route_experts_workspace(const ar_route_experts_args *args);
 
 /*
  * ar_silu_mul_fp8 -- the gated activation, rounded to 8 bits.  Row r of x holds dim gates and dim factors after them:

@@ -1,4 +1,8 @@
 // ar_silu_fp8.cu -- ar_silu_mul_fp8: the gated activation with e4m3 output and scales.
+//
+// One pass, 8 channels to a thread: 16 bytes of gates, 16 of factors, 8 of output.  Groups of a power of two up to 256 lie in
+// 1 to 32 lanes of a warp, whose largest value goes round by shuffles; a row that is one group is a block's, its
+// values kept in registers until the block's largest is known.  Bound by memory: 5 bytes a channel.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -17,7 +21,153 @@ __device__ __forceinline__ float top_of(float a, float b) {
     return r;
 }
 
+// The same of a (0 or more already) and two others.
+__device__ __forceinline__ float top_of(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+    return r;
+}
+
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdiv_rn(g, 1.0f + expf(-g)) * u; }
+
+// The same for gates from -8 on, by the hardware's power of two and reciprocal.  Its argument, up to 11.6, is rounded by 2^-21 and
+// off by 2^-22.6 for log2(e)'s sake: exp(-g) is off by less than 2^-20.5 with the instruction's own 2^-22, y by less than 2^-19.9.
+__device__ __forceinline__ float quick_silu_mul(float g, float u) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * r * u;
+}
+
+// A group's scale, and what its values are multiplied by, from its largest value.
+__device__ __forceinline__ float2 scale_of(float top) {
+    if (top > 0x1p-60f && top < 0x1p100f) return make_float2(top * (1.0f / 448.0f), __fdividef(448.0f, top));   // within 2 units of the last place of 1 / scale
+    const float scale = top == 0 ? 1.0f : __fdiv_rn(top, 448.0f);
+    return make_float2(scale, 0);
+}
+
+union Vec {
+    uint4 v;
+    uint32_t u[4];
+};
+
+// The 8 values of a thread, and the larger of `top` and theirs.
+template <typename T> __device__ __forceinline__ float values(const Vec &g, const Vec &u, float (&y)[8], float top) {
+    float low = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 a = pair_of<T>(g.u[e]), b = pair_of<T>(u.u[e]);
+        low = fminf(fminf(low, a.x), a.y);
+        y[2 * e] = quick_silu_mul(a.x, b.x);
+        y[2 * e + 1] = quick_silu_mul(a.y, b.y);
+    }
+    if (low < -8.0f) {          // (seldom; y is the smaller the more so)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 a = pair_of<T>(g.u[e]), b = pair_of<T>(u.u[e]);
+            y[2 * e] = silu_mul(a.x, b.x);
+            y[2 * e + 1] = silu_mul(a.y, b.y);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = top_of(top, y[2 * e], y[2 * e + 1]);
+    return top;
+}
+
+__device__ __forceinline__ uint2 rounded(const float (&y)[8], float2 s) {
+    uint32_t b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 v = s.y != 0 ? make_float2(y[2 * e] * s.y, y[2 * e + 1] * s.y) : make_float2(__fdiv_rn(y[2 * e], s.x), __fdiv_rn(y[2 * e + 1], s.x));
+        b[e] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+    }
+    return make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+}
+
+constexpr int kGroupThreads = 256, kGroupVecs = 2;
+
+// n / d for n below 2^31, by a product and a shift (d's multiplier is ceil(2^(32 + shift) / d) - 2^32, with the least shift that
+// 2^shift >= d: the error is below n / 2^(32 + shift) < 1 / d).
+struct Divisor {
+    uint32_t d, factor, shift;
+    explicit Divisor(uint32_t by) : d(by), shift(0) {
+        while (((uint64_t)1 << shift) < by) ++shift;
+        factor = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - by)) / by + 1);
+    }
+    __device__ uint32_t of(uint32_t n) const { return (__umulhi(n, factor) + n) >> shift; }
+};
+
+// `lanes` threads to a group, kGroupVecs vectors to a thread; a row's vectors are counted up to whole groups.
+template <typename T>
+__global__ void __launch_bounds__(kGroupThreads) groups_kernel(const ar_silu_mul_fp8_args a, int lanes, int groups, const Divisor row_vecs) {
+    after_the_stream();
+    const int vecs = a.dim / 8, padded = groups * lanes;
+    const uint32_t all = (uint32_t)a.rows * padded;
+    Vec g[kGroupVecs], u[kGroupVecs];
+    int row[kGroupVecs], at[kGroupVecs];
+#pragma unroll
+    for (int i = 0; i < kGroupVecs; ++i) {
+        const uint32_t n = (blockIdx.x * kGroupVecs + i) * kGroupThreads + threadIdx.x;
+        row[i] = n < all ? (int)row_vecs.of(n) : -1;
+        at[i] = (int)n - row[i] * padded;
+        g[i].v = u[i].v = make_uint4(0, 0, 0, 0);
+        if (row[i] >= 0 && at[i] < vecs) {
+            const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + (int64_t)row[i] * a.x_stride) + at[i];
+            g[i].v = __ldcs(x);
+            u[i].v = __ldcs(x + vecs);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kGroupVecs; ++i) {
+        float y[8];
+        float top = values<T>(g[i], u[i], y, 0.0f);
+#pragma unroll
+        for (int d = 16; d; d /= 2)
+            if (d < lanes) top = top_of(top, __shfl_xor_sync(~0u, top, d));
+        if (row[i] < 0 || at[i] >= vecs) continue;
+        const float2 s = scale_of(top);
+        reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + (int64_t)row[i] * a.dim)[at[i]] = rounded(y, s);
+        if (at[i] % lanes == 0) a.scales[(int64_t)row[i] * groups + at[i] / lanes] = s.x;
+    }
+}
+
+// A block to a row that is one group, V vectors to a thread.
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) row_kernel(const ar_silu_mul_fp8_args a) {
+    after_the_stream();
+    __shared__ float tops[32];
+    const int vecs = a.dim / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = blockIdx.x;
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + row * a.x_stride);
+    Vec g[V], u[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int at = i * blockDim.x + threadIdx.x;
+        g[i].v = u[i].v = make_uint4(0, 0, 0, 0);
+        if (at < vecs) {
+            g[i].v = __ldcs(x + at);
+            u[i].v = __ldcs(x + vecs + at);
+        }
+    }
+    float y[V][8], top = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) top = values<T>(g[i], u[i], y[i], top);
+#pragma unroll
+    for (int d = 16; d; d /= 2) top = top_of(top, __shfl_xor_sync(~0u, top, d));
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+    top = lane < blockDim.x / 32 ? tops[lane] : 0.0f;
+#pragma unroll
+    for (int d = 16; d; d /= 2) top = top_of(top, __shfl_xor_sync(~0u, top, d));
+    const float2 s = scale_of(top);
+    uint2 *out = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + row * a.dim);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int at = i * blockDim.x + threadIdx.x;
+        if (at < vecs) out[at] = rounded(y[i], s);
+    }
+    if (threadIdx.x == 0) a.scales[row] = s.x;
+}
 
 // Blocks go from group to group, any size and alignment: once over it for the maximum, once for the output.
 template <typename T>
@@ -47,8 +197,20 @@ __global__ void __launch_bounds__(128) any_group_kernel(const ar_silu_mul_fp8_ar
 
 template <typename T>
 cudaError_t start(const ar_silu_mul_fp8_args &a, cudaStream_t s) {
-    const int64_t groups = a.rows * (a.group ? (a.dim + a.group - 1) / a.group : 1);
-    return launch_next(any_group_kernel<T>, dim3((unsigned)std::min(groups, (int64_t)1 << 20)), 128, 0, s, 0, a);
+    const int group = a.group ? a.group : a.dim, groups = a.group ? (a.dim + a.group - 1) / a.group : 1, vecs = a.dim / 8;
+    // Vectors need rows on 16 bytes, and an output on 8.
+    if (a.dim > 0 && a.dim % 8 == 0 && !misaligned(a.x, 16) && a.x_stride % 8 == 0 && !misaligned(a.out, 8)) {
+        if (group <= 256 && group >= 8 && !(group & (group - 1))) {
+            const int64_t all = a.rows * groups * (group / 8), each = kGroupThreads * kGroupVecs;
+            if (all < 0x7fff0000)          // (2^34 channels)
+                return launch_next(groups_kernel<T>, dim3((unsigned)((all + each - 1) / each)), kGroupThreads, 0, s, 0, a, group / 8, groups,
+                                   Divisor((uint32_t)(groups * (group / 8))));
+        } else if (groups == 1 && vecs <= 4096) {
+            const int v = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4, threads = ((vecs + v - 1) / v + 31) / 32 * 32;
+            return launch_next(v == 1 ? row_kernel<T, 1> : v == 2 ? row_kernel<T, 2> : row_kernel<T, 4>, dim3((unsigned)a.rows), threads, 0, s, 0, a);
+        }
+    }
+    return launch_next(any_group_kernel<T>, dim3((unsigned)std::min(a.rows * groups, (int64_t)1 << 20)), 128, 0, s, 0, a);
 }
 
 }  // namespace

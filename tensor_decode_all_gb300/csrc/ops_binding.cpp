@@ -538,6 +538,11 @@ PyObject *route(PyObject *const *o) {
     a.logits = logits.data_ptr(); a.weights = static_cast<float *>(out[0].data_ptr()); a.expert_ids = p(out[1]); a.offsets = p(out[2]);
     a.rows = p(out[3]); a.place = p(out[4]); a.logits_stride = logits.stride(0); a.tokens = T;
     a.dtype = type == at::kFloat ? AR_F32 : code_16("logits", logits); a.experts = (int32_t)std::min(E, kInt); a.chosen = (int32_t)k; a.normalize = normalize;
+    Tensor counts;
+    if (const size_t bytes = ar_route_experts_workspace(&a)) {
+        counts = make({(int64_t)(bytes / sizeof(int32_t))}, at::kInt, logits);
+        a.workspace = p(counts);
+    }
     const int rc = ar_route_experts(&a, stream_of(dev));
     if (rc) return fail(rc, "ar_route_experts");
     return o[3] != Py_None ? (Py_INCREF(o[3]), o[3]) : tuple_of({&out[0], &out[1], &out[2], &out[3], &out[4]});

@@ -36,7 +36,7 @@ class MatmulFp8Args(ctypes.Structure):
 
 class RouteExpertsArgs(ctypes.Structure):
     _fields_ = [("logits", _P), ("weights", _P), ("expert_ids", _P), ("offsets", _P), ("rows", _P), ("place", _P),
-                ("logits_stride", _I64), ("tokens", _I64),
+                ("workspace", _P), ("logits_stride", _I64), ("tokens", _I64),
                 ("dtype", _I32), ("experts", _I32), ("chosen", _I32), ("normalize", _I32)]
 
 
@@ -67,6 +67,8 @@ def _ffn():
             f.argtypes = [_P, _P]
             f.restype = ctypes.c_int
         L.ar_matmul_fp8_status.argtypes = []
+        L.ar_route_experts_workspace.argtypes = [_P]
+        L.ar_route_experts_workspace.restype = ctypes.c_size_t
         _lib = L
     return _lib
 

@@ -21,7 +21,7 @@ def lib():
 
 def test_symbols_are_declared_and_exported(lib):
     names = tda.declared_symbols(os.path.join(ar._build.INCLUDE, "ar_ffn.h"))
-    assert set(names) == {"ar_matmul_fp8", "ar_matmul_fp8_status", "ar_route_experts", "ar_silu_mul_fp8", "ar_experts_sum"}
+    assert set(names) == {"ar_matmul_fp8", "ar_matmul_fp8_status", "ar_route_experts", "ar_route_experts_workspace", "ar_silu_mul_fp8", "ar_experts_sum"}
     assert set(names) <= set(tda.declared_symbols())
     for n in names:
         assert hasattr(lib, n)
@@ -61,7 +61,7 @@ def _matmul(**kw):
 
 
 def _route(**kw):
-    base = dict(logits=A, weights=A, expert_ids=A, offsets=A, rows=A, place=A, logits_stride=8, tokens=3, dtype=4, experts=8, chosen=2, normalize=1)
+    base = dict(logits=A, weights=A, expert_ids=A, offsets=A, rows=A, place=A, workspace=A, logits_stride=8, tokens=3, dtype=4, experts=8, chosen=2, normalize=1)
     return ffn.RouteExpertsArgs(**{**base, **kw})
 
 
@@ -90,7 +90,8 @@ def test_matmul_refusals(lib, kw, code):
     (dict(place=None), 1), (dict(logits=A + 2), 1), (dict(weights=A + 2), 1), (dict(expert_ids=A + 1), 1), (dict(offsets=A + 1), 1),
     (dict(rows=A + 2), 1), (dict(place=A + 2), 1), (dict(dtype=3), 1), (dict(dtype=5), 1), (dict(tokens=-1), 1), (dict(experts=0, chosen=0), 1),
     (dict(chosen=0), 1), (dict(chosen=9), 1), (dict(normalize=2), 1), (dict(experts=1025), 2), (dict(experts=64, chosen=33), 2),
-    (dict(tokens=(1 << 29) + 1), 2)])
+    (dict(tokens=(1 << 29) + 1), 2), (dict(tokens=1000, workspace=None), 1),
+    (dict(tokens=1000, workspace=A + 2), 1)])
 def test_route_refusals(lib, kw, code):
     assert _rc(lib, "ar_route_experts", _route(**kw)) == code
 
@@ -109,6 +110,17 @@ def test_silu_refusals(lib, kw, code):
     (dict(chosen=-1), 1), (dict(rows=(1 << 30) + 1), 2), (dict(tokens=(1 << 30) + 1), 2), (dict(dim=(1 << 20) + 1), 2), (dict(chosen=1025), 2)])
 def test_sum_refusals(lib, kw, code):
     assert _rc(lib, "ar_experts_sum", _sum(**kw)) == code
+
+
+def test_the_routers_workspace(lib):
+    """None for what one block does, nor for what a sort does; else four bytes to an expert and block."""
+    def size(**kw):
+        return lib.ar_route_experts_workspace(ctypes.addressof(_route(**kw)))
+    assert size(tokens=3) == 0 and size(tokens=0) == 0 and size(tokens=64) == 0
+    assert size(tokens=8191, experts=256, chosen=8) == 128 * 256 * 4
+    assert size(tokens=1 << 27, experts=256, chosen=8) == 0
+    assert size(tokens=100, experts=2000) == 0 and size(tokens=100, chosen=0) == 0
+    assert lib.ar_route_experts_workspace(None) == 0
 
 
 def test_null_and_empty_calls(lib):

@@ -255,6 +255,15 @@ def test_routes(T, E, k, dtype, normalize):
     _check_route(_tda().route_experts(x.cuda(), k, normalize=normalize), x, k, normalize)
 
 
+@pytest.mark.parametrize("T,E,k", [(65, 16, 16), (64, 1000, 16), (200, 700, 32), (2049, 513, 3), (33000, 12, 8), (5000, 7, 7)])
+def test_routes_of_many_tokens(T, E, k):
+    """In one block, in many, and past what those take; a column of equal logits, and tokens without an expert."""
+    x = torch.randn(T, E, generator=H.gen(T)).half()
+    x[:, E // 2] = 1.0
+    x[T // 3:T // 3 + 5] = -math.inf
+    _check_route(_tda().route_experts(x.cuda(), k), x, k, True)
+
+
 @pytest.mark.parametrize("normalize", [True, False])
 def test_routes_of_special_logits(normalize):
     inf, nan = math.inf, math.nan
@@ -278,6 +287,18 @@ def test_routes_of_special_logits(normalize):
         _check_route(r, x, k, normalize)
     assert r.experts[0].tolist() == [-1] * 6 and r.weights[0].tolist() == [0.0] * 6
     assert (r.rows[r.offsets[-1]:] == -1).all() and len(r.rows) > r.offsets[-1]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_routes_of_special_short_logits(dtype):
+    """16-bit types' ends: infinities beside their largest number, subnormals, zeros of both signs, NaN of both signs."""
+    dt = H.DT[dtype]
+    big, tiny = torch.finfo(dt).max, torch.finfo(dt).smallest_normal / 4
+    row = [0.0, -0.0, math.nan, -math.nan, math.inf, -math.inf, big, -big, tiny, -tiny, 1.0, -1.0] + [0.5] * 21
+    x = torch.tensor([row, row[::-1], [-v for v in row], [v if v == v and abs(v) < 1 else -math.inf for v in row]]).to(dt)
+    for k in (1, 5, 12, 32):
+        _check_route(_tda().route_experts(x.cuda(), k), x, k, True)
+        _check_route(_tda().route_experts(x.cuda(), k, normalize=False), x, k, False)
 
 
 def test_routes_of_no_tokens_and_strided_logits():
