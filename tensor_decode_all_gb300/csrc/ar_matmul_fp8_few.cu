@@ -8,8 +8,8 @@
 // scales by word copies beside them, all to one barrier a stage.  Rows that are picked by number come four at a time.
 //
 // Where there are fewer tiles than the GPU has room for, a cluster of blocks shares a tile's channels: each block
-// sums its part, deals its sums out to the cluster's shared memory by columns, and adds up its own columns in
-// the blocks' order.
+// sums its part and leaves its sums in its shared memory, and each adds up some of the rows from all blocks, in their
+// order.
 #include "ar_matmul_fp8.cuh"
 #include "ar_tensor.cuh"
 
@@ -24,30 +24,34 @@ template <int TOK> struct Few {
     static constexpr int WeightBytes = kBlock * kBlock, RowBytes = TOK * kBlock, ScaleBytes = (TOK + 4) * 4;
     static constexpr int Buffers = TOK <= 64 ? 4 : 2;                 // of sums in tensor memory
     static constexpr int Columns = TOK * Buffers;
-    static constexpr int StageBytes = WeightBytes + RowBytes + ScaleBytes;
-    static constexpr int Stages = 112 * 1024 / StageBytes;            // two blocks to a multiprocessor
-    static constexpr int Smem = Stages * StageBytes + (2 * Stages + 2 * Buffers) * 8 + 16 + 1024;
+    static constexpr int StageBytes = WeightBytes + RowBytes;
+    static constexpr int Stages = (112 * 1024 - 4 * ScaleBytes) / (StageBytes + ScaleBytes);        // two blocks to a multiprocessor
+    // A stage is free when the matrix instructions have read it, its scales when they have been multiplied by: up to
+    // `Buffers` groups later.
+    static constexpr int Scales = Stages + Buffers;
+    static constexpr int Smem = Stages * StageBytes + Scales * ScaleBytes + (2 * Stages + Scales + 2 * Buffers) * 8 + 16 + 1024;
 };
 
 template <int TOK>
 __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_constant__ Product p, const __grid_constant__ CUtensorMap weight,
                                                              const __grid_constant__ CUtensorMap x, int cluster, int row_tiles) {
     using F = Few<TOK>;
-    constexpr int S = F::Stages, B = F::Buffers;
+    constexpr int S = F::Stages, B = F::Buffers, Q = F::Scales;
     extern __shared__ uint8_t raw[];
     const ar_matmul_fp8_args &a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t base = (shared_address(raw) + 1023) & ~1023u;
     const uint32_t weights = base, rows_at = weights + S * F::WeightBytes, scales = rows_at + S * F::RowBytes;
-    const uint32_t full = scales + S * F::ScaleBytes, empty = full + S * 8, sums_full = empty + S * 8, sums_empty = sums_full + B * 8;
+    const uint32_t full = scales + Q * F::ScaleBytes, empty = full + S * 8, scaled = empty + S * 8, sums_full = scaled + Q * 8, sums_empty = sums_full + B * 8;
     const uint32_t tmem_at = sums_empty + B * 8;
     uint8_t *const shared = raw + (base - shared_address(raw));
     if (warp == 0) {
         if (lane == 0) {
             for (int i = 0; i < S; ++i) {
-                bar_init(full + 8 * i, 33);            // the bulk copies' thread, and each lane's word copies
-                bar_init(empty + 8 * i, 4);
+                bar_init(full + 8 * i, 1);
+                bar_init(empty + 8 * i, 1);
             }
+            for (int i = 0; i < Q; ++i) bar_init(scaled + 8 * i, 32);      // each lane's copies
             for (int i = 0; i < B; ++i) {
                 bar_init(sums_full + 8 * i, 1);
                 bar_init(sums_empty + 8 * i, 4);
@@ -80,6 +84,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_consta
     Rows rows = {0, 0, 0};
 
     if (warp == 0) {
+        Ring<S> stage;
+        Ring<Q> words_of;
         int issued = 0;
         for (int64_t u = blockIdx.x / cluster; fine; u += step) {
             rows = tile_of(u, feature);
@@ -101,10 +107,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_consta
                 scale[i] = r >= 0 ? a.x_scales + r * a.x_scales_stride : nullptr;
             }
             const float *weight_scale = a.weight_scales + ((int64_t)rows.expert * features + feature / kBlock) * p.groups;
-            for (int k = k0; k < k1; ++k, ++issued) {
-                const int s = issued % S;
-                if (!(fine = bar_wait_warp(empty + 8 * s, (issued / S & 1) ^ 1))) break;
-                const uint32_t bar = full + 8 * s, to = rows_at + s * F::RowBytes, words = scales + s * F::ScaleBytes;
+            for (int k = k0; k < k1; ++k, ++issued, stage.next(), words_of.next()) {
+                const uint32_t s = stage.at;
+                if (!(fine = bar_wait_warp(empty + 8 * s, stage.parity ^ 1))) break;
+                const uint32_t bar = full + 8 * s, to = rows_at + s * F::RowBytes, words = scales + words_of.at * F::ScaleBytes;
                 if (lane == 0) {
                     bar_expect(bar, F::WeightBytes + F::RowBytes);
                     tensor_load(weights + s * F::WeightBytes, &weight, bar, k * kBlock, feature, rows.expert);
@@ -116,27 +122,32 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_consta
                 for (int i = 0; i < (TOK + 31) / 32; ++i)
                     if (TOK >= 32 || lane < TOK)
                         copy_word(words + 4 * (lane + 32 * i), scale[i] ? scale[i] + (a.x_row_scales ? 0 : k) : a.x_scales, scale[i] != nullptr);
-                bar_arrive_copies(bar);
+                bar_arrive_copies(scaled + 8 * words_of.at);
                 __syncwarp();
             }
         }
         if (!fine)                                     // what is under way has to land before the block may end
-            for (int i = max(issued - S, 0); i < issued; ++i) (void)bar_wait_warp(full + 8 * (i % S), i / S & 1);
+            for (int i = max(issued - S, 0); i < issued; ++i)
+                (void)(bar_wait_warp(full + 8 * (i % S), i / S & 1) && bar_wait_warp(scaled + 8 * (i % Q), i / Q & 1));
     } else if (warp == 1) {
+        const uint64_t weights_operand = operand_of(weights), rows_operand = operand_of(rows_at);
+        const bool one = elected();
+        Ring<S> stage;
+        Ring<B> buffer;
         int n = 0;
         for (int64_t u = blockIdx.x / cluster; fine; u += step) {
             rows = tile_of(u, feature);
             if (rows.count == 0 || (any && cluster > 1)) break;
             any = true;
-            for (int k = k0; k < k1; ++k, ++n) {
-                const int s = n % S, b = n % B;
-                if (!(fine = bar_wait_warp(sums_empty + 8 * b, (n / B & 1) ^ 1) && bar_wait_warp(full + 8 * s, n / S & 1))) break;
+            for (int k = k0; k < k1; ++k, ++n, stage.next(), buffer.next()) {
+                if (!(fine = bar_wait_warp(full + 8 * stage.at, stage.parity, sums_empty + 8 * buffer.at, buffer.parity ^ 1))) break;
                 tmem_after_sync();
-                if (lane == 0) {
-                    const uint64_t w = operand_of(weights + s * F::WeightBytes), r = operand_of(rows_at + s * F::RowBytes);
+                if (one) {
+                    const uint64_t w = weights_operand + stage.at * (F::WeightBytes >> 4), r = rows_operand + stage.at * (F::RowBytes >> 4);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) mma_e4m3(tmem + b * TOK, w + 2 * i, r + 2 * i, product_shape(kBlock, TOK), i > 0);
-                    mma_commit(sums_full + 8 * b);
+                    for (int i = 0; i < 4; ++i) mma_e4m3(tmem + buffer.at * TOK, w + 2 * i, r + 2 * i, product_shape(kBlock, TOK), i > 0);
+                    mma_commit(empty + 8 * stage.at);
+                    mma_commit(sums_full + 8 * buffer.at);
                 }
                 __syncwarp();
             }
@@ -145,82 +156,116 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_consta
             for (int i = max(n - B, 0); i < n; ++i) (void)bar_wait_warp(sums_full + 8 * (i % B), i / B & 1);
     } else {
         const int quarter = warp & 3, mine = quarter * 32 + lane;
-        int n = 0;
+        const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
+        Ring<Q> words_of;
+        Ring<B> buffer;
         for (int64_t u = blockIdx.x / cluster; fine; u += step) {
             rows = tile_of(u, feature);
             if (rows.count == 0 || (any && cluster > 1)) break;
             any = true;
-            float sum[TOK];
+            // which rows have one of x (a bit each)
+            unsigned there[(TOK + 31) / 32];
 #pragma unroll
-            for (int j = 0; j < TOK; ++j) sum[j] = 0;
-            for (int k = k0; k < k1; ++k, ++n) {
-                const int s = n % S, b = n % B;
-                // (the stage's own barrier too: the scales are ordinary copies)
-                if (!(fine = bar_wait_warp(sums_full + 8 * b, n / B & 1) && bar_wait_warp(full + 8 * s, n / S & 1))) break;
+            for (int i = 0; i < (TOK + 31) / 32; ++i) {
+                there[i] = ~0u;
+                if (a.row_of) there[i] = __ballot_sync(~0u, i * 32 + lane < rows.count && source_row(a, rows.first + i * 32 + lane) >= 0);
+            }
+            auto real = [&](int row) {
+                unsigned bits = there[0];
+#pragma unroll
+                for (int i = 1; i < (TOK + 31) / 32; ++i)
+                    if (row >> 5 == i) bits = there[i];
+                return bits >> (row & 31) & 1;
+            };
+            unsigned long long sum[TOK / 2];
+#pragma unroll
+            for (int j = 0; j < TOK / 2; ++j) sum[j] = 0;
+            for (int k = k0; k < k1; ++k, words_of.next(), buffer.next()) {
+                if (!(fine = bar_wait_warp(scaled + 8 * words_of.at, words_of.parity, sums_full + 8 * buffer.at, buffer.parity))) break;
                 tmem_after_sync();
-                const float *words = reinterpret_cast<const float *>(shared + (scales - base) + s * F::ScaleBytes);
-                const float sw = words[TOK];
-                constexpr int W = TOK < 32 ? TOK : 32;
+                const float *words = reinterpret_cast<const float *>(shared + (scales - base)) + words_of.at * (F::ScaleBytes / 4);
+                const unsigned long long sw = pair_of_floats(words[TOK], words[TOK]);
+                constexpr int W = TOK == 16 || TOK == 128 ? 16 : 32;      // (128 sums leave no room for 32 more)
 #pragma unroll
                 for (int j = 0; j < TOK; j += W) {
                     float v[W];
-                    tmem_load(tmem + ((uint32_t)(quarter * 32) << 16) + b * TOK + j, v);
+                    tmem_load(from + buffer.at * TOK + j, v);
                     tmem_wait_loads(v);
 #pragma unroll
                     for (int i = 0; i < W; i += 4) {
                         const float4 sx = *reinterpret_cast<const float4 *>(words + j + i);
-                        sum[j + i] = fmaf(v[i], sx.x * sw, sum[j + i]);
-                        sum[j + i + 1] = fmaf(v[i + 1], sx.y * sw, sum[j + i + 1]);
-                        sum[j + i + 2] = fmaf(v[i + 2], sx.z * sw, sum[j + i + 2]);
-                        sum[j + i + 3] = fmaf(v[i + 3], sx.w * sw, sum[j + i + 3]);
+                        fma2(sum[(j + i) / 2], pair_of_floats(v[i], v[i + 1]), mul2(pair_of_floats(sx.x, sx.y), sw));
+                        fma2(sum[(j + i) / 2 + 1], pair_of_floats(v[i + 2], v[i + 3]), mul2(pair_of_floats(sx.z, sx.w), sw));
                     }
                 }
                 tmem_before_sync();
                 __syncwarp();
-                if (lane == 0) {
-                    bar_arrive(sums_empty + 8 * b);
-                    bar_arrive(empty + 8 * s);
-                }
+                if (lane == 0) bar_arrive(sums_empty + 8 * buffer.at);
             }
             if (!fine) break;
+            auto store = [&](int row, float v) {
+                if (row < rows.count && feature + mine < a.out_dim) {
+                    const int64_t at = (rows.first + row) * a.out_stride + feature + mine;
+                    if (a.dtype == AR_F16) static_cast<__half *>(a.out)[at] = __float2half_rn(v);
+                    else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
+                }
+            };
             if (cluster > 1) {
-                // (one tile to a cluster: nothing follows in the stages' memory)
+                // Own sums to own memory (one tile to a cluster: nothing follows in the stages), four rows of a feature side
+                // by side; then this block's rows from all blocks, added in their order.
+#pragma unroll
+                for (int j = 0; j < TOK; j += 4) {
+                    const float2 lo = floats_of(sum[j / 2]), hi = floats_of(sum[j / 2 + 1]);
+                    *reinterpret_cast<float4 *>(shared + ((j / 4) * kBlock + mine) * 16) = make_float4(lo.x, lo.y, hi.x, hi.y);
+                }
                 __syncwarp();
                 cluster_sync_all();
                 const int each = TOK / cluster;
+                if (each >= 4) {
+                    // all loads of up to 64 rows together: four rows of block i % cluster, the blocks' in turn
+                    const int ways = __ffs(cluster) - 1;
 #pragma unroll
-                for (int j = 0; j < TOK; ++j)
-                    cluster_store(cluster_address(base + ((rank * each + j % each) * kBlock + mine) * 4, j / each), sum[j]);
-                __syncwarp();
-                cluster_sync_all();
-                const float *parts = reinterpret_cast<const float *>(shared);
-#pragma unroll 1
-                for (int j = 0; j < each; ++j) {
-                    float v = parts[j * kBlock + mine];
-                    for (int r = 1; r < cluster; ++r) v += parts[(r * each + j) * kBlock + mine];
-                    const int row = rank * each + j;
-                    if (row < rows.count && feature + mine < a.out_dim) {
-                        if (a.row_of && source_row(a, rows.first + row) < 0) v = 0;
-                        const int64_t at = (rows.first + row) * a.out_stride + feature + mine;
-                        if (a.dtype == AR_F16) static_cast<__half *>(a.out)[at] = __float2half_rn(v);
-                        else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
+                    for (int i0 = 0; i0 < TOK / 4; i0 += 16) {
+                        constexpr int N = TOK / 4 < 16 ? TOK / 4 : 16;
+                        float4 v[N];
+#pragma unroll
+                        for (int i = 0; i < N; ++i)
+                            v[i] = cluster_load4(cluster_address(base + ((rank * (each / 4) + ((i0 + i) >> ways)) * kBlock + mine) * 16, (i0 + i) & (cluster - 1)));
+                        float4 w = v[0];
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            const int r = (i0 + i) & (cluster - 1), row = rank * each + 4 * ((i0 + i) >> ways);
+                            w = r == 0 ? v[i] : make_float4(w.x + v[i].x, w.y + v[i].y, w.z + v[i].z, w.w + v[i].w);
+                            if (r == cluster - 1) {
+                                store(row, real(row) ? w.x : 0.0f);
+                                store(row + 1, real(row + 1) ? w.y : 0.0f);
+                                store(row + 2, real(row + 2) ? w.z : 0.0f);
+                                store(row + 3, real(row + 3) ? w.w : 0.0f);
+                            }
+                        }
+                    }
+                } else {
+                    for (int row = rank * each; row < (rank + 1) * each; ++row) {
+                        const uint32_t at = base + ((row / 4) * kBlock + mine) * 16 + row % 4 * 4;
+                        float v[16];
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) v[r] = r < cluster ? cluster_load(cluster_address(at, r)) : 0.0f;
+#pragma unroll
+                        for (int r = 1; r < 16; ++r)
+                            if (r < cluster) v[0] += v[r];
+                        store(row, real(row) ? v[0] : 0.0f);
                     }
                 }
+                __syncwarp();
+                cluster_sync_all();           // (the others have read)
                 joined = true;
                 break;
             }
 #pragma unroll
-            for (int j0 = 0; j0 < TOK; j0 += 32) {
-                unsigned there = ~0u;
-                if (a.row_of) there = __ballot_sync(~0u, j0 + lane < rows.count && source_row(a, rows.first + j0 + lane) >= 0);
-#pragma unroll
-                for (int j = j0; j < j0 + 32 && j < TOK; ++j)
-                    if (j < rows.count && feature + mine < a.out_dim) {
-                        const float v = there >> (j - j0) & 1 ? sum[j] : 0.0f;
-                        const int64_t at = (rows.first + j) * a.out_stride + feature + mine;
-                        if (a.dtype == AR_F16) static_cast<__half *>(a.out)[at] = __float2half_rn(v);
-                        else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
-                    }
+            for (int j = 0; j < TOK; j += 2) {
+                const float2 v = floats_of(sum[j / 2]);
+                store(j, there[j / 32] >> (j & 31) & 1 ? v.x : 0.0f);
+                store(j + 1, there[j / 32] >> (j & 31) & 2 ? v.y : 0.0f);
             }
         }
     }

@@ -26,21 +26,10 @@ constexpr int kManyThreads = 384;             // a warpgroup for copies, instruc
 // Registers a thread: 168 at the start, 384 * 168 = 128 * 72 + 256 * 216.
 constexpr int kRegistersMoving = 72, kRegistersAdding = 216;
 constexpr int kTileRows = 256, kTileFeatures = 256;
-constexpr int kManyStages = 6, kOperandBytes = kBlock * kBlock, kManyScaleBytes = (kBlock + 4) * 4, kTiles = 4;
-constexpr int kManyStageBytes = 2 * kOperandBytes + kManyScaleBytes;
-constexpr int kManySmem = kManyStages * kManyStageBytes + kTiles * 16 + (3 * kManyStages + 4 + 2 * kTiles) * 8 + 16 + 1024;
+// A stage is free when the matrix instructions have read it, its scales when they have been multiplied by: up to two groups later.
+constexpr int kManyStages = 6, kManyScales = kManyStages + 2, kOperandBytes = kBlock * kBlock, kManyScaleBytes = (kBlock + 4) * 4, kTiles = 4;
+constexpr int kManySmem = kManyStages * 2 * kOperandBytes + kManyScales * kManyScaleBytes + kTiles * 16 + (2 * kManyStages + kManyScales + 4 + 2 * kTiles) * 8 + 16 + 1024;
 constexpr int kRowTilesTogether = 8;
-
-__device__ __forceinline__ unsigned long long pair_of_floats(float a, float b) {
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 floats_of(unsigned long long v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
 
 // What the pair does next: rows first .. first + count - 1 of the call (both blocks'), features from `feature` on.  Count 0: no more.
 struct Tile {
@@ -49,15 +38,15 @@ struct Tile {
 
 __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_constant__ Product p, const __grid_constant__ CUtensorMap weight,
                                                                const __grid_constant__ CUtensorMap x) {
-    constexpr int S = kManyStages;
+    constexpr int S = kManyStages, Q = kManyScales;
     extern __shared__ uint8_t raw[];
     const ar_matmul_fp8_args &a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t base = (shared_address(raw) + 1023) & ~1023u;
-    const uint32_t rows_at = base, weights = rows_at + S * kOperandBytes, scales = weights + S * kOperandBytes, tiles_at = scales + S * kManyScaleBytes;
+    const uint32_t rows_at = base, weights = rows_at + S * kOperandBytes, scales = weights + S * kOperandBytes, tiles_at = scales + Q * kManyScaleBytes;
     // full: block 0's, both blocks' operands; scaled: the scales; empty: a stage's; sums_full, sums_empty (block 0's): the halves of
     // tensor memory; known, used: the next tiles
-    const uint32_t full = tiles_at + kTiles * 16, scaled = full + S * 8, empty = scaled + S * 8, sums_full = empty + S * 8, sums_empty = sums_full + 16;
+    const uint32_t full = tiles_at + kTiles * 16, scaled = full + S * 8, empty = scaled + Q * 8, sums_full = empty + S * 8, sums_empty = sums_full + 16;
     const uint32_t known = sums_empty + 16, used = known + kTiles * 8, tmem_at = used + kTiles * 8;
     uint8_t *const shared = raw + (base - shared_address(raw));
     volatile Tile *const tiles = reinterpret_cast<volatile Tile *>(shared + (tiles_at - base));
@@ -66,9 +55,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
         if (lane == 0) {
             for (int i = 0; i < S; ++i) {
                 bar_init(full + 8 * i, 1);
-                bar_init(scaled + 8 * i, 32);
-                bar_init(empty + 8 * i, 8);
+                bar_init(empty + 8 * i, 1);
             }
+            for (int i = 0; i < Q; ++i) bar_init(scaled + 8 * i, 32);      // each lane's copies
             for (int i = 0; i < 2; ++i) {
                 bar_init(sums_full + 8 * i, 1);
                 bar_init(sums_empty + 8 * i, 16);
@@ -110,6 +99,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
         if (warp == 0) {
             const uint32_t full_of_0 = cluster_address(full, 0);
             Ring<S> stage;
+            Ring<Q> words_of;
             int issued = 0;
             while (fine) {
                 const Tile tile = next_tile();
@@ -134,10 +124,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
                 // the weight's scales of both halves, by two lanes
                 const int half = tile.feature / kBlock + lane;
                 const float *weight_scale = lane < 2 && half < blocks ? a.weight_scales + ((int64_t)tile.expert * blocks + half) * p.groups : nullptr;
-                for (int k = 0; k < p.groups; ++k, ++issued, stage.next()) {
+                for (int k = 0; k < p.groups; ++k, ++issued, stage.next(), words_of.next()) {
                     const uint32_t s = stage.at;
                     if (!(fine = bar_wait_warp(empty + 8 * s, stage.parity ^ 1))) break;
-                    const uint32_t bar = full_of_0 + 8 * s, to = rows_at + s * kOperandBytes, words = scales + s * kManyScaleBytes;
+                    const uint32_t bar = full_of_0 + 8 * s, to = rows_at + s * kOperandBytes, words = scales + words_of.at * kManyScaleBytes;
                     if (lane == 0) {
                         if (rank == 0) bar_expect(full + 8 * s, 4 * kOperandBytes);
                         pair_tensor_load(weights + s * kOperandBytes, &weight, bar, k * kBlock, tile.feature + rank * kBlock, tile.expert);
@@ -147,12 +137,12 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
 #pragma unroll
                     for (int i = 0; i < 4; ++i) copy_word(words + 4 * (lane + 32 * i), scale[i] ? scale[i] + (a.x_row_scales ? 0 : k) : a.x_scales, scale[i] != nullptr);
                     if (lane < 2) copy_word(words + 4 * (kBlock + lane), weight_scale ? weight_scale + k : a.weight_scales, weight_scale != nullptr);
-                    bar_arrive_copies(scaled + 8 * s);
+                    bar_arrive_copies(scaled + 8 * words_of.at);
                     __syncwarp();
                 }
             }
             if (!fine) {                                   // what is under way has to land before the blocks may end
-                for (int i = max(issued - S, 0); i < issued; ++i) (void)bar_wait_warp(scaled + 8 * (i % S), i / S & 1);
+                for (int i = max(issued - S, 0); i < issued; ++i) (void)bar_wait_warp(scaled + 8 * (i % Q), i / Q & 1);
                 if (rank == 0)
                     for (int i = max(issued - S, 0); i < issued; ++i) (void)bar_wait_warp(full + 8 * (i % S), i / S & 1);
             }
@@ -178,6 +168,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
                         pair_mma_e4m3(to, r + 2, w + 2, shape, true);
                         pair_mma_e4m3(to, r + 4, w + 4, shape, true);
                         pair_mma_e4m3(to, r + 6, w + 6, shape, true);
+                        pair_mma_commit(empty + 8 * stage.at);
                         pair_mma_commit(sums_full + 8 * half.at);
                     }
                     __syncwarp();
@@ -235,7 +226,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
         const uint32_t empty_of_0 = cluster_address(sums_empty, 0);
         // stores of 32, 16 and 2 bytes
         const int wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride % 16 == 0 ? 16 : reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_stride % 8 == 0 ? 8 : 1;
-        Ring<S> stage;
+        Ring<Q> words_of;
         Ring<2> sums;
         // (written out for either width: one loop that asks which keeps its sums in registers a third as fast)
         auto take = [&](const Tile &tile, auto short_tile) {
@@ -250,13 +241,12 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
             unsigned long long sum[kOwn / 2];
 #pragma unroll
             for (int j = 0; j < kOwn / 2; ++j) sum[j] = 0;
-            for (int k = 0; k < p.groups; ++k, stage.next(), sums.next()) {
-                if (!(fine = bar_wait_warp(scaled + 8 * stage.at, stage.parity))) return;
-                const float *words = reinterpret_cast<const float *>(shared + (scales - base)) + stage.at * (kManyScaleBytes / 4);
+            for (int k = 0; k < p.groups; ++k, words_of.next(), sums.next()) {
+                if (!(fine = bar_wait_warp(scaled + 8 * words_of.at, words_of.parity))) return;
+                const float *words = reinterpret_cast<const float *>(shared + (scales - base)) + words_of.at * (kManyScaleBytes / 4);
                 const float f = words[mine] * words[kBlock + block];
                 if (!(fine = bar_wait_warp(sums_full + 8 * sums.at, sums.parity))) return;
                 tmem_after_sync();
-                if (lane == 0) bar_arrive(empty + 8 * stage.at);      // (the sums are there: nothing reads the stage any more)
                 // 16 columns are on their way while the 16 before are multiplied and added
                 const unsigned long long both = pair_of_floats(f, f);
                 const uint32_t at = from + sums.at * kTileFeatures;
@@ -268,7 +258,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
                     if (j < kOwn / 16 - 1) tmem_load(at + (j + 1) * 16, v[(j + 1) & 1]);
 #pragma unroll
                     for (int i = 0; i < 16; i += 2)
-                        asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(sum[j * 8 + i / 2]) : "l"(pair_of_floats(v[j & 1][i], v[j & 1][i + 1])), "l"(both));
+                        fma2(sum[j * 8 + i / 2], pair_of_floats(v[j & 1][i], v[j & 1][i + 1]), both);
                     if (j < kOwn / 16 - 1) tmem_wait_loads(v[(j + 1) & 1]);
                 }
                 tmem_before_sync();
