@@ -2,7 +2,7 @@
 //
 // 128 features of the weight are the matrix instruction's lanes, up to TOK rows its columns, so that few rows leave
 // little of it empty: per group of 128 channels four tcgen05.mma sum the group's products in tensor memory,
-// and four warps, a feature to a thread, multiply what came out by the two scales and add it up in registers.
+// and four warps (eight), a feature to a thread, multiply what came out by the two scales and add it up in registers.
 //
 // A warp copies, another issues the instructions; weight tiles (16 KB) and rows come by bulk tensor copies, the
 // scales by word copies beside them, all to one barrier a stage.  Rows that are picked by number come four at a time.
@@ -10,6 +10,8 @@
 // Where there are fewer tiles than the GPU has room for, a cluster of blocks shares a tile's channels: each block
 // sums its part and leaves its sums in its shared memory, and each adds up some of the rows from all blocks, in their
 // order.
+#include <algorithm>
+
 #include "ar_matmul_fp8.cuh"
 #include "ar_tensor.cuh"
 
@@ -18,14 +20,15 @@ namespace {
 
 __device__ int g_few_status;
 
-constexpr int kFewThreads = 192;              // copies, instructions, four warps that add up
-
 template <int TOK> struct Few {
     static constexpr int WeightBytes = kBlock * kBlock, RowBytes = TOK * kBlock, ScaleBytes = (TOK + 4) * 4;
     static constexpr int Buffers = TOK <= 64 ? 4 : 2;                 // of sums in tensor memory
     static constexpr int Columns = TOK * Buffers;
     static constexpr int StageBytes = WeightBytes + RowBytes;
-    static constexpr int Stages = (112 * 1024 - 4 * ScaleBytes) / (StageBytes + ScaleBytes);        // two blocks to a multiprocessor
+    // Two blocks to a multiprocessor; with 128 rows one, whose sums are eight warps' (with four they would not fit their registers).
+    static constexpr int Blocks = TOK <= 64 ? 2 : 1, Halves = TOK <= 64 ? 1 : 2, Own = TOK / Halves;
+    static constexpr int Threads = 64 + 128 * Halves;               // copies, instructions, warps that add up
+    static constexpr int Stages = (224 * 1024 / Blocks - 4 * ScaleBytes) / (StageBytes + ScaleBytes);
     // A stage is free when the matrix instructions have read it, its scales when they have been multiplied by: up to
     // `Buffers` groups later.
     static constexpr int Scales = Stages + Buffers;
@@ -33,7 +36,7 @@ template <int TOK> struct Few {
 };
 
 template <int TOK>
-__global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_constant__ Product p, const __grid_constant__ CUtensorMap weight,
+__global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kernel(const __grid_constant__ Product p, const __grid_constant__ CUtensorMap weight,
                                                              const __grid_constant__ CUtensorMap x, int cluster, int row_tiles) {
     using F = Few<TOK>;
     constexpr int S = F::Stages, B = F::Buffers, Q = F::Scales;
@@ -54,7 +57,7 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_consta
             for (int i = 0; i < Q; ++i) bar_init(scaled + 8 * i, 32);      // each lane's copies
             for (int i = 0; i < B; ++i) {
                 bar_init(sums_full + 8 * i, 1);
-                bar_init(sums_empty + 8 * i, 4);
+                bar_init(sums_empty + 8 * i, 4 * F::Halves);
             }
             bar_init_done();
             tensor_prefetch(&weight);
@@ -155,45 +158,41 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_consta
         if (!fine)
             for (int i = max(n - B, 0); i < n; ++i) (void)bar_wait_warp(sums_full + 8 * (i % B), i / B & 1);
     } else {
-        const int quarter = warp & 3, mine = quarter * 32 + lane;
-        const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16);
+        // a feature, and `Own` of the rows, to a thread
+        constexpr int Own = F::Own;
+        const int quarter = warp & 3, mine = quarter * 32 + lane, begin = (warp - 2) / 4 * Own;
+        const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + begin;
         Ring<Q> words_of;
         Ring<B> buffer;
         for (int64_t u = blockIdx.x / cluster; fine; u += step) {
             rows = tile_of(u, feature);
             if (rows.count == 0 || (any && cluster > 1)) break;
             any = true;
-            // which rows have one of x (a bit each)
-            unsigned there[(TOK + 31) / 32];
+            // which of the rows have one of x (a bit each)
+            unsigned there[(Own + 31) / 32];
 #pragma unroll
-            for (int i = 0; i < (TOK + 31) / 32; ++i) {
+            for (int i = 0; i < (Own + 31) / 32; ++i) {
+                const int row = begin + i * 32 + lane;
                 there[i] = ~0u;
-                if (a.row_of) there[i] = __ballot_sync(~0u, i * 32 + lane < rows.count && source_row(a, rows.first + i * 32 + lane) >= 0);
+                if (a.row_of) there[i] = __ballot_sync(~0u, row < rows.count && source_row(a, rows.first + row) >= 0);
             }
-            auto real = [&](int row) {
-                unsigned bits = there[0];
+            unsigned long long sum[Own / 2];
 #pragma unroll
-                for (int i = 1; i < (TOK + 31) / 32; ++i)
-                    if (row >> 5 == i) bits = there[i];
-                return bits >> (row & 31) & 1;
-            };
-            unsigned long long sum[TOK / 2];
-#pragma unroll
-            for (int j = 0; j < TOK / 2; ++j) sum[j] = 0;
+            for (int j = 0; j < Own / 2; ++j) sum[j] = 0;
             for (int k = k0; k < k1; ++k, words_of.next(), buffer.next()) {
                 if (!(fine = bar_wait_warp(scaled + 8 * words_of.at, words_of.parity, sums_full + 8 * buffer.at, buffer.parity))) break;
                 tmem_after_sync();
                 const float *words = reinterpret_cast<const float *>(shared + (scales - base)) + words_of.at * (F::ScaleBytes / 4);
                 const unsigned long long sw = pair_of_floats(words[TOK], words[TOK]);
-                constexpr int W = TOK == 16 || TOK == 128 ? 16 : 32;      // (128 sums leave no room for 32 more)
+                constexpr int W = Own < 32 ? Own : 32;
 #pragma unroll
-                for (int j = 0; j < TOK; j += W) {
+                for (int j = 0; j < Own; j += W) {
                     float v[W];
                     tmem_load(from + buffer.at * TOK + j, v);
                     tmem_wait_loads(v);
 #pragma unroll
                     for (int i = 0; i < W; i += 4) {
-                        const float4 sx = *reinterpret_cast<const float4 *>(words + j + i);
+                        const float4 sx = *reinterpret_cast<const float4 *>(words + begin + j + i);
                         fma2(sum[(j + i) / 2], pair_of_floats(v[i], v[i + 1]), mul2(pair_of_floats(sx.x, sx.y), sw));
                         fma2(sum[(j + i) / 2 + 1], pair_of_floats(v[i + 2], v[i + 3]), mul2(pair_of_floats(sx.z, sx.w), sw));
                     }
@@ -212,40 +211,37 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_consta
             };
             if (cluster > 1) {
                 // Own sums to own memory (one tile to a cluster: nothing follows in the stages), four rows of a feature side
-                // by side; then this block's rows from all blocks, added in their order.
+                // by side; then some rows from all blocks, added in their order.
 #pragma unroll
-                for (int j = 0; j < TOK; j += 4) {
+                for (int j = 0; j < Own; j += 4) {
                     const float2 lo = floats_of(sum[j / 2]), hi = floats_of(sum[j / 2 + 1]);
-                    *reinterpret_cast<float4 *>(shared + ((j / 4) * kBlock + mine) * 16) = make_float4(lo.x, lo.y, hi.x, hi.y);
+                    *reinterpret_cast<float4 *>(shared + (((begin + j) / 4) * kBlock + mine) * 16) = make_float4(lo.x, lo.y, hi.x, hi.y);
                 }
                 __syncwarp();
                 cluster_sync_all();
-                const int each = TOK / cluster;
+                const int each = Own / cluster, low = rank * (TOK / cluster) + begin / cluster;      // rows low .. low + each - 1
+                auto real = [&](int row) { return !a.row_of || (row < rows.count && source_row(a, rows.first + row) >= 0); };
                 if (each >= 4) {
-                    // all loads of up to 64 rows together: four rows of block i % cluster, the blocks' in turn
+                    // all loads together: four rows from block i % cluster, the blocks' in turn
                     const int ways = __ffs(cluster) - 1;
+                    float4 v[Own / 4];
 #pragma unroll
-                    for (int i0 = 0; i0 < TOK / 4; i0 += 16) {
-                        constexpr int N = TOK / 4 < 16 ? TOK / 4 : 16;
-                        float4 v[N];
+                    for (int i = 0; i < Own / 4; ++i)
+                        v[i] = cluster_load4(cluster_address(base + ((low / 4 + (i >> ways)) * kBlock + mine) * 16, i & (cluster - 1)));
+                    float4 w = v[0];
 #pragma unroll
-                        for (int i = 0; i < N; ++i)
-                            v[i] = cluster_load4(cluster_address(base + ((rank * (each / 4) + ((i0 + i) >> ways)) * kBlock + mine) * 16, (i0 + i) & (cluster - 1)));
-                        float4 w = v[0];
-#pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            const int r = (i0 + i) & (cluster - 1), row = rank * each + 4 * ((i0 + i) >> ways);
-                            w = r == 0 ? v[i] : make_float4(w.x + v[i].x, w.y + v[i].y, w.z + v[i].z, w.w + v[i].w);
-                            if (r == cluster - 1) {
-                                store(row, real(row) ? w.x : 0.0f);
-                                store(row + 1, real(row + 1) ? w.y : 0.0f);
-                                store(row + 2, real(row + 2) ? w.z : 0.0f);
-                                store(row + 3, real(row + 3) ? w.w : 0.0f);
-                            }
+                    for (int i = 0; i < Own / 4; ++i) {
+                        const int r = i & (cluster - 1), row = low + 4 * (i >> ways);
+                        w = r == 0 ? v[i] : make_float4(w.x + v[i].x, w.y + v[i].y, w.z + v[i].z, w.w + v[i].w);
+                        if (r == cluster - 1) {
+                            store(row, real(row) ? w.x : 0.0f);
+                            store(row + 1, real(row + 1) ? w.y : 0.0f);
+                            store(row + 2, real(row + 2) ? w.z : 0.0f);
+                            store(row + 3, real(row + 3) ? w.w : 0.0f);
                         }
                     }
                 } else {
-                    for (int row = rank * each; row < (rank + 1) * each; ++row) {
+                    for (int row = low; row < low + each; ++row) {
                         const uint32_t at = base + ((row / 4) * kBlock + mine) * 16 + row % 4 * 4;
                         float v[16];
 #pragma unroll
@@ -262,10 +258,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_consta
                 break;
             }
 #pragma unroll
-            for (int j = 0; j < TOK; j += 2) {
+            for (int j = 0; j < Own; j += 2) {
                 const float2 v = floats_of(sum[j / 2]);
-                store(j, there[j / 32] >> (j & 31) & 1 ? v.x : 0.0f);
-                store(j + 1, there[j / 32] >> (j & 31) & 2 ? v.y : 0.0f);
+                store(begin + j, there[j / 32] >> (j & 31) & 1 ? v.x : 0.0f);
+                store(begin + j + 1, there[j / 32] >> (j & 31) & 2 ? v.y : 0.0f);
             }
         }
     }
@@ -282,8 +278,10 @@ __global__ void __launch_bounds__(kFewThreads, 2) few_kernel(const __grid_consta
 }
 
 template <int TOK>
-cudaError_t start_few_of(const Product &p, cudaStream_t s, int cluster, int64_t units, int row_tiles, int multiprocessors) {
+cudaError_t start_few_of(const Product &p, cudaStream_t s, int multiprocessors) {
     using F = Few<TOK>;
+    const int64_t tiles = most_tiles(p.a, TOK), units = tiles * ((p.a.out_dim + kBlock - 1) / kBlock);
+    const int row_tiles = p.a.offsets ? 0 : (int)tiles;
     static bool ready[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -295,8 +293,11 @@ cudaError_t start_few_of(const Product &p, cudaStream_t s, int cluster, int64_t 
     if (e != cudaSuccess) return e;
     CUtensorMap weight, x;
     if (!map_weight(&weight, p.a, kBlock) || !map_rows(&x, p.a, TOK)) return cudaErrorInvalidValue;
-    const int64_t blocks = cluster > 1 ? units * cluster : units < 2 * multiprocessors ? units : 2 * multiprocessors;
-    return launch_next(few_kernel<TOK>, dim3((unsigned)blocks), kFewThreads, F::Smem, s, cluster > 1 ? cluster : 0, p, weight, x, cluster, row_tiles);
+    const int64_t room = (int64_t)F::Blocks * multiprocessors;
+    int cluster = 1;
+    while (cluster < 16 && units * cluster * 2 <= room && p.groups >= cluster * 4) cluster *= 2;
+    const int64_t blocks = cluster > 1 ? units * cluster : std::min(units, room);
+    return launch_next(few_kernel<TOK>, dim3((unsigned)blocks), F::Threads, F::Smem, s, cluster > 1 ? cluster : 0, p, weight, x, cluster, row_tiles);
 }
 
 }  // namespace
@@ -306,15 +307,10 @@ cudaError_t start_few(const Product &p, cudaStream_t s, int multiprocessors) {
     // Columns for the rows that a tile is likely to have: all of them, or twice an expert's share.
     const int64_t likely = a.offsets ? 2 * a.rows / a.experts : a.rows;
     const int tok = likely <= 16 ? 16 : likely <= 32 ? 32 : likely <= 64 ? 64 : 128;
-    const int features = (a.out_dim + kBlock - 1) / kBlock;
-    const int64_t tiles = most_tiles(a, tok), units = tiles * features;
-    int cluster = 1;
-    while (cluster < 16 && units * cluster * 2 <= 2 * multiprocessors && p.groups >= cluster * 4) cluster *= 2;
-    const int row_tiles = a.offsets ? 0 : (int)tiles;
-    return tok == 16   ? start_few_of<16>(p, s, cluster, units, row_tiles, multiprocessors)
-           : tok == 32 ? start_few_of<32>(p, s, cluster, units, row_tiles, multiprocessors)
-           : tok == 64 ? start_few_of<64>(p, s, cluster, units, row_tiles, multiprocessors)
-                       : start_few_of<128>(p, s, cluster, units, row_tiles, multiprocessors);
+    return tok == 16   ? start_few_of<16>(p, s, multiprocessors)
+           : tok == 32 ? start_few_of<32>(p, s, multiprocessors)
+           : tok == 64 ? start_few_of<64>(p, s, multiprocessors)
+                       : start_few_of<128>(p, s, multiprocessors);
 }
 
 int take_few_status(int *code) {
