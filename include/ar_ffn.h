@@ -52,6 +52,7 @@ typedef struct ar_matmul_fp8_args {
     void *out;                  /* [rows][out_dim] */
     const int32_t *offsets;     /* [experts + 1], or NULL */
     const int32_t *row_of;      /* [rows], or NULL */
+    void *workspace;            /* ar_matmul_fp8_workspace() bytes, on 16 bytes, this call's alone until it has run; NULL: none */
     int64_t x_stride, x_scales_stride, weight_stride, expert_stride, out_stride;
     int64_t rows, x_rows;
     int32_t dtype;              /* AR_F16 or AR_BF16, of out */
@@ -60,6 +61,10 @@ typedef struct ar_matmul_fp8_args {
     int32_t x_row_scales;       /* 0 or 1 */
 } ar_matmul_fp8_args;
 AR_API int ar_matmul_fp8(const ar_matmul_fp8_args *args, ar_stream_t stream);
+
+/* Bytes of working memory with which a call that picks many rows (row_of) is faster: room for these rows and their scales, side by
+ * side.  0: none is used. */
+AR_API size_t ar_matmul_fp8_workspace(const ar_matmul_fp8_args *args);
 
 /* The first error recorded by the products on the current device since the last call of this function: AR_ETIMEOUT
  * after a copy or a matrix instruction that did not end within its limit (the call ends, its outputs are

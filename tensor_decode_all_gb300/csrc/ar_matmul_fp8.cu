@@ -1,6 +1,8 @@
 // ar_matmul_fp8.cu -- ar_matmul_fp8: the checks of a call, the choice of its kernel, and the kernel that takes any alignment.
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "ar_matmul_fp8.cuh"
 
 namespace {
@@ -131,9 +133,14 @@ bool copyable(const void *at, int64_t rows, int64_t stride, int64_t dim) {
 
 bool fast(const Product &p) {
     const ar_matmul_fp8_args &a = p.a;
+    // (picked rows are found by 32 bits)
+    if (a.row_of && a.x_rows > 1 && a.x_rows > ((int64_t)16 << 32) / std::max(a.x_stride, (int64_t)1)) return false;
     return a.dim > 0 && a.x_rows > 0 && copyable(a.x, a.x_rows, a.x_stride, a.dim) && copyable(a.weight, a.out_dim, a.weight_stride, a.dim) &&
            copyable(a.weight, a.experts, a.expert_stride, a.dim) && encoder();
 }
+
+// Which of the fast kernels.
+bool takes_many(const ar_matmul_fp8_args &a) { return (a.offsets ? a.rows / a.experts : a.rows) > 256; }
 
 int multiprocessors_of_device() {
     static int known[64] = {};
@@ -160,7 +167,7 @@ bool map_weight(CUtensorMap *m, const ar_matmul_fp8_args &a, int box) {
 bool map_rows(CUtensorMap *m, const ar_matmul_fp8_args &a, int box) {
     const int64_t row = a.x_rows > 1 ? a.x_stride : (a.dim + 15) / 16 * 16;
     const cuuint64_t dims[2] = {(cuuint64_t)a.dim, (cuuint64_t)a.x_rows}, strides[1] = {(cuuint64_t)row};
-    const cuuint32_t boxes[2] = {kBlock, a.row_of ? 1u : (cuuint32_t)box};
+    const cuuint32_t boxes[2] = {kBlock, (cuuint32_t)box};
     return encode(m, a.x, 2, dims, strides, boxes);
 }
 
@@ -176,7 +183,7 @@ extern "C" AR_API int ar_matmul_fp8(const ar_matmul_fp8_args *args, ar_stream_t 
     if (a.rows > most || a.x_rows > most || a.dim > 1 << 20 || a.out_dim > 1 << 20 || a.experts > 1024) return AR_ETOOBIG;
     if (a.rows == 0 || a.out_dim == 0) return AR_OK;
     if (!a.out || (a.dim > 0 && (!a.weight || !a.weight_scales || (a.x_rows > 0 && (!a.x || !a.x_scales))))) return AR_EINVAL;
-    if (misaligned(a.x_scales, 4) || misaligned(a.weight_scales, 4) || misaligned(a.out, 2) || misaligned(a.offsets, 4) || misaligned(a.row_of, 4))
+    if (misaligned(a.x_scales, 4) || misaligned(a.weight_scales, 4) || misaligned(a.out, 2) || misaligned(a.offsets, 4) || misaligned(a.row_of, 4) || misaligned(a.workspace, 16))
         return AR_EINVAL;
     Product p;
     p.a = a;
@@ -184,8 +191,14 @@ extern "C" AR_API int ar_matmul_fp8(const ar_matmul_fp8_args *args, ar_stream_t 
     if (!fast(p)) return launch_status(start_any(p, stream));
     const int multiprocessors = multiprocessors_of_device();
     if (multiprocessors < 2) return AR_ECUDA;
-    if ((a.offsets ? a.rows / a.experts : a.rows) > 256) return launch_status(start_many(p, stream, multiprocessors));
+    if (takes_many(a) && (!a.row_of || a.workspace)) return launch_status(start_many(p, stream, multiprocessors));
     return launch_status(start_few(p, stream, multiprocessors));
+}
+
+extern "C" AR_API size_t ar_matmul_fp8_workspace(const ar_matmul_fp8_args *args) {
+    if (!args || !args->row_of || args->rows <= 0 || args->dim <= 0 || args->experts < 1 || !takes_many(*args)) return 0;
+    const size_t groups = args->x_row_scales ? 1 : ((size_t)args->dim + kBlock - 1) / kBlock;
+    return (size_t)args->rows * ((size_t)pitch_of(*args) + groups * sizeof(float));
 }
 
 extern "C" AR_API int ar_matmul_fp8_status(void) {

@@ -6,6 +6,7 @@
 
 #include "ar_ffn.h"
 #include "ar_kv4.cuh"
+#include "ar_tensor.cuh"
 
 namespace tda {
 
@@ -82,10 +83,45 @@ __device__ __forceinline__ int64_t source_row(const ar_matmul_fp8_args &a, int64
     return r >= 0 && r < a.x_rows ? r : -1;
 }
 
-// How the copy engine sees the weight, a box of `box` features of a group; and the rows of x, a box of `box` rows,
-// or one where they are picked by number.  False: it cannot (the addresses and strides are checked before).
+// Rows of x that are picked by number, N of them, copied a group of channels at a time by one warp: 16 bytes to a lane, eight lanes to a row, in the
+// order that the copy engine gives a tile's rows.  Where there is no row, another or none is copied: what comes of it is not used.
+// (Two or three instructions to a copy: a warp has no time for more.)
+template <int N> struct Picked {
+    uint32_t at[N / 4];          // of row 4 i + which, in 16 bytes from x on
+    int here;                    // rows that are there
+    __device__ __forceinline__ void look_up(const ar_matmul_fp8_args &a, int first, int count) {
+        const int64_t stride = a.x_rows > 1 ? a.x_stride / 16 : 0;
+        here = count;
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const int j = 4 * i + (threadIdx.x >> 3 & 3);
+            at[i] = (uint32_t)(j < count ? max(source_row(a, first + j), (int64_t)0) * stride : 0);
+        }
+    }
+    __device__ __forceinline__ void copy(const ar_matmul_fp8_args &a, uint32_t to, int group) const {
+        const int piece = threadIdx.x & 7, which = threadIdx.x >> 3 & 3, channel = group * kBlock + piece * 16, bytes = max(0, min(a.dim - channel, 16));
+        const uint8_t *from = static_cast<const uint8_t *>(a.x) + (bytes ? channel : 0);
+        const uint32_t even = to + which * kBlock + ((piece ^ which) << 4), odd = to + which * kBlock + ((piece ^ (which + 4)) << 4);
+        // Few rows: none is copied that is not there.  Many: eight copies at a time, so that their addresses are there before the first.
+        constexpr int M = N <= 32 ? 1 : 8;
+#pragma unroll
+        for (int i0 = 0; i0 < N / 4; i0 += M) {
+            if (4 * i0 >= here) break;
+            const uint8_t *p[M];
+#pragma unroll
+            for (int i = 0; i < M; ++i) p[i] = from + (uint64_t)at[i0 + i] * 16;
+#pragma unroll
+            for (int i = 0; i < M; ++i) copy_piece(((i0 + i) & 1 ? odd : even) + (i0 + i) * 4 * kBlock, p[i], bytes);
+        }
+    }
+};
+
+// How the copy engine sees the weight, a box of `box` features of a group; and the rows of x, a box of `box` rows.  False: it cannot (the addresses and strides are checked before).
 bool map_weight(CUtensorMap *m, const ar_matmul_fp8_args &a, int box);
 bool map_rows(CUtensorMap *m, const ar_matmul_fp8_args &a, int box);
+
+// Bytes from a picked row to the next in the workspace.
+inline int64_t pitch_of(const ar_matmul_fp8_args &a) { return ((int64_t)a.dim + 15) / 16 * 16; }
 
 // The kernels for rows on 16 bytes, and the first error that each has recorded (and forgets).
 cudaError_t start_few(const Product &p, cudaStream_t s, int multiprocessors);

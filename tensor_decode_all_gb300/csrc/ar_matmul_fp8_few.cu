@@ -5,7 +5,7 @@
 // and four warps (eight), a feature to a thread, multiply what came out by the two scales and add it up in registers.
 //
 // A warp copies, another issues the instructions; weight tiles (16 KB) and rows come by bulk tensor copies, the
-// scales by word copies beside them, all to one barrier a stage.  Rows that are picked by number come four at a time.
+// scales by word copies beside them.  Rows that are picked by number come 16 bytes to a lane.
 //
 // Where there are fewer tiles than the GPU has room for, a cluster of blocks shares a tile's channels: each block
 // sums its part and leaves its sums in its shared memory, and each adds up some of the rows from all blocks, in their
@@ -35,7 +35,8 @@ template <int TOK> struct Few {
     static constexpr int Smem = Stages * StageBytes + Scales * ScaleBytes + (2 * Stages + Scales + 2 * Buffers) * 8 + 16 + 1024;
 };
 
-template <int TOK>
+// kPicked: row_of is given.
+template <int TOK, bool kPicked>
 __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kernel(const __grid_constant__ Product p, const __grid_constant__ CUtensorMap weight,
                                                              const __grid_constant__ CUtensorMap x, int cluster, int row_tiles) {
     using F = Few<TOK>;
@@ -51,7 +52,7 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
     if (warp == 0) {
         if (lane == 0) {
             for (int i = 0; i < S; ++i) {
-                bar_init(full + 8 * i, 1);
+                bar_init(full + 8 * i, kPicked ? 33 : 1);      // the bulk copies' thread, and each lane's copies of picked rows
                 bar_init(empty + 8 * i, 1);
             }
             for (int i = 0; i < Q; ++i) bar_init(scaled + 8 * i, 32);      // each lane's copies
@@ -94,19 +95,13 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
             rows = tile_of(u, feature);
             if (rows.count == 0 || (any && cluster > 1)) break;
             any = true;
-            int picked[4] = {0, 0, 0, 0};
-            if (a.row_of && lane < TOK / 4) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = 4 * lane + i;
-                    picked[i] = j < rows.count ? (int)max(source_row(a, rows.first + j), (int64_t)0) : 0;
-                }
-            }
+            Picked<TOK> picked;
+            if (kPicked) picked.look_up(a, rows.first, rows.count);
             const float *scale[(TOK + 31) / 32];
 #pragma unroll
             for (int i = 0; i < (TOK + 31) / 32; ++i) {
                 const int j = lane + 32 * i;
-                const int64_t r = j < rows.count ? source_row(a, rows.first + j) : -1;
+                const int64_t r = j >= rows.count ? -1 : kPicked ? source_row(a, rows.first + j) : rows.first + j;
                 scale[i] = r >= 0 ? a.x_scales + r * a.x_scales_stride : nullptr;
             }
             const float *weight_scale = a.weight_scales + ((int64_t)rows.expert * features + feature / kBlock) * p.groups;
@@ -115,12 +110,15 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
                 if (!(fine = bar_wait_warp(empty + 8 * s, stage.parity ^ 1))) break;
                 const uint32_t bar = full + 8 * s, to = rows_at + s * F::RowBytes, words = scales + words_of.at * F::ScaleBytes;
                 if (lane == 0) {
-                    bar_expect(bar, F::WeightBytes + F::RowBytes);
+                    bar_expect(bar, F::WeightBytes + (kPicked ? 0 : F::RowBytes));
                     tensor_load(weights + s * F::WeightBytes, &weight, bar, k * kBlock, feature, rows.expert);
-                    if (!a.row_of) tensor_load(to, &x, bar, k * kBlock, rows.first);
+                    if (!kPicked) tensor_load(to, &x, bar, k * kBlock, rows.first);
                     copy_word(words + 4 * TOK, weight_scale + k, true);
                 }
-                if (a.row_of && lane < TOK / 4) tensor_gather(to + lane * 4 * kBlock, &x, bar, k * kBlock, picked);
+                if constexpr (kPicked) {
+                    picked.copy(a, to, k);
+                    bar_arrive_copies(bar);
+                }
 #pragma unroll
                 for (int i = 0; i < (TOK + 31) / 32; ++i)
                     if (TOK >= 32 || lane < TOK)
@@ -145,6 +143,7 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
             for (int k = k0; k < k1; ++k, ++n, stage.next(), buffer.next()) {
                 if (!(fine = bar_wait_warp(full + 8 * stage.at, stage.parity, sums_empty + 8 * buffer.at, buffer.parity ^ 1))) break;
                 tmem_after_sync();
+                if (kPicked) written_for_mma();
                 if (one) {
                     const uint64_t w = weights_operand + stage.at * (F::WeightBytes >> 4), r = rows_operand + stage.at * (F::RowBytes >> 4);
 #pragma unroll
@@ -174,7 +173,7 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
             for (int i = 0; i < (Own + 31) / 32; ++i) {
                 const int row = begin + i * 32 + lane;
                 there[i] = ~0u;
-                if (a.row_of) there[i] = __ballot_sync(~0u, row < rows.count && source_row(a, rows.first + row) >= 0);
+                if (kPicked) there[i] = __ballot_sync(~0u, row < rows.count && source_row(a, rows.first + row) >= 0);
             }
             unsigned long long sum[Own / 2];
 #pragma unroll
@@ -220,7 +219,7 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
                 __syncwarp();
                 cluster_sync_all();
                 const int each = Own / cluster, low = rank * (TOK / cluster) + begin / cluster;      // rows low .. low + each - 1
-                auto real = [&](int row) { return !a.row_of || (row < rows.count && source_row(a, rows.first + row) >= 0); };
+                auto real = [&](int row) { return !kPicked || (row < rows.count && source_row(a, rows.first + row) >= 0); };
                 if (each >= 4) {
                     // all loads together: four rows from block i % cluster, the blocks' in turn
                     const int ways = __ffs(cluster) - 1;
@@ -277,7 +276,7 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
     if (warp == 1) tmem_free(tmem, F::Columns);
 }
 
-template <int TOK>
+template <int TOK, bool kPicked>
 cudaError_t start_few_of(const Product &p, cudaStream_t s, int multiprocessors) {
     using F = Few<TOK>;
     const int64_t tiles = most_tiles(p.a, TOK), units = tiles * ((p.a.out_dim + kBlock - 1) / kBlock);
@@ -286,8 +285,8 @@ cudaError_t start_few_of(const Product &p, cudaStream_t s, int multiprocessors) 
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev >= 64 || !*(volatile bool *)&ready[dev])) {
-        e = cudaFuncSetAttribute(few_kernel<TOK>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::Smem);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(few_kernel<TOK>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = cudaFuncSetAttribute(few_kernel<TOK, kPicked>, cudaFuncAttributeMaxDynamicSharedMemorySize, F::Smem);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(few_kernel<TOK, kPicked>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e == cudaSuccess && dev < 64) *(volatile bool *)&ready[dev] = true;
     }
     if (e != cudaSuccess) return e;
@@ -297,7 +296,11 @@ cudaError_t start_few_of(const Product &p, cudaStream_t s, int multiprocessors) 
     int cluster = 1;
     while (cluster < 16 && units * cluster * 2 <= room && p.groups >= cluster * 4) cluster *= 2;
     const int64_t blocks = cluster > 1 ? units * cluster : std::min(units, room);
-    return launch_next(few_kernel<TOK>, dim3((unsigned)blocks), F::Threads, F::Smem, s, cluster > 1 ? cluster : 0, p, weight, x, cluster, row_tiles);
+    return launch_next(few_kernel<TOK, kPicked>, dim3((unsigned)blocks), F::Threads, F::Smem, s, cluster > 1 ? cluster : 0, p, weight, x, cluster, row_tiles);
+}
+
+template <int TOK> cudaError_t start_few_of(const Product &p, cudaStream_t s, int multiprocessors) {
+    return p.a.row_of ? start_few_of<TOK, true>(p, s, multiprocessors) : start_few_of<TOK, false>(p, s, multiprocessors);
 }
 
 }  // namespace

@@ -36,6 +36,25 @@ struct Tile {
     int expert, first, count, feature;
 };
 
+// Picked rows of x and their scales, side by side in the workspace: a warp to a row.  (The copy engine's own way to pick rows takes 0.6 us
+// for 128 of them, and copies by threads take the time of the shared memory's instructions: either a tile would wait
+// for them; 67 MB come and go in 25 us.)
+__global__ void __launch_bounds__(256) pick_kernel(const ar_matmul_fp8_args a, uint8_t *rows, float *scales, int pitch, int groups) {
+    after_the_stream();
+    const int lane = threadIdx.x & 31;
+    const int begin = a.offsets ? clamp_row(a.offsets[0], a.rows) : 0, end = a.offsets ? clamp_row(a.offsets[a.experts], a.rows) : (int)a.rows;
+    for (int64_t row = begin + (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < end; row += (int64_t)gridDim.x * 8) {
+        const int64_t from = source_row(a, row);
+        if (from < 0) continue;            // (what is there is not used)
+        const uint8_t *x = static_cast<const uint8_t *>(a.x) + from * a.x_stride;
+        const int whole = a.dim / 16;
+#pragma unroll 4
+        for (int i = lane; i < whole; i += 32) reinterpret_cast<uint4 *>(rows + row * pitch)[i] = reinterpret_cast<const uint4 *>(x)[i];
+        if (lane < a.dim % 16) rows[row * pitch + whole * 16 + lane] = x[whole * 16 + lane];
+        for (int i = lane; i < groups; i += 32) scales[row * groups + i] = a.x_scales[from * a.x_scales_stride + i];
+    }
+}
+
 __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_constant__ Product p, const __grid_constant__ CUtensorMap weight,
                                                                const __grid_constant__ CUtensorMap x) {
     constexpr int S = kManyStages, Q = kManyScales;
@@ -106,20 +125,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
                 if (tile.count == 0) break;
                 // (half of them are read twice where the tile is short)
                 const int own = tile.count <= kBlock ? kBlock / 2 : kBlock, first = tile.first + rank * own, count = min(tile.count - rank * own, own);
-                int picked[4] = {0, 0, 0, 0};
-                if (a.row_of) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int j = 4 * lane + i;
-                        picked[i] = j < count ? (int)max(source_row(a, first + j), (int64_t)0) : 0;
-                    }
-                }
                 const float *scale[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int j = lane + 32 * i;
-                    const int64_t r = j < count ? source_row(a, first + j) : -1;
-                    scale[i] = r >= 0 ? a.x_scales + r * a.x_scales_stride : nullptr;
+                    scale[i] = j < count ? a.x_scales + (int64_t)(first + j) * a.x_scales_stride : nullptr;
                 }
                 // the weight's scales of both halves, by two lanes
                 const int half = tile.feature / kBlock + lane;
@@ -131,9 +141,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
                     if (lane == 0) {
                         if (rank == 0) bar_expect(full + 8 * s, 4 * kOperandBytes);
                         pair_tensor_load(weights + s * kOperandBytes, &weight, bar, k * kBlock, tile.feature + rank * kBlock, tile.expert);
-                        if (!a.row_of) pair_tensor_load(to, &x, bar, k * kBlock, first);
+                        pair_tensor_load(to, &x, bar, k * kBlock, first);
                     }
-                    if (a.row_of) pair_tensor_gather(to + lane * 4 * kBlock, &x, bar, k * kBlock, picked);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) copy_word(words + 4 * (lane + 32 * i), scale[i] ? scale[i] + (a.x_row_scales ? 0 : k) : a.x_scales, scale[i] != nullptr);
                     if (lane < 2) copy_word(words + 4 * (kBlock + lane), weight_scale ? weight_scale + k : a.weight_scales, weight_scale != nullptr);
@@ -319,10 +328,25 @@ cudaError_t start_many(const Product &p, cudaStream_t s, int multiprocessors) {
         if (e == cudaSuccess && dev < 64) *(volatile bool *)&ready[dev] = true;
     }
     if (e != cudaSuccess) return e;
+    Product q = p;
+    if (a.row_of) {
+        const int64_t pitch = pitch_of(a);
+        const int groups = a.x_row_scales ? 1 : p.groups;
+        uint8_t *rows = static_cast<uint8_t *>(a.workspace);
+        float *scales = reinterpret_cast<float *>(rows + a.rows * pitch);
+        e = launch_next(pick_kernel, dim3((unsigned)std::min((a.rows + 7) / 8, (int64_t)8 * multiprocessors)), 256, 0, s, 0, a, rows, scales, (int)pitch, groups);
+        if (e != cudaSuccess) return e;
+        q.a.x = rows;
+        q.a.x_stride = pitch;
+        q.a.x_scales = scales;
+        q.a.x_scales_stride = groups;
+    }
     CUtensorMap weight, x;
-    if (!map_weight(&weight, a, kBlock) || !map_rows(&x, a, kBlock)) return cudaErrorInvalidValue;
+    ar_matmul_fp8_args in_order = q.a;
+    if (a.row_of) in_order.x_rows = a.rows;
+    if (!map_weight(&weight, a, kBlock) || !map_rows(&x, in_order, kBlock)) return cudaErrorInvalidValue;
     const int64_t units = most_tiles(a, kTileRows) * ((a.out_dim + kTileFeatures - 1) / kTileFeatures), pairs = multiprocessors / 2;
-    return launch_next(many_kernel, dim3((unsigned)(2 * std::min(2 * units, pairs))), kManyThreads, kManySmem, s, 2, p, weight, x);
+    return launch_next(many_kernel, dim3((unsigned)(2 * std::min(2 * units, pairs))), kManyThreads, kManySmem, s, 2, q, weight, x);
 }
 
 int take_many_status(int *code) {

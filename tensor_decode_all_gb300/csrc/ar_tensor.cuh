@@ -84,11 +84,14 @@ __device__ __forceinline__ void tensor_load(uint32_t to, const CUtensorMap *m, u
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(to),
                  "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
 }
-// Four rows of any numbers, one after another (the map's box is one row high).
-__device__ __forceinline__ void tensor_gather(uint32_t to, const CUtensorMap *m, uint32_t bar, int x, const int (&rows)[4]) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(to),
-                 "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(rows[0]), "r"(rows[1]), "r"(rows[2]), "r"(rows[3]) : "memory");
+// The first `bytes` of 16, and zeros.
+__device__ __forceinline__ void copy_piece(uint32_t to, const void *from, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// What ordinary accesses and word copies have written is there for matrix instructions after this.
+__device__ __forceinline__ void written_for_mma() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // One word, or a zero where it is not there.
 __device__ __forceinline__ void copy_word(uint32_t to, const float *from, bool there) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
@@ -189,17 +192,17 @@ __device__ __forceinline__ void pair_tensor_load(uint32_t to, const CUtensorMap 
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(to),
                  "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
 }
-__device__ __forceinline__ void pair_tensor_gather(uint32_t to, const CUtensorMap *m, uint32_t bar, int x, const int (&rows)[4]) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(to),
-                 "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(rows[0]), "r"(rows[1]), "r"(rows[2]), "r"(rows[3]) : "memory");
-}
-
 // -------------------------------------------------------------------- clusters
 
 // An arrival on a barrier of any block of the cluster that orders no ordinary memory accesses: those of tensor memory are
 // ordered by its own fences (with a release at cluster scope it took 1100 cycles).
 __device__ __forceinline__ void cluster_bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The same after ordinary writes of this block that its own share of a pair's instructions reads.
+__device__ __forceinline__ void cluster_bar_arrive_written(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // The warpgroup's registers a thread from here on.

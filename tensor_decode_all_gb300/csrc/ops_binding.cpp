@@ -492,6 +492,11 @@ PyObject *matmul(PyObject *const *o) {
     a.x_stride = x.stride(0); a.x_scales_stride = xs.stride(0); a.weight_stride = w.stride(lead); a.expert_stride = experts ? w.stride(0) : 0;
     a.out_stride = out.stride(0); a.rows = rows; a.x_rows = N; a.dtype = code_16("out", out); a.out_dim = (int32_t)F; a.dim = (int32_t)K;
     a.experts = (int32_t)std::min(E, kInt); a.x_row_scales = row_scales;
+    Tensor room;
+    if (const size_t bytes = ar_matmul_fp8_workspace(&a)) {
+        room = make({(int64_t)bytes}, at::kByte, x);
+        a.workspace = room.data_ptr();
+    }
     const int rc = ar_matmul_fp8(&a, stream_of(dev));
     if (rc) return fail(rc, "ar_matmul_fp8");
     return o[6] != Py_None ? (Py_INCREF(o[6]), o[6]) : THPVariable_Wrap(out);

@@ -29,6 +29,7 @@ _P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 
 class MatmulFp8Args(ctypes.Structure):
     _fields_ = [("x", _P), ("x_scales", _P), ("weight", _P), ("weight_scales", _P), ("out", _P), ("offsets", _P), ("row_of", _P),
+                ("workspace", _P),
                 ("x_stride", _I64), ("x_scales_stride", _I64), ("weight_stride", _I64), ("expert_stride", _I64), ("out_stride", _I64),
                 ("rows", _I64), ("x_rows", _I64),
                 ("dtype", _I32), ("out_dim", _I32), ("dim", _I32), ("experts", _I32), ("x_row_scales", _I32)]
@@ -67,6 +68,8 @@ def _ffn():
             f.argtypes = [_P, _P]
             f.restype = ctypes.c_int
         L.ar_matmul_fp8_status.argtypes = []
+        L.ar_matmul_fp8_workspace.argtypes = [_P]
+        L.ar_matmul_fp8_workspace.restype = ctypes.c_size_t
         L.ar_route_experts_workspace.argtypes = [_P]
         L.ar_route_experts_workspace.restype = ctypes.c_size_t
         _lib = L

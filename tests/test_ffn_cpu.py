@@ -21,7 +21,7 @@ def lib():
 
 def test_symbols_are_declared_and_exported(lib):
     names = tda.declared_symbols(os.path.join(ar._build.INCLUDE, "ar_ffn.h"))
-    assert set(names) == {"ar_matmul_fp8", "ar_matmul_fp8_status", "ar_route_experts", "ar_route_experts_workspace", "ar_silu_mul_fp8", "ar_experts_sum"}
+    assert set(names) == {"ar_matmul_fp8", "ar_matmul_fp8_workspace", "ar_matmul_fp8_status", "ar_route_experts", "ar_route_experts_workspace", "ar_silu_mul_fp8", "ar_experts_sum"}
     assert set(names) <= set(tda.declared_symbols())
     for n in names:
         assert hasattr(lib, n)
@@ -55,7 +55,7 @@ A = 4096   # an address that no refused call touches
 
 
 def _matmul(**kw):
-    base = dict(x=A, x_scales=A, weight=A, weight_scales=A, out=A, offsets=None, row_of=None, x_stride=256, x_scales_stride=2,
+    base = dict(x=A, x_scales=A, weight=A, weight_scales=A, out=A, offsets=None, row_of=None, workspace=None, x_stride=256, x_scales_stride=2,
                 weight_stride=256, expert_stride=0, out_stride=64, rows=3, x_rows=3, dtype=2, out_dim=64, dim=256, experts=1, x_row_scales=0)
     return ffn.MatmulFp8Args(**{**base, **kw})
 
@@ -77,7 +77,7 @@ def _sum(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(x=None), 1), (dict(x_scales=None), 1), (dict(weight=None), 1), (dict(weight_scales=None), 1), (dict(out=None), 1),
     (dict(x_scales=A + 2), 1), (dict(weight_scales=A + 1), 1), (dict(out=A + 1), 1), (dict(offsets=A + 2), 1),
-    (dict(row_of=A + 2), 1), (dict(dtype=3), 1), (dict(dtype=0), 1), (dict(rows=-1, x_rows=-1), 1), (dict(x_rows=4), 1), (dict(dim=-1), 1),
+    (dict(row_of=A + 2), 1), (dict(workspace=A + 8), 1), (dict(dtype=3), 1), (dict(dtype=0), 1), (dict(rows=-1, x_rows=-1), 1), (dict(x_rows=4), 1), (dict(dim=-1), 1),
     (dict(out_dim=-1), 1), (dict(experts=0, offsets=A), 1), (dict(experts=2), 1), (dict(x_row_scales=2), 1),
     (dict(rows=(1 << 30) + 1, x_rows=(1 << 30) + 1), 2), (dict(row_of=A, x_rows=(1 << 30) + 1), 2), (dict(dim=(1 << 20) + 1), 2),
     (dict(out_dim=(1 << 20) + 1), 2), (dict(offsets=A, experts=1025), 2)])
@@ -110,6 +110,17 @@ def test_silu_refusals(lib, kw, code):
     (dict(chosen=-1), 1), (dict(rows=(1 << 30) + 1), 2), (dict(tokens=(1 << 30) + 1), 2), (dict(dim=(1 << 20) + 1), 2), (dict(chosen=1025), 2)])
 def test_sum_refusals(lib, kw, code):
     assert _rc(lib, "ar_experts_sum", _sum(**kw)) == code
+
+
+def test_the_products_workspace(lib):
+    """Room for picked rows and their scales, where there are many of them."""
+    def size(**kw):
+        return lib.ar_matmul_fp8_workspace(ctypes.addressof(_matmul(**kw)))
+    assert size(rows=5000, x_rows=5000) == 0 and size(row_of=A) == 0 and size(row_of=A, rows=5000, dim=0) == 0
+    assert size(row_of=A, rows=5000) == 5000 * (256 + 2 * 4)
+    assert size(row_of=A, rows=5000, dim=250, x_row_scales=1) == 5000 * (256 + 4)
+    assert size(row_of=A, offsets=A, experts=64, rows=5000) == 0 and size(row_of=A, offsets=A, experts=0, rows=5000) == 0
+    assert lib.ar_matmul_fp8_workspace(None) == 0
 
 
 def test_the_routers_workspace(lib):
