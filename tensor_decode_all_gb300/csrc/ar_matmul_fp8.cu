@@ -139,9 +139,6 @@ bool fast(const Product &p) {
            copyable(a.weight, a.experts, a.expert_stride, a.dim) && encoder();
 }
 
-// Which of the fast kernels.
-bool takes_many(const ar_matmul_fp8_args &a) { return (a.offsets ? a.rows / a.experts : a.rows) > 256; }
-
 int multiprocessors_of_device() {
     static int known[64] = {};
     int dev = 0, n = 0;
@@ -150,6 +147,22 @@ int multiprocessors_of_device() {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
     if (dev < 64) *(volatile int *)&known[dev] = n;
     return n;
+}
+
+// Which of the fast kernels: the one that takes less time by its steps (groups of 128 channels that follow each other) in the tiles that follow each
+// other.  A step took 0.55 us with 128 rows to a block and 0.39 with 256 to a pair: 128 rows of 8192 times 8192 features 23 us
+// against 27, 256 35 against 27; 384 rows times 1280 features, whose channels are shared by clusters, 14.8 against 26.  Up to 64 rows (32 to an expert)
+// the weights' bytes count, and the first is always faster (64 rows: 18 against 27; 32 experts of 32 rows 48 against 53, of 64
+// rows 76 against 54).
+bool takes_many(const ar_matmul_fp8_args &a) {
+    const int64_t experts = a.offsets ? a.experts : 1, rows = (a.rows + experts - 1) / experts, groups = (a.dim + kBlock - 1) / kBlock;
+    if (rows <= (a.offsets ? 32 : 64)) return false;
+    const int known = multiprocessors_of_device(), multiprocessors = known > 1 ? known : 152;
+    auto up = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
+    const int64_t tiles = experts * up(rows, 128) * up(a.out_dim, 128), pairs = experts * up(rows, 256) * up(a.out_dim, 256);
+    int64_t share = 1;
+    while (share < 16 && tiles * share * 2 <= multiprocessors && groups >= share * 4) share *= 2;
+    return 39 * up(pairs, multiprocessors / 2) * groups < 55 * up(tiles * share, multiprocessors) * up(groups, share);
 }
 
 }  // namespace

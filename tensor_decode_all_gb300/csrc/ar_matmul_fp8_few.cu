@@ -276,6 +276,32 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
     if (warp == 1) tmem_free(tmem, F::Columns);
 }
 
+// How many clusters of that many blocks run at the same time: those of a cluster share a part of the GPU, which holds a whole number
+// of them (15 of 8 blocks, not 19, with a block to a multiprocessor; the runtime counts one to a multiprocessor).
+template <int TOK, bool kPicked> cudaError_t clusters_at_once(int cluster, int *most) {
+    using F = Few<TOK>;
+    static int known[64][5] = {};
+    int dev = 0, log = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    while (1 << log < cluster) ++log;
+    if (dev < 64 && (*most = *(volatile int *)&known[dev][log]) > 0) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)cluster);
+    cfg.blockDim = dim3(F::Threads);
+    cfg.dynamicSmemBytes = F::Smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(most, few_kernel<TOK, kPicked>, &cfg);
+    *most *= F::Blocks;
+    if (e == cudaSuccess && dev < 64) *(volatile int *)&known[dev][log] = std::max(*most, 1);
+    return e;
+}
+
 template <int TOK, bool kPicked>
 cudaError_t start_few_of(const Product &p, cudaStream_t s, int multiprocessors) {
     using F = Few<TOK>;
@@ -293,8 +319,15 @@ cudaError_t start_few_of(const Product &p, cudaStream_t s, int multiprocessors) 
     CUtensorMap weight, x;
     if (!map_weight(&weight, p.a, kBlock) || !map_rows(&x, p.a, TOK)) return cudaErrorInvalidValue;
     const int64_t room = (int64_t)F::Blocks * multiprocessors;
+    // Blocks to share a tile's channels, as long as all tiles' run at the same time and each has four groups or more.
     int cluster = 1;
-    while (cluster < 16 && units * cluster * 2 <= room && p.groups >= cluster * 4) cluster *= 2;
+    while (cluster < 16 && units * cluster * 2 <= room && p.groups >= cluster * 4) {
+        int most = 0;
+        e = clusters_at_once<TOK, kPicked>(cluster * 2, &most);
+        if (e != cudaSuccess) return e;
+        if (units > most) break;
+        cluster *= 2;
+    }
     const int64_t blocks = cluster > 1 ? units * cluster : std::min(units, room);
     return launch_next(few_kernel<TOK, kPicked>, dim3((unsigned)blocks), F::Threads, F::Smem, s, cluster > 1 ? cluster : 0, p, weight, x, cluster, row_tiles);
 }

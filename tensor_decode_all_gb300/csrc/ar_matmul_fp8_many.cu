@@ -28,7 +28,8 @@ constexpr int kRegistersMoving = 72, kRegistersAdding = 216;
 constexpr int kTileRows = 256, kTileFeatures = 256;
 // A stage is free when the matrix instructions have read it, its scales when they have been multiplied by: up to two groups later.
 constexpr int kManyStages = 6, kManyScales = kManyStages + 2, kOperandBytes = kBlock * kBlock, kManyScaleBytes = (kBlock + 4) * 4, kTiles = 4;
-constexpr int kManySmem = kManyStages * 2 * kOperandBytes + kManyScales * kManyScaleBytes + kTiles * 16 + (2 * kManyStages + kManyScales + 4 + 2 * kTiles) * 8 + 16 + 1024;
+constexpr int kOddPitch = 34, kOddBytes = 32 * kOddPitch * 2;       // a warp's 32 rows of 32 results, where they leave by twos of bytes
+constexpr int kManySmem = kManyStages * 2 * kOperandBytes + 8 * kOddBytes + kManyScales * kManyScaleBytes + kTiles * 16 + (2 * kManyStages + kManyScales + 4 + 2 * kTiles) * 8 + 16 + 1024;
 constexpr int kRowTilesTogether = 8;
 
 // What the pair does next: rows first .. first + count - 1 of the call (both blocks'), features from `feature` on.  Count 0: no more.
@@ -55,6 +56,9 @@ __global__ void __launch_bounds__(256) pick_kernel(const ar_matmul_fp8_args a, u
     }
 }
 
+// kOdd: rows of out that do not lie on 16 bytes.  (A kernel of its own: with both ways to store in one, the loops before them take a third
+// longer, for want of registers.)
+template <bool kOdd>
 __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_constant__ Product p, const __grid_constant__ CUtensorMap weight,
                                                                const __grid_constant__ CUtensorMap x) {
     constexpr int S = kManyStages, Q = kManyScales;
@@ -62,7 +66,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
     const ar_matmul_fp8_args &a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t base = (shared_address(raw) + 1023) & ~1023u;
-    const uint32_t rows_at = base, weights = rows_at + S * kOperandBytes, scales = weights + S * kOperandBytes, tiles_at = scales + Q * kManyScaleBytes;
+    const uint32_t rows_at = base, weights = rows_at + S * kOperandBytes, odd_at = weights + S * kOperandBytes, scales = odd_at + 8 * kOddBytes, tiles_at = scales + Q * kManyScaleBytes;
     // full: block 0's, both blocks' operands; scaled: the scales; empty: a stage's; sums_full, sums_empty (block 0's): the halves of
     // tensor memory; known, used: the next tiles
     const uint32_t full = tiles_at + kTiles * 16, scaled = full + S * 8, empty = scaled + Q * 8, sums_full = empty + S * 8, sums_empty = sums_full + 16;
@@ -233,8 +237,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
         registers_up<kRegistersAdding>();
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t empty_of_0 = cluster_address(sums_empty, 0);
-        // stores of 32, 16 and 2 bytes
-        const int wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride % 16 == 0 ? 16 : reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.out_stride % 8 == 0 ? 8 : 1;
+        const bool wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0 && a.out_stride % 16 == 0;      // stores of 32 bytes
         Ring<Q> words_of;
         Ring<2> sums;
         // (written out for either width: one loop that asks which keeps its sums in registers a third as fast)
@@ -274,9 +277,30 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
                 __syncwarp();
                 if (lane == 0) cluster_bar_arrive(empty_of_0 + 8 * sums.at);
             }
+            const int there = min(a.out_dim - feature, kOwn);
+            if constexpr (kOdd) {
+                // Rows that do not lie on 16 bytes: 32 features at a time by way of shared memory, a row to a store.
+                uint16_t *const odd = reinterpret_cast<uint16_t *>(shared + (odd_at - base) + (warp - 4) * kOddBytes);
+                const int low = mine - lane;
+#pragma unroll
+                for (int j = 0; j < kOwn; j += 32) {
+                    if (j >= there) break;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float2 v = floats_of(sum[j / 2 + e]);
+                        if (!real) v = make_float2(0, 0);
+                        *reinterpret_cast<uint32_t *>(odd + lane * kOddPitch + 2 * e) = a.dtype == AR_F16 ? to_pair<__half>(v) : to_pair<__nv_bfloat16>(v);
+                    }
+                    __syncwarp();
+                    if (j + lane < there)
+                        for (int r = 0; r < 32 && low + r < count; ++r)
+                            static_cast<uint16_t *>(a.out)[(int64_t)(first + low + r) * a.out_stride + feature + j + lane] = odd[r * kOddPitch + lane];
+                    __syncwarp();
+                }
+                return;
+            }
             if (mine >= count) return;
             uint16_t *const row = static_cast<uint16_t *>(a.out) + (int64_t)(first + mine) * a.out_stride + feature;
-            const int there = min(a.out_dim - feature, kOwn);
 #pragma unroll
             for (int j = 0; j < kOwn; j += 16) {
                 if (j >= there) break;
@@ -287,10 +311,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
                     if (!real) v = make_float2(0, 0);
                     w[e] = a.dtype == AR_F16 ? to_pair<__half>(v) : to_pair<__nv_bfloat16>(v);
                 }
-                if (wide == 16 && j + 16 <= there) {
+                if (wide && j + 16 <= there) {
                     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row + j), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
                                  "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
-                } else if (wide >= 8 && j + 16 <= there) {
+                } else if (j + 16 <= there) {
                     *reinterpret_cast<uint4 *>(row + j) = make_uint4(w[0], w[1], w[2], w[3]);
                     *reinterpret_cast<uint4 *>(row + j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
                 } else {
@@ -324,7 +348,8 @@ cudaError_t start_many(const Product &p, cudaStream_t s, int multiprocessors) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev >= 64 || !*(volatile bool *)&ready[dev])) {
-        e = cudaFuncSetAttribute(many_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kManySmem);
+        e = cudaFuncSetAttribute(many_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kManySmem);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(many_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kManySmem);
         if (e == cudaSuccess && dev < 64) *(volatile bool *)&ready[dev] = true;
     }
     if (e != cudaSuccess) return e;
@@ -346,7 +371,8 @@ cudaError_t start_many(const Product &p, cudaStream_t s, int multiprocessors) {
     if (a.row_of) in_order.x_rows = a.rows;
     if (!map_weight(&weight, a, kBlock) || !map_rows(&x, in_order, kBlock)) return cudaErrorInvalidValue;
     const int64_t units = most_tiles(a, kTileRows) * ((a.out_dim + kTileFeatures - 1) / kTileFeatures), pairs = multiprocessors / 2;
-    return launch_next(many_kernel, dim3((unsigned)(2 * std::min(2 * units, pairs))), kManyThreads, kManySmem, s, 2, q, weight, x);
+    const bool odd = reinterpret_cast<uintptr_t>(a.out) % 16 != 0 || a.out_stride % 8 != 0;
+    return launch_next(odd ? many_kernel<true> : many_kernel<false>, dim3((unsigned)(2 * std::min(2 * units, pairs))), kManyThreads, kManySmem, s, 2, q, weight, x);
 }
 
 int take_many_status(int *code) {
