@@ -9,6 +9,7 @@
 
 #include "ar_ffn.h"
 #include "ar_kv4.cuh"
+#include "ar_tensor.cuh"
 
 namespace {
 
@@ -30,13 +31,19 @@ __device__ __forceinline__ float top_of(float a, float b, float c) {
 
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdiv_rn(g, 1.0f + expf(-g)) * u; }
 
-// The same for gates from -8 on, by the hardware's power of two and reciprocal.  Its argument, up to 11.6, is rounded by 2^-21 and
-// off by 2^-22.6 for log2(e)'s sake: exp(-g) is off by less than 2^-20.5 with the instruction's own 2^-22, y by less than 2^-19.9.
-__device__ __forceinline__ float quick_silu_mul(float g, float u) {
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return g * r * u;
+// Two at a time (the adds and products are instructions of two), for gates from -8 on, by the hardware's power of two and reciprocal.  The
+// power's argument, up to 11.6, is rounded by 2^-21 and off by 2^-22.6 for log2(e)'s sake: exp(-g) is off by less than 2^-20.5
+// with the instruction's own 2^-22, y by less than 2^-19.9.
+__device__ __forceinline__ float2 quick_silu_mul(float2 g, float2 u) {
+    float2 e, r;
+    const unsigned long long gates = pair_of_floats(g.x, g.y);
+    e = floats_of(mul2(gates, pair_of_floats(-1.4426950408889634f, -1.4426950408889634f)));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    r = floats_of(add2(pair_of_floats(e.x, e.y), pair_of_floats(1, 1)));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r.y));
+    return floats_of(mul2(mul2(gates, pair_of_floats(r.x, r.y)), pair_of_floats(u.x, u.y)));
 }
 
 // A group's scale, and what its values are multiplied by, from its largest value.
@@ -56,10 +63,10 @@ template <typename T> __device__ __forceinline__ float values(const Vec &g, cons
     float low = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float2 a = pair_of<T>(g.u[e]), b = pair_of<T>(u.u[e]);
-        low = fminf(fminf(low, a.x), a.y);
-        y[2 * e] = quick_silu_mul(a.x, b.x);
-        y[2 * e + 1] = quick_silu_mul(a.y, b.y);
+        const float2 a = pair_of<T>(g.u[e]), v = quick_silu_mul(a, pair_of<T>(u.u[e]));
+        asm("min.f32 %0, %0, %1, %2;" : "+f"(low) : "f"(a.x), "f"(a.y));
+        y[2 * e] = v.x;
+        y[2 * e + 1] = v.y;
     }
     if (low < -8.0f) {          // (seldom; y is the smaller the more so)
 #pragma unroll
@@ -76,10 +83,14 @@ template <typename T> __device__ __forceinline__ float values(const Vec &g, cons
 
 __device__ __forceinline__ uint2 rounded(const float (&y)[8], float2 s) {
     uint32_t b[4];
+    if (s.y != 0) {
+        const unsigned long long factor = pair_of_floats(s.y, s.y);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float2 v = s.y != 0 ? make_float2(y[2 * e] * s.y, y[2 * e + 1] * s.y) : make_float2(__fdiv_rn(y[2 * e], s.x), __fdiv_rn(y[2 * e + 1], s.x));
-        b[e] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+        for (int e = 0; e < 4; ++e) b[e] = __nv_cvt_float2_to_fp8x2(floats_of(mul2(pair_of_floats(y[2 * e], y[2 * e + 1]), factor)), __NV_SATFINITE, __NV_E4M3);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            b[e] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(y[2 * e], s.x), __fdiv_rn(y[2 * e + 1], s.x)), __NV_SATFINITE, __NV_E4M3);
     }
     return make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
 }
