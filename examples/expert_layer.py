@@ -62,7 +62,9 @@ def layer(ranks, handle, norm, router, i, chosen, xs, residuals):
             partial.append(tda.experts_sum(y, r.weights, r.place))
             sums.append(torch.empty_like(partial[-1]))
             routes.append(r)
-    handle.allreduce_each(partial, sums, [r.stream for r in ranks])
+    # (one launch of all ranks: products of many rows take whole multiprocessors, and a rank that waited for another's on all of
+    # them would keep it from running)
+    handle.allreduce_all(partial, sums, [r.stream for r in ranks])
     nxt, after = [], []
     for rank, total, residual in zip(ranks, sums, residuals):
         with torch.cuda.stream(rank.stream):

@@ -42,6 +42,9 @@ extern "C" {
  * Weights, x and out whose rows all begin on 16 bytes take the fast kernels (x_stride, weight_stride and expert_stride
  * multiples of 16 bytes; out is free), others a slower one.
  * out must not overlap an input.
+ * Logical ranks on one GPU: a product of many rows needs whole multiprocessors.  An exchange that is launched rank by rank
+ * (ar_allreduce) and has a block on each of them, waiting for a rank whose product has not begun, keeps it from beginning
+ * until the exchange's own limit; behind such products use the calls that launch all ranks at once (ar_allreduce_all).
  * Errors: AR_EINVAL, AR_ETOOBIG (rows or x_rows > 2^30, dim > 2^20, out_dim > 2^20, experts > 1024), AR_ECUDA.
  */
 typedef struct ar_matmul_fp8_args {

@@ -465,11 +465,13 @@ PyObject *matmul(PyObject *const *o) {
         check("offsets", offsets, dev, at::kInt, 1, true);
         check_shape("offsets", offsets, {E + 1});
         if (E < 1) refuse("weight", "no experts");
+        if (o[6] != Py_None && may_share(tensor("out", o[6]), offsets)) refuse("out", "overlaps offsets");
         a.offsets = static_cast<int32_t *>(offsets.data_ptr());
     }
     if (o[5] != Py_None) {
         const Tensor &of = tensor("rows", o[5]);
         check("rows", of, dev, at::kInt, 1, true);
+        if (o[6] != Py_None && may_share(tensor("out", o[6]), of)) refuse("out", "overlaps rows");
         rows = of.size(0);
         a.row_of = static_cast<int32_t *>(of.data_ptr());
     }

@@ -1,5 +1,8 @@
 """The operators of include/ar_ffn.h against plain implementations in 64 bits (tests/ffn_helpers.py)."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -231,6 +234,84 @@ def test_many_experts_most_without_rows():
         offsets.append(offsets[-1] + c)
     out = _tda().experts_matmul_fp8(x.cuda(), xs.cuda(), w.cuda(), ws.cuda(), _i32(offsets))
     _check_experts(out, x, xs, w, ws, offsets)
+
+
+@pytest.mark.parametrize("M,N,K,row_scale", [(5000, 2304, 256, False), (3, 1280, 20000, False), (40, 130, 9000, True), (2500, 333, 384, True), (1100, 4104, 272, False)])
+def test_products_of_many_tiles_and_long_rows(M, N, K, row_scale):
+    """Several tiles to a block, rings of stages gone round many times, an odd output, channels shared by clusters."""
+    x, xs, w, ws = _operands(M + N, M, N, K, row_scale=row_scale)
+    H.check_product(_tda().matmul_fp8(x.cuda(), xs.cuda(), w.cuda(), ws.cuda()), x, xs, w, ws)
+
+
+@pytest.mark.parametrize("E,each,N,K,row_scale", [(100, 3, 512, 256, True), (300, 1, 256, 144, False), (12, 40, 1024, 640, False), (7, 500, 520, 384, True)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_experts_of_many_tiles(E, each, N, K, row_scale, gather):
+    counts = [each + (i * 7) % 3 for i in range(E)]
+    offsets = [0]
+    for n in counts:
+        offsets.append(offsets[-1] + n)
+    R = offsets[-1]
+    T = max(1, R // 3) if gather else R
+    x, xs, w, ws = _operands(E + each, T, N, K, E, row_scale)
+    rows = torch.randint(0, T, (R,), generator=H.gen(E)).tolist() if gather else None
+    out = _tda().experts_matmul_fp8(x.cuda(), xs.cuda(), w.cuda(), ws.cuda(), _i32(offsets), rows=_i32(rows) if gather else None, dtype=torch.float16)
+    _check_experts(out, x, xs, w, ws, offsets, rows)
+
+
+def test_products_on_several_streams_at_once():
+    """Calls of all kinds that overlap on the GPU, each many times: the same results as alone."""
+    tda = _tda()
+    jobs = []
+    for seed, (M, N, K) in enumerate(((3, 1280, 4096), (60, 2048, 2048), (100, 2048, 1024), (1500, 1024, 512))):
+        ops = [t.cuda() for t in _operands(seed, M, N, K)]
+        jobs.append((lambda ops=ops: tda.matmul_fp8(*ops)))
+    x, xs, w, ws = _operands(9, 200, 512, 512, 8)
+    o, rows = _i32([0, 100, 300, 300, 500, 900, 1000, 1400, 1600]), torch.randint(0, 200, (1600,), generator=H.gen(3)).int().cuda()
+    ex = [t.cuda() for t in (x, xs, w, ws)]
+    jobs.append(lambda: tda.experts_matmul_fp8(*ex, o, rows=rows))
+    small = _i32([0, 1, 5, 9, 9, 20, 22, 29, 30])
+    jobs.append(lambda: tda.experts_matmul_fp8(*ex, small, rows=rows[:30]))
+    alone = [j() for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[] for _ in jobs]
+    for _ in range(20):
+        for j, s, g in zip(jobs, streams, got):
+            with torch.cuda.stream(s):
+                g.append(j())
+    torch.cuda.synchronize()
+    for a, g in zip(alone, got):
+        assert all(torch.equal(a, b) for b in g)
+    tda.matmul_fp8_check()
+
+
+def test_a_first_call_under_capture():
+    """A process whose first calls are captured: nothing that they set up needs another call before."""
+    code = """
+import sys, torch
+sys.path.insert(0, %r)
+import tensor_decode_all_gb300 as tda
+from tests import ffn_helpers as H
+g = H.gen(1)
+def operands(M, N, K):
+    return [t.cuda() for t in (H.eights(g, M, K), H.scales(g, M, -(-K // 128)), H.eights(g, N, K), H.scales(g, -(-N // 128), -(-K // 128)))]
+small, large = operands(5, 640, 2048), operands(700, 512, 512)
+logits, x = torch.randn(900, 64, device="cuda"), torch.randn(8, 256, device="cuda").half()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    a, b, r, s = tda.matmul_fp8(*small), tda.matmul_fp8(*large), tda.route_experts(logits, 4), tda.silu_mul_fp8(x)
+    t = tda.experts_sum(x.repeat(4, 1), torch.ones(8, 2, device="cuda"), torch.arange(16, dtype=torch.int32, device="cuda").view(8, 2))
+graph.replay()
+torch.cuda.synchronize()
+for out, ops in ((a, small), (b, large)):
+    H.check_product(out, *(v.cpu() for v in ops))
+H.check_silu(*s, x.cpu(), 128)
+assert torch.equal(r.experts, tda.route_experts(logits, 4).experts)
+tda.matmul_fp8_check()
+""" % os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 # -------------------------------------------------------------- route_experts
