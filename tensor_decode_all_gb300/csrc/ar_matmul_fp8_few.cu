@@ -8,8 +8,8 @@
 // scales by word copies beside them.  Rows that are picked by number come 16 bytes to a lane.
 //
 // Where there are fewer tiles than the GPU has room for, a cluster of blocks shares a tile's channels: each block
-// sums its part and leaves its sums in its shared memory, and each adds up some of the rows from all blocks, in their
-// order.
+// sums its part and sends its sums to the blocks' shared memory, each row's to one of them, which adds them up in the blocks' order as soon
+// as a barrier has counted their bytes: no meeting of the cluster at the end.
 #include <algorithm>
 
 #include "ar_matmul_fp8.cuh"
@@ -29,10 +29,13 @@ template <int TOK> struct Few {
     static constexpr int Blocks = TOK <= 64 ? 2 : 1, Halves = TOK <= 64 ? 1 : 2, Own = TOK / Halves;
     static constexpr int Threads = 64 + 128 * Halves;               // copies, instructions, warps that add up
     static constexpr int Stages = (224 * 1024 / Blocks - 4 * ScaleBytes) / (StageBytes + ScaleBytes);
+    // The sums that a block of a cluster is sent take the place of a stage (two).
+    static constexpr int PartBytes = TOK * kBlock * 4, Given = TOK <= 64 ? 1 : 2;
+    static constexpr int Room = std::max(Stages * StageBytes, (Stages - Given) * StageBytes + PartBytes);
     // A stage is free when the matrix instructions have read it, its scales when they have been multiplied by: up to
     // `Buffers` groups later.
     static constexpr int Scales = Stages + Buffers;
-    static constexpr int Smem = Stages * StageBytes + Scales * ScaleBytes + (2 * Stages + Scales + 2 * Buffers) * 8 + 16 + 1024;
+    static constexpr int Smem = Room + Scales * ScaleBytes + (2 * Stages + Scales + 2 * Buffers + 1) * 8 + 16 + 1024;
 };
 
 // kPicked: row_of is given.
@@ -45,9 +48,11 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
     const ar_matmul_fp8_args &a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t base = (shared_address(raw) + 1023) & ~1023u;
-    const uint32_t weights = base, rows_at = weights + S * F::WeightBytes, scales = rows_at + S * F::RowBytes;
+    // a stage: the weight's tile, and the rows after it
+    const uint32_t scales = base + F::Room;
     const uint32_t full = scales + Q * F::ScaleBytes, empty = full + S * 8, scaled = empty + S * 8, sums_full = scaled + Q * 8, sums_empty = sums_full + B * 8;
-    const uint32_t tmem_at = sums_empty + B * 8;
+    const uint32_t sent = sums_empty + B * 8, tmem_at = sent + 8;
+    const uint32_t stages = cluster > 1 ? S - F::Given : S, parts = base + (S - F::Given) * F::StageBytes;
     uint8_t *const shared = raw + (base - shared_address(raw));
     if (warp == 0) {
         if (lane == 0) {
@@ -60,7 +65,9 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
                 bar_init(sums_full + 8 * i, 1);
                 bar_init(sums_empty + 8 * i, 4 * F::Halves);
             }
+            bar_init(sent, 1);
             bar_init_done();
+            if (cluster > 1) bar_expect(sent, F::PartBytes);
             tensor_prefetch(&weight);
             tensor_prefetch(&x);
         }
@@ -69,6 +76,7 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
     }
     tmem_before_sync();
     __syncthreads();
+    if (cluster > 1) cluster_sync_all();           // (nobody sends to a barrier that is not there yet)
     tmem_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(shared + (tmem_at - base));
     after_the_stream();
@@ -83,7 +91,7 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
         feature = (int)(row_tiles ? u / row_tiles : u % features) * kBlock;
         return feature < a.out_dim ? rows_of_tile(a, t, TOK) : Rows{0, 0, 0};
     };
-    bool fine = true, any = false, joined = false;     // no wait ran out; there was a tile; the cluster's blocks have met
+    bool fine = true, any = false;     // no wait ran out; there was a tile
     int feature = 0;
     Rows rows = {0, 0, 0};
 
@@ -105,13 +113,13 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
                 scale[i] = r >= 0 ? a.x_scales + r * a.x_scales_stride : nullptr;
             }
             const float *weight_scale = a.weight_scales + ((int64_t)rows.expert * features + feature / kBlock) * p.groups;
-            for (int k = k0; k < k1; ++k, ++issued, stage.next(), words_of.next()) {
+            for (int k = k0; k < k1; ++k, ++issued, stage.next(stages), words_of.next()) {
                 const uint32_t s = stage.at;
                 if (!(fine = bar_wait_warp(empty + 8 * s, stage.parity ^ 1))) break;
-                const uint32_t bar = full + 8 * s, to = rows_at + s * F::RowBytes, words = scales + words_of.at * F::ScaleBytes;
+                const uint32_t bar = full + 8 * s, at = base + s * F::StageBytes, to = at + F::WeightBytes, words = scales + words_of.at * F::ScaleBytes;
                 if (lane == 0) {
                     bar_expect(bar, F::WeightBytes + (kPicked ? 0 : F::RowBytes));
-                    tensor_load(weights + s * F::WeightBytes, &weight, bar, k * kBlock, feature, rows.expert);
+                    tensor_load(at, &weight, bar, k * kBlock, feature, rows.expert);
                     if (!kPicked) tensor_load(to, &x, bar, k * kBlock, rows.first);
                     copy_word(words + 4 * TOK, weight_scale + k, true);
                 }
@@ -128,10 +136,10 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
             }
         }
         if (!fine)                                     // what is under way has to land before the block may end
-            for (int i = max(issued - S, 0); i < issued; ++i)
-                (void)(bar_wait_warp(full + 8 * (i % S), i / S & 1) && bar_wait_warp(scaled + 8 * (i % Q), i / Q & 1));
+            for (int n = stages, i = max(issued - n, 0); i < issued; ++i)
+                (void)(bar_wait_warp(full + 8 * (i % n), i / n & 1) && bar_wait_warp(scaled + 8 * (i % Q), i / Q & 1));
     } else if (warp == 1) {
-        const uint64_t weights_operand = operand_of(weights), rows_operand = operand_of(rows_at);
+        const uint64_t operand = operand_of(base);
         const bool one = elected();
         Ring<S> stage;
         Ring<B> buffer;
@@ -140,12 +148,12 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
             rows = tile_of(u, feature);
             if (rows.count == 0 || (any && cluster > 1)) break;
             any = true;
-            for (int k = k0; k < k1; ++k, ++n, stage.next(), buffer.next()) {
+            for (int k = k0; k < k1; ++k, ++n, stage.next(stages), buffer.next()) {
                 if (!(fine = bar_wait_warp(full + 8 * stage.at, stage.parity, sums_empty + 8 * buffer.at, buffer.parity ^ 1))) break;
                 tmem_after_sync();
                 if (kPicked) written_for_mma();
                 if (one) {
-                    const uint64_t w = weights_operand + stage.at * (F::WeightBytes >> 4), r = rows_operand + stage.at * (F::RowBytes >> 4);
+                    const uint64_t w = operand + stage.at * (F::StageBytes >> 4), r = w + (F::WeightBytes >> 4);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) mma_e4m3(tmem + buffer.at * TOK, w + 2 * i, r + 2 * i, product_shape(kBlock, TOK), i > 0);
                     mma_commit(empty + 8 * stage.at);
@@ -209,28 +217,39 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
                 }
             };
             if (cluster > 1) {
-                // Own sums to own memory (one tile to a cluster: nothing follows in the stages), four rows of a feature side
-                // by side; then some rows from all blocks, added in their order.
-#pragma unroll
-                for (int j = 0; j < Own; j += 4) {
-                    const float2 lo = floats_of(sum[j / 2]), hi = floats_of(sum[j / 2 + 1]);
-                    *reinterpret_cast<float4 *>(shared + (((begin + j) / 4) * kBlock + mine) * 16) = make_float4(lo.x, lo.y, hi.x, hi.y);
-                }
-                __syncwarp();
-                cluster_sync_all();
-                const int each = Own / cluster, low = rank * (TOK / cluster) + begin / cluster;      // rows low .. low + each - 1
+                // Four rows of a feature side by side (or one, where a block has fewer) to the block whose rows they are; then this
+                // block's `mine` rows of all blocks, added in their order.  One tile to a cluster.
+                const int each = TOK / cluster, ways = __ffs(cluster) - 1, own_rows = Own >> ways, low = (begin >> ways);      // of this block's: low .. low + own_rows - 1
+                const float *got = reinterpret_cast<const float *>(shared + (parts - base));
                 auto real = [&](int row) { return !kPicked || (row < rows.count && source_row(a, rows.first + row) >= 0); };
                 if (each >= 4) {
-                    // all loads together: four rows from block i % cluster, the blocks' in turn
-                    const int ways = __ffs(cluster) - 1;
+                    const int quads = each / 4, log = __ffs(quads) - 1;
+#pragma unroll
+                    for (int j = 0; j < Own; j += 4) {
+                        const float2 lo = floats_of(sum[j / 2]), hi = floats_of(sum[j / 2 + 1]);
+                        const int q = (begin + j) / 4, to = q >> log;
+                        cluster_send(cluster_address(parts + ((rank * quads + (q & (quads - 1))) * kBlock + mine) * 16, to), cluster_address(sent, to), make_float4(lo.x, lo.y, hi.x, hi.y));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < Own; ++j) {
+                        const float2 v = floats_of(sum[j / 2]);
+                        const int to = (begin + j) / each;
+                        cluster_send(cluster_address(parts + ((rank * each + (begin + j) % each) * kBlock + mine) * 4, to), cluster_address(sent, to), j & 1 ? v.y : v.x);
+                    }
+                }
+                if (!(fine = bar_wait_warp(sent, 0))) break;
+                if (each >= 4) {
+                    // all loads together: four rows of block i % cluster, the blocks' in turn
+                    const int quads = each / 4;
                     float4 v[Own / 4];
 #pragma unroll
                     for (int i = 0; i < Own / 4; ++i)
-                        v[i] = cluster_load4(cluster_address(base + ((low / 4 + (i >> ways)) * kBlock + mine) * 16, i & (cluster - 1)));
+                        v[i] = reinterpret_cast<const float4 *>(got)[((i & (cluster - 1)) * quads + low / 4 + (i >> ways)) * kBlock + mine];
                     float4 w = v[0];
 #pragma unroll
                     for (int i = 0; i < Own / 4; ++i) {
-                        const int r = i & (cluster - 1), row = low + 4 * (i >> ways);
+                        const int r = i & (cluster - 1), row = rank * each + low + 4 * (i >> ways);
                         w = r == 0 ? v[i] : make_float4(w.x + v[i].x, w.y + v[i].y, w.z + v[i].z, w.w + v[i].w);
                         if (r == cluster - 1) {
                             store(row, real(row) ? w.x : 0.0f);
@@ -240,20 +259,12 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
                         }
                     }
                 } else {
-                    for (int row = low; row < low + each; ++row) {
-                        const uint32_t at = base + ((row / 4) * kBlock + mine) * 16 + row % 4 * 4;
-                        float v[16];
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) v[r] = r < cluster ? cluster_load(cluster_address(at, r)) : 0.0f;
-#pragma unroll
-                        for (int r = 1; r < 16; ++r)
-                            if (r < cluster) v[0] += v[r];
-                        store(row, real(row) ? v[0] : 0.0f);
+                    for (int row = low; row < low + own_rows; ++row) {
+                        float v = got[row * kBlock + mine];
+                        for (int r = 1; r < cluster; ++r) v += got[(r * each + row) * kBlock + mine];
+                        store(rank * each + row, real(rank * each + row) ? v : 0.0f);
                     }
                 }
-                __syncwarp();
-                cluster_sync_all();           // (the others have read)
-                joined = true;
                 break;
             }
 #pragma unroll
@@ -265,13 +276,9 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
         }
     }
     if (!fine && lane == 0) atomicCAS(&g_few_status, 0, AR_ETIMEOUT);
-    if (cluster > 1 && any && !joined) {
-        __syncwarp();
-        cluster_sync_all();
-        cluster_sync_all();
-    }
     tmem_before_sync();
-    __syncthreads();
+    // (a block that gave up waits until no other can send to it any more; one that did not has got all that is sent to it)
+    if (__syncthreads_or(!fine) && cluster > 1) cluster_sync_all();
     tmem_after_sync();
     if (warp == 1) tmem_free(tmem, F::Columns);
 }

@@ -60,11 +60,11 @@ __device__ __forceinline__ bool elected() {
     return r;
 }
 
-// Where a warp stands in a ring of N stages: the stage, and the parity of its present round.
+// Where a warp stands in a ring of N stages (or of fewer): the stage, and the parity of its present round.
 template <int N> struct Ring {
     uint32_t at = 0, parity = 0;
-    __device__ __forceinline__ void next() {
-        if (++at == N) {
+    __device__ __forceinline__ void next(uint32_t stages = N) {
+        if (++at == stages) {
             at = 0;
             parity ^= 1;
         }
@@ -222,15 +222,14 @@ __device__ __forceinline__ uint32_t cluster_address(uint32_t own, uint32_t rank)
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(own), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float cluster_load(uint32_t at) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
+// Numbers sent to another block's memory, whose barrier counts their bytes.
+__device__ __forceinline__ void cluster_send(uint32_t to, uint32_t bar, float v) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(to), "f"(v), "r"(bar) : "memory");
 }
-__device__ __forceinline__ float4 cluster_load4(uint32_t at) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-    return v;
+__device__ __forceinline__ void cluster_send(uint32_t to, uint32_t bar, float4 v) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w),
+                 "r"(bar)
+                 : "memory");
 }
 
 // ------------------------------------------------------- pairs of binary32 numbers
