@@ -209,60 +209,62 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
                 if (lane == 0) bar_arrive(sums_empty + 8 * buffer.at);
             }
             if (!fine) break;
+            uint16_t *const here = static_cast<uint16_t *>(a.out) + (int64_t)rows.first * a.out_stride + feature + mine;
+            const int high = feature + mine < a.out_dim ? rows.count : 0;
+            const bool half = a.dtype == AR_F16;
+            // (without a branch: one to a store took longer than the rest)
             auto store = [&](int row, float v) {
-                if (row < rows.count && feature + mine < a.out_dim) {
-                    const int64_t at = (rows.first + row) * a.out_stride + feature + mine;
-                    if (a.dtype == AR_F16) static_cast<__half *>(a.out)[at] = __float2half_rn(v);
-                    else static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
-                }
+                const uint16_t h = __half_as_ushort(__float2half_rn(v)), b = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+                asm volatile("{ .reg .pred p; setp.ne.b32 p, %2, 0; @p st.global.b16 [%0], %1; }" ::"l"(here + row * a.out_stride), "h"((uint16_t)(half ? h : b)), "r"((int)(row < high))
+                             : "memory");
             };
             if (cluster > 1) {
                 // Four rows of a feature side by side (or one, where a block has fewer) to the block whose rows they are; then this
-                // block's `mine` rows of all blocks, added in their order.  One tile to a cluster.
-                const int each = TOK / cluster, ways = __ffs(cluster) - 1, own_rows = Own >> ways, low = (begin >> ways);      // of this block's: low .. low + own_rows - 1
-                const float *got = reinterpret_cast<const float *>(shared + (parts - base));
+                // block's rows of all blocks, added in their order.  One tile to a cluster.
+                const int ways = __ffs(cluster) - 1, each = TOK >> ways, own_rows = Own >> ways, low = begin >> ways;      // this thread's: low .. low + own_rows - 1 of the block's
+                const float *got = reinterpret_cast<const float *>(shared + (parts - base)) + mine;
                 auto real = [&](int row) { return !kPicked || (row < rows.count && source_row(a, rows.first + row) >= 0); };
                 if (each >= 4) {
-                    const int quads = each / 4, log = __ffs(quads) - 1;
+                    uint32_t to = 0;
 #pragma unroll
                     for (int j = 0; j < Own; j += 4) {
+                        const int row = (begin + j) & (each - 1);
+                        if (j == 0 || row == 0) to = cluster_address(parts, (begin + j) / each);
                         const float2 lo = floats_of(sum[j / 2]), hi = floats_of(sum[j / 2 + 1]);
-                        const int q = (begin + j) / 4, to = q >> log;
-                        cluster_send(cluster_address(parts + ((rank * quads + (q & (quads - 1))) * kBlock + mine) * 16, to), cluster_address(sent, to), make_float4(lo.x, lo.y, hi.x, hi.y));
+                        cluster_send(to + ((rank * each + row) * kBlock + mine * 4) * 4, to + (sent - parts), make_float4(lo.x, lo.y, hi.x, hi.y));
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < Own; ++j) {
+                        const int row = j & (each - 1);
+                        const uint32_t to = cluster_address(parts, j >> (each - 1));       // (each: 1 or 2)
                         const float2 v = floats_of(sum[j / 2]);
-                        const int to = (begin + j) / each;
-                        cluster_send(cluster_address(parts + ((rank * each + (begin + j) % each) * kBlock + mine) * 4, to), cluster_address(sent, to), j & 1 ? v.y : v.x);
+                        cluster_send(to + ((rank * each + row) * kBlock + mine) * 4, to + (sent - parts), j & 1 ? v.y : v.x);
                     }
                 }
                 if (!(fine = bar_wait_warp(sent, 0))) break;
                 if (each >= 4) {
-                    // all loads together: four rows of block i % cluster, the blocks' in turn
-                    const int quads = each / 4;
-                    float4 v[Own / 4];
-#pragma unroll
-                    for (int i = 0; i < Own / 4; ++i)
-                        v[i] = reinterpret_cast<const float4 *>(got)[((i & (cluster - 1)) * quads + low / 4 + (i >> ways)) * kBlock + mine];
-                    float4 w = v[0];
-#pragma unroll
-                    for (int i = 0; i < Own / 4; ++i) {
-                        const int r = i & (cluster - 1), row = rank * each + low + 4 * (i >> ways);
-                        w = r == 0 ? v[i] : make_float4(w.x + v[i].x, w.y + v[i].y, w.z + v[i].z, w.w + v[i].w);
-                        if (r == cluster - 1) {
-                            store(row, real(row) ? w.x : 0.0f);
-                            store(row + 1, real(row + 1) ? w.y : 0.0f);
-                            store(row + 2, real(row + 2) ? w.z : 0.0f);
-                            store(row + 3, real(row + 3) ? w.w : 0.0f);
+#pragma unroll 2
+                    for (int i = 0; i < own_rows; i += 4) {
+                        const float *from = got + (low + i) * kBlock + mine * 3;      // (four to a feature)
+                        float4 w = *reinterpret_cast<const float4 *>(from);
+#pragma unroll 4
+                        for (int r = 1; r < cluster; ++r) {
+                            const float4 v = *reinterpret_cast<const float4 *>(from + r * each * kBlock);
+                            w = make_float4(w.x + v.x, w.y + v.y, w.z + v.z, w.w + v.w);
                         }
+                        const int row = rank * each + low + i;
+                        store(row, real(row) ? w.x : 0.0f);
+                        store(row + 1, real(row + 1) ? w.y : 0.0f);
+                        store(row + 2, real(row + 2) ? w.z : 0.0f);
+                        store(row + 3, real(row + 3) ? w.w : 0.0f);
                     }
                 } else {
-                    for (int row = low; row < low + own_rows; ++row) {
-                        float v = got[row * kBlock + mine];
-                        for (int r = 1; r < cluster; ++r) v += got[(r * each + row) * kBlock + mine];
-                        store(rank * each + row, real(rank * each + row) ? v : 0.0f);
+                    for (int i = 0; i < each; ++i) {
+                        float v = got[i * kBlock];
+#pragma unroll 4
+                        for (int r = 1; r < cluster; ++r) v += got[(r * each + i) * kBlock];
+                        store(rank * each + i, real(rank * each + i) ? v : 0.0f);
                     }
                 }
                 break;
