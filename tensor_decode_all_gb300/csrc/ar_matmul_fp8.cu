@@ -150,8 +150,9 @@ int multiprocessors_of_device() {
 }
 
 // Which of the fast kernels: the one that takes less time by its steps (groups of 128 channels that follow each other) in the tiles that follow each
-// other.  A step took 0.55 us with 128 rows to a block and 0.39 with 256 to a pair: 128 rows of 8192 times 8192 features 23 us
-// against 27, 256 35 against 27; 384 rows times 1280 features, whose channels are shared by clusters, 14.8 against 26.  Up to 64 rows (32 to an expert)
+// other, in units of 10 ns: with 128 rows to a block 0.5 us a step and 4 us besides, 6.3 where clusters share the channels; with 256 to a pair
+// 0.39 and 4.5, and 3 more to a tile whose results leave by twos of bytes.  128 rows of 8192 times 8192 features took 21 us against 27,
+// 256 35 against 27; 384 rows times 1280 features 14.8 against 26; 97 rows of 816 times 10853 8.3 against 11.3.  Up to 64 rows (32 to an expert)
 // the weights' bytes count, and the first is always faster (64 rows: 18 against 27; 32 experts of 32 rows 48 against 53, of 64
 // rows 76 against 54).
 bool takes_many(const ar_matmul_fp8_args &a) {
@@ -162,7 +163,8 @@ bool takes_many(const ar_matmul_fp8_args &a) {
     const int64_t tiles = experts * up(rows, 128) * up(a.out_dim, 128), pairs = experts * up(rows, 256) * up(a.out_dim, 256);
     int64_t share = 1;
     while (share < 16 && tiles * share * 2 <= multiprocessors && groups >= share * 4) share *= 2;
-    return 39 * up(pairs, multiprocessors / 2) * groups < 55 * up(tiles * share, multiprocessors) * up(groups, share);
+    const bool odd = misaligned(a.out, 16) || a.out_stride % 8 != 0;
+    return 450 + up(pairs, multiprocessors / 2) * (39 * groups + (odd ? 300 : 0)) < (share > 1 ? 630 : 400) + 50 * up(tiles * share, multiprocessors) * up(groups, share);
 }
 
 }  // namespace

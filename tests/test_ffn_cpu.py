@@ -117,8 +117,8 @@ def test_the_products_workspace(lib):
     def size(**kw):
         return lib.ar_matmul_fp8_workspace(ctypes.addressof(_matmul(**kw)))
     assert size(rows=5000, x_rows=5000) == 0 and size(row_of=A) == 0 and size(row_of=A, rows=5000, dim=0) == 0
-    assert size(row_of=A, rows=5000) == 5000 * (256 + 2 * 4)
-    assert size(row_of=A, rows=5000, dim=250, x_row_scales=1) == 5000 * (256 + 4)
+    assert size(row_of=A, rows=5000, dim=2560, out_dim=2048) == 5000 * (2560 + 20 * 4)
+    assert size(row_of=A, rows=5000, dim=2550, out_dim=2048, x_row_scales=1) == 5000 * (2560 + 4)
     assert size(row_of=A, offsets=A, experts=64, rows=500) == 0 and size(row_of=A, offsets=A, experts=0, rows=5000) == 0
     assert lib.ar_matmul_fp8_workspace(None) == 0
 
