@@ -28,8 +28,10 @@ constexpr int kRegistersMoving = 72, kRegistersAdding = 216;
 constexpr int kTileRows = 256, kTileFeatures = 256;
 // A stage is free when the matrix instructions have read it, its scales when they have been multiplied by: up to two groups later.
 constexpr int kManyStages = 6, kManyScales = kManyStages + 2, kOperandBytes = kBlock * kBlock, kManyScaleBytes = (kBlock + 4) * 4, kTiles = 4;
+constexpr int kFourScales = 3, kFourBytes = (kBlock + 2) * 16;      // (four groups' scales: those of 12 groups reach past two that are added and six that are copied)
+constexpr int kScaleRoom = std::max(kFourScales * kFourBytes, kManyScales * kManyScaleBytes);
 constexpr int kOddPitch = 34, kOddBytes = 32 * kOddPitch * 2;       // a warp's 32 rows of 32 results, where they leave by twos of bytes
-constexpr int kManySmem = kManyStages * 2 * kOperandBytes + 8 * kOddBytes + kManyScales * kManyScaleBytes + kTiles * 16 + (2 * kManyStages + kManyScales + 4 + 2 * kTiles) * 8 + 16 + 1024;
+constexpr int kManySmem = kManyStages * 2 * kOperandBytes + 8 * kOddBytes + kScaleRoom + kTiles * 16 + (2 * kManyStages + kManyScales + 4 + 2 * kTiles) * 8 + 16 + 1024;
 constexpr int kRowTilesTogether = 8;
 
 // What the pair does next: rows first .. first + count - 1 of the call (both blocks'), features from `feature` on.  Count 0: no more.
@@ -58,15 +60,17 @@ __global__ void __launch_bounds__(256) pick_kernel(const ar_matmul_fp8_args a, u
 
 // kOdd: rows of out that do not lie on 16 bytes.  (A kernel of its own: with both ways to store in one, the loops before them take a third
 // longer, for want of registers.)
-template <bool kOdd>
+// kFours: scales come 16 bytes at a time, four groups' together, because the copies of single words (a line for each) take 4 to 10% of the time:
+// 8191 x 8192 -> 5120 237 to 245 us against 260 to 265, 32792 rows of 64 experts 266 to 286 against 290 to 297, in a row of calls.
+template <bool kOdd, bool kFours>
 __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_constant__ Product p, const __grid_constant__ CUtensorMap weight,
                                                                const __grid_constant__ CUtensorMap x) {
-    constexpr int S = kManyStages, Q = kManyScales;
+    constexpr int S = kManyStages, Q = kFours ? kFourScales : kManyScales;
     extern __shared__ uint8_t raw[];
     const ar_matmul_fp8_args &a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t base = (shared_address(raw) + 1023) & ~1023u;
-    const uint32_t rows_at = base, weights = rows_at + S * kOperandBytes, odd_at = weights + S * kOperandBytes, scales = odd_at + 8 * kOddBytes, tiles_at = scales + Q * kManyScaleBytes;
+    const uint32_t rows_at = base, weights = rows_at + S * kOperandBytes, odd_at = weights + S * kOperandBytes, scales = odd_at + 8 * kOddBytes, tiles_at = scales + kScaleRoom;
     // full: block 0's, both blocks' operands; scaled: the scales; empty: a stage's; sums_full, sums_empty (block 0's): the halves of
     // tensor memory; known, used: the next tiles
     const uint32_t full = tiles_at + kTiles * 16, scaled = full + S * 8, empty = scaled + Q * 8, sums_full = empty + S * 8, sums_empty = sums_full + 16;
@@ -123,7 +127,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
             const uint32_t full_of_0 = cluster_address(full, 0);
             Ring<S> stage;
             Ring<Q> words_of;
-            int issued = 0;
+            int issued = 0, scales_asked = 0;
             while (fine) {
                 const Tile tile = next_tile();
                 if (tile.count == 0) break;
@@ -138,24 +142,36 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
                 // the weight's scales of both halves, by two lanes
                 const int half = tile.feature / kBlock + lane;
                 const float *weight_scale = lane < 2 && half < blocks ? a.weight_scales + ((int64_t)tile.expert * blocks + half) * p.groups : nullptr;
-                for (int k = 0; k < p.groups; ++k, ++issued, stage.next(), words_of.next()) {
+                for (int k = 0; k < p.groups; ++k, ++issued, stage.next()) {
                     const uint32_t s = stage.at;
                     if (!(fine = bar_wait_warp(empty + 8 * s, stage.parity ^ 1))) break;
-                    const uint32_t bar = full_of_0 + 8 * s, to = rows_at + s * kOperandBytes, words = scales + words_of.at * kManyScaleBytes;
+                    const uint32_t bar = full_of_0 + 8 * s, to = rows_at + s * kOperandBytes, words = scales + words_of.at * (kFours ? kFourBytes : kManyScaleBytes);
                     if (lane == 0) {
                         if (rank == 0) bar_expect(full + 8 * s, 4 * kOperandBytes);
                         pair_tensor_load(weights + s * kOperandBytes, &weight, bar, k * kBlock, tile.feature + rank * kBlock, tile.expert);
                         pair_tensor_load(to, &x, bar, k * kBlock, first);
                     }
+                    if constexpr (kFours) {
+                        if (k % 4 == 0) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) copy_word(words + 4 * (lane + 32 * i), scale[i] ? scale[i] + (a.x_row_scales ? 0 : k) : a.x_scales, scale[i] != nullptr);
-                    if (lane < 2) copy_word(words + 4 * (kBlock + lane), weight_scale ? weight_scale + k : a.weight_scales, weight_scale != nullptr);
-                    bar_arrive_copies(scaled + 8 * words_of.at);
+                            for (int i = 0; i < 4; ++i) copy_piece(words + 16 * (lane + 32 * i), scale[i] ? scale[i] + k : a.x_scales, scale[i] ? 16 : 0);
+                            if (lane < 2) copy_piece(words + 16 * (kBlock + lane), weight_scale ? weight_scale + k : a.weight_scales, weight_scale ? 16 : 0);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) copy_word(words + 4 * (lane + 32 * i), scale[i] ? scale[i] + (a.x_row_scales ? 0 : k) : a.x_scales, scale[i] != nullptr);
+                        if (lane < 2) copy_word(words + 4 * (kBlock + lane), weight_scale ? weight_scale + k : a.weight_scales, weight_scale != nullptr);
+                    }
+                    if (!kFours || k % 4 == 0) {
+                        bar_arrive_copies(scaled + 8 * words_of.at);
+                        words_of.next();
+                        ++scales_asked;
+                    }
                     __syncwarp();
                 }
             }
             if (!fine) {                                   // what is under way has to land before the blocks may end
-                for (int i = max(issued - S, 0); i < issued; ++i) (void)bar_wait_warp(scaled + 8 * (i % Q), i / Q & 1);
+                for (int i = max(scales_asked - Q, 0); i < scales_asked; ++i) (void)bar_wait_warp(scaled + 8 * (i % Q), i / Q & 1);
                 if (rank == 0)
                     for (int i = max(issued - S, 0); i < issued; ++i) (void)bar_wait_warp(full + 8 * (i % S), i / S & 1);
             }
@@ -253,10 +269,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) many_kernel(const __grid_cons
             unsigned long long sum[kOwn / 2];
 #pragma unroll
             for (int j = 0; j < kOwn / 2; ++j) sum[j] = 0;
-            for (int k = 0; k < p.groups; ++k, words_of.next(), sums.next()) {
-                if (!(fine = bar_wait_warp(scaled + 8 * words_of.at, words_of.parity))) return;
-                const float *words = reinterpret_cast<const float *>(shared + (scales - base)) + words_of.at * (kManyScaleBytes / 4);
-                const float f = words[mine] * words[kBlock + block];
+            for (int k = 0; k < p.groups; ++k, sums.next()) {
+                if ((!kFours || k % 4 == 0) && !(fine = bar_wait_warp(scaled + 8 * words_of.at, words_of.parity))) return;
+                const float *words = reinterpret_cast<const float *>(shared + (scales - base)) + words_of.at * ((kFours ? kFourBytes : kManyScaleBytes) / 4);
+                const float f = kFours ? words[4 * mine + k % 4] * words[4 * (kBlock + block) + k % 4] : words[mine] * words[kBlock + block];
+                if (!kFours || k % 4 == 3) words_of.next();
                 if (!(fine = bar_wait_warp(sums_full + 8 * sums.at, sums.parity))) return;
                 tmem_after_sync();
                 // 16 columns are on their way while the 16 before are multiplied and added
@@ -348,8 +365,8 @@ cudaError_t start_many(const Product &p, cudaStream_t s, int multiprocessors) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev >= 64 || !*(volatile bool *)&ready[dev])) {
-        e = cudaFuncSetAttribute(many_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kManySmem);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(many_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kManySmem);
+        for (const auto kernel : {many_kernel<false, false>, many_kernel<false, true>, many_kernel<true, false>, many_kernel<true, true>})
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kManySmem);
         if (e == cudaSuccess && dev < 64) *(volatile bool *)&ready[dev] = true;
     }
     if (e != cudaSuccess) return e;
@@ -372,7 +389,8 @@ cudaError_t start_many(const Product &p, cudaStream_t s, int multiprocessors) {
     if (!map_weight(&weight, a, kBlock) || !map_rows(&x, in_order, kBlock)) return cudaErrorInvalidValue;
     const int64_t units = most_tiles(a, kTileRows) * ((a.out_dim + kTileFeatures - 1) / kTileFeatures), pairs = multiprocessors / 2;
     const bool odd = reinterpret_cast<uintptr_t>(a.out) % 16 != 0 || a.out_stride % 8 != 0;
-    return launch_next(odd ? many_kernel<true> : many_kernel<false>, dim3((unsigned)(2 * std::min(2 * units, pairs))), kManyThreads, kManySmem, s, 2, q, weight, x);
+    const bool fours = !a.x_row_scales && p.groups % 4 == 0 && q.a.x_scales_stride % 4 == 0 && !misaligned(q.a.x_scales, 16) && !misaligned(a.weight_scales, 16);
+    return launch_next(odd ? (fours ? many_kernel<true, true> : many_kernel<true, false>) : fours ? many_kernel<false, true> : many_kernel<false, false>, dim3((unsigned)(2 * std::min(2 * units, pairs))), kManyThreads, kManySmem, s, 2, q, weight, x);
 }
 
 int take_many_status(int *code) {

@@ -78,16 +78,17 @@ def _ffn():
 
 # ----------------------------------------------------------------- products
 
-def matmul_fp8(x, x_scales, weight, weight_scales, *, out=None, dtype=None, stream=None):
+def matmul_fp8(x, x_scales, weight, weight_scales, *, rows=None, out=None, dtype=None, stream=None):
     """x times weight^T, both e4m3 with scales (see ar_matmul_fp8 in ar_ffn.h).
 
     x [rows, dim] (rows of any stride) and `x_scales` float32 [rows, ceil(dim / 128)] or [rows, 1], as add_norm_fp8 gives
     them with group 128 or 0; `weight` [out_dim, dim] and `weight_scales` float32 [ceil(out_dim / 128), ceil(dim / 128)], one
-    to a block of 128 x 128.  Returns [rows, out_dim] of `dtype` (float16 or bfloat16, the default), or `out`.
+    to a block of 128 x 128.  With `rows` (int32 [n]) row i of the result belongs to x[rows[i]], as for the logits of the
+    requests' last tokens.  Returns [rows, out_dim] of `dtype` (float16 or bfloat16, the default), or `out`.
     """
     if stream is not None:
-        return _under(stream, matmul_fp8, x, x_scales, weight, weight_scales, out=out, dtype=dtype)
-    return (ops._native or ops._binding()).matmul(x, x_scales, weight, weight_scales, None, None, out, dtype)
+        return _under(stream, matmul_fp8, x, x_scales, weight, weight_scales, rows=rows, out=out, dtype=dtype)
+    return (ops._native or ops._binding()).matmul(x, x_scales, weight, weight_scales, None, rows, out, dtype)
 
 
 def experts_matmul_fp8(x, x_scales, weight, weight_scales, offsets, *, rows=None, out=None, dtype=None, stream=None):

@@ -236,11 +236,27 @@ def test_many_experts_most_without_rows():
     _check_experts(out, x, xs, w, ws, offsets)
 
 
-@pytest.mark.parametrize("M,N,K,row_scale", [(5000, 2304, 256, False), (3, 1280, 20000, False), (40, 130, 9000, True), (2500, 333, 384, True), (1100, 4104, 272, False)])
+@pytest.mark.parametrize("M,N,K,row_scale", [(5000, 2304, 256, False), (3, 1280, 20000, False), (40, 130, 9000, True), (2500, 333, 384, True), (1100, 4104, 272, False), (2500, 333, 512, False),
+                                           (700, 512, 1536, False)])
 def test_products_of_many_tiles_and_long_rows(M, N, K, row_scale):
     """Several tiles to a block, rings of stages gone round many times, an odd output, channels shared by clusters."""
     x, xs, w, ws = _operands(M + N, M, N, K, row_scale=row_scale)
     H.check_product(_tda().matmul_fp8(x.cuda(), xs.cuda(), w.cuda(), ws.cuda()), x, xs, w, ws)
+
+
+@pytest.mark.parametrize("n", [1, 20, 100, 900])
+@pytest.mark.parametrize("K", [512, 130 * 16, 250])
+def test_products_of_picked_rows(n, K):
+    """`rows`: any number of times, in any order, numbers outside x among them."""
+    x, xs, w, ws = _operands(n + K, 33, 200, K)
+    rows = torch.randint(0, 33, (n,), generator=H.gen(n))
+    bad = [i for i in (0, 7, n - 1) if 1 < i < n]
+    for i in bad:
+        rows[i] = 33 + i
+    out = _tda().matmul_fp8(x.cuda(), xs.cuda(), w.cuda(), ws.cuda(), rows=rows.int().cuda())
+    keep = [i for i in range(n) if i not in bad]
+    H.check_product(out[keep], x.view(torch.uint8)[rows[keep]].view(F8), xs[rows[keep]], w, ws)
+    assert (out[bad] == 0).all()
 
 
 @pytest.mark.parametrize("E,each,N,K,row_scale", [(100, 3, 512, 256, True), (300, 1, 256, 144, False), (12, 40, 1024, 640, False), (7, 500, 520, 384, True)])
