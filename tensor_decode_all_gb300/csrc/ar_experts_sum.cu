@@ -31,61 +31,49 @@ union Vec {
     uint32_t u[4];
 };
 
-// V vectors to a thread, one token to a block (and a part of its channels, by blockIdx.y).
-template <typename T, int V>
+// A block to a token (and a part of its channels, by blockIdx.y).
+template <typename T>
 __global__ void __launch_bounds__(256) vector_sum_kernel(const ar_experts_sum_args a) {
     after_the_stream();
     const int64_t token = blockIdx.x;
-    const int vecs = a.dim / 8;
+    const int vecs = a.dim / 8, at = blockIdx.y * blockDim.x + threadIdx.x;
     const int *place = a.place + token * a.chosen;
     const float *weight = a.weights + token * a.chosen;
-    float sum[V][8] = {};
-    for (int j0 = 0; j0 < a.chosen; j0 += 8 / V) {
-        Vec x[8 / V][V];
-        float w[8 / V];
-        bool there[8 / V];
+    float sum[8] = {};
+    for (int j0 = 0; j0 < a.chosen; j0 += 8) {
+        Vec x[8];
+        float w[8];
+        bool there[8];
 #pragma unroll
-        for (int j = 0; j < 8 / V; ++j) {
+        for (int j = 0; j < 8; ++j) {
             const int p = j0 + j < a.chosen ? place[j0 + j] : -1;
             there[j] = p >= 0 && p < a.rows;
             w[j] = there[j] ? weight[j0 + j] : 0.0f;
             const uint4 *row = reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + p * a.x_stride);
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int at = (blockIdx.y * V + i) * blockDim.x + threadIdx.x;
-                if (there[j] && at < vecs) x[j][i].v = __ldcs(row + at);
-                else x[j][i].v = make_uint4(0, 0, 0, 0);
-            }
+            x[j].v = there[j] && at < vecs ? __ldcs(row + at) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int j = 0; j < 8 / V; ++j)
+        for (int j = 0; j < 8; ++j)
             if (there[j]) {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 v = pair_of<T>(x[j][i].u[e]);
-                        sum[i][2 * e] = fmaf(w[j], v.x, sum[i][2 * e]);
-                        sum[i][2 * e + 1] = fmaf(w[j], v.y, sum[i][2 * e + 1]);
-                    }
+                for (int e = 0; e < 4; ++e) {
+                    const float2 v = pair_of<T>(x[j].u[e]);
+                    sum[2 * e] = fmaf(w[j], v.x, sum[2 * e]);
+                    sum[2 * e + 1] = fmaf(w[j], v.y, sum[2 * e + 1]);
+                }
             }
     }
-    uint4 *out = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + token * a.out_stride);
+    Vec o;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int at = (blockIdx.y * V + i) * blockDim.x + threadIdx.x;
-        Vec o;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o.u[e] = to_pair<T>(make_float2(sum[i][2 * e], sum[i][2 * e + 1]));
-        if (at < vecs) out[at] = o.v;
-    }
+    for (int e = 0; e < 4; ++e) o.u[e] = to_pair<T>(make_float2(sum[2 * e], sum[2 * e + 1]));
+    if (at < vecs) reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + token * a.out_stride)[at] = o.v;
 }
 
 template <typename T>
 cudaError_t start(const ar_experts_sum_args &a, cudaStream_t s) {
     if (a.dim % 8 == 0 && !misaligned(a.x, 16) && a.x_stride % 8 == 0 && !misaligned(a.out, 16) && a.out_stride % 8 == 0) {
         const int vecs = a.dim / 8, threads = vecs < 256 ? (vecs + 31) / 32 * 32 : 256, parts = (vecs + threads - 1) / threads;
-        return launch_next(vector_sum_kernel<T, 1>, dim3((unsigned)a.tokens, (unsigned)parts), threads, 0, s, 0, a);
+        return launch_next(vector_sum_kernel<T>, dim3((unsigned)a.tokens, (unsigned)parts), threads, 0, s, 0, a);
     }
     return launch_next(any_sum_kernel<T>, dim3((unsigned)a.tokens, (unsigned)std::min(64, (a.dim + 255) / 256)), 256, 0, s, 0, a);
 }

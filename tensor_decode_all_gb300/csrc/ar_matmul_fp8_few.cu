@@ -44,8 +44,9 @@ template <int TOK> struct Few {
 
 // kPicked: row_of is given.
 template <int TOK, bool kPicked>
-__global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kernel(const __grid_constant__ Product p, const __grid_constant__ CUtensorMap weight,
-                                                             const __grid_constant__ CUtensorMap x, int cluster, int row_tiles) {
+__global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kernel(const __grid_constant__ Product p,
+                                                                                       const __grid_constant__ CUtensorMap weight,
+                                                                                       const __grid_constant__ CUtensorMap x, int cluster, int row_tiles) {
     using F = Few<TOK>;
     constexpr int S = F::Stages, B = F::Buffers, Q = F::Scales;
     extern __shared__ uint8_t raw[];

@@ -394,7 +394,8 @@ cudaError_t start_many(const Product &p, cudaStream_t s, int multiprocessors) {
     const int64_t units = most_tiles(a, kTileRows) * ((a.out_dim + kTileFeatures - 1) / kTileFeatures), pairs = multiprocessors / 2;
     const bool odd = reinterpret_cast<uintptr_t>(a.out) % 16 != 0 || a.out_stride % 8 != 0;
     const bool fours = !a.x_row_scales && p.groups % 4 == 0 && q.a.x_scales_stride % 4 == 0 && !misaligned(q.a.x_scales, 16) && !misaligned(a.weight_scales, 16);
-    return launch_next(odd ? (fours ? many_kernel<true, true> : many_kernel<true, false>) : fours ? many_kernel<false, true> : many_kernel<false, false>, dim3((unsigned)(2 * std::min(2 * units, pairs))), kManyThreads, kManySmem, s, 2, q, weight, x);
+    const auto kernel = odd ? (fours ? many_kernel<true, true> : many_kernel<true, false>) : fours ? many_kernel<false, true> : many_kernel<false, false>;
+    return launch_next(kernel, dim3((unsigned)(2 * std::min(2 * units, pairs))), kManyThreads, kManySmem, s, 2, q, weight, x);
 }
 
 int take_many_status(int *code) {

@@ -88,8 +88,6 @@ __device__ __forceinline__ void tensor_load(uint32_t to, const CUtensorMap *m, u
 __device__ __forceinline__ void copy_piece(uint32_t to, const void *from, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 // What ordinary accesses and word copies have written is there for matrix instructions after this.
 __device__ __forceinline__ void written_for_mma() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // One word, or a zero where it is not there.
@@ -198,11 +196,6 @@ __device__ __forceinline__ void pair_tensor_load(uint32_t to, const CUtensorMap 
 // ordered by its own fences (with a release at cluster scope it took 1100 cycles).
 __device__ __forceinline__ void cluster_bar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// The same after ordinary writes of this block that its own share of a pair's instructions reads.
-__device__ __forceinline__ void cluster_bar_arrive_written(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // The warpgroup's registers a thread from here on.
