@@ -1,4 +1,5 @@
 """The operators of include/ar_ffn.h against plain implementations in 64 bits (tests/ffn_helpers.py)."""
+import ctypes
 import math
 import os
 import subprocess
@@ -242,6 +243,41 @@ def test_products_of_many_tiles_and_long_rows(M, N, K, row_scale):
     """Several tiles to a block, rings of stages gone round many times, an odd output, channels shared by clusters."""
     x, xs, w, ws = _operands(M + N, M, N, K, row_scale=row_scale)
     H.check_product(_tda().matmul_fp8(x.cuda(), xs.cuda(), w.cuda(), ws.cuda()), x, xs, w, ws)
+
+
+def test_large_products_into_strided_rows():
+    """Many rows: outputs on 32 bytes, on 16, and on neither, inside wider rows."""
+    M, N, K = 3000, 2312, 2048
+    x, xs, w, ws = _operands(17, M, N, K)
+    dev = [t.cuda() for t in (x, xs, w, ws)]
+    want, mag = H.product(x, xs, w, ws)
+    limit = H.product_bound(want, mag, ws.shape[1], torch.float16).cuda()
+    want = want.cuda()
+    for at, more in ((0, 24), (8, 16), (3, 0), (16, 1)):
+        room = torch.full((M + 2, at + N + more), 7.0, dtype=torch.float16, device="cuda")
+        out = room[1:M + 1, at:at + N]
+        _tda().matmul_fp8(*dev, out=out)
+        assert ((out.double() - want).abs() <= limit).all()
+        assert (room[0] == 7).all() and (room[M + 1] == 7).all() and (room[:, :at] == 7).all() and (room[:, at + N:] == 7).all()
+
+
+def test_picked_rows_without_a_workspace():
+    """The C call with NULL for it: another kernel, the same product."""
+    tda = _tda()
+    from tensor_decode_all_gb300 import ffn
+    n, N, K = 900, 200, 512
+    x, xs, w, ws = _operands(3, 33, N, K)
+    rows = torch.randint(0, 33, (n,), generator=H.gen(3)).int()
+    dev = [t.cuda() for t in (x, xs, w, ws, rows)]
+    out = torch.empty(n, N, dtype=torch.bfloat16, device="cuda")
+    args = ffn.MatmulFp8Args(x=dev[0].data_ptr(), x_scales=dev[1].data_ptr(), weight=dev[2].data_ptr(), weight_scales=dev[3].data_ptr(), out=out.data_ptr(),
+                             offsets=None, row_of=dev[4].data_ptr(), workspace=None, x_stride=K, x_scales_stride=4, weight_stride=K, expert_stride=0,
+                             out_stride=N, rows=n, x_rows=33, dtype=2, out_dim=N, dim=K, experts=1, x_row_scales=0)
+    lib = ffn._ffn()
+    assert lib.ar_matmul_fp8_workspace(ctypes.addressof(args)) == n * (K + 16)
+    assert lib.ar_matmul_fp8(ctypes.addressof(args), torch.cuda.current_stream().cuda_stream) == 0
+    H.check_product(out, x.view(torch.uint8)[rows.long()].view(F8), xs[rows.long()], w, ws)
+    H.check_product(tda.matmul_fp8(*dev[:4], rows=dev[4]), x.view(torch.uint8)[rows.long()].view(F8), xs[rows.long()], w, ws)
 
 
 @pytest.mark.parametrize("n", [1, 20, 100, 900])
