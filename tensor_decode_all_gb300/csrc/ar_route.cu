@@ -13,8 +13,8 @@
 // blocks, each with a run of the pairs, each warp of it with a part of that run: count by warp and expert, add up over warps
 // and blocks (through the cluster's shared memory), then go over the pairs again.
 //
-// 8191 tokens to 8 of 256 experts take 19 us in GB300 graph replays (the choice 13 us by itself, two thirds of the cycles issue an
-// instruction, some 600 to a token; the places 10), where the sort took 22 besides the choice; 5 tokens to 4 of 32, in one block, 3.0 us.
+// 8191 tokens to 8 of 256 experts take 18 to 19 us in GB300 graph replays (the choice 13 us by itself, two thirds of the cycles issue an
+// instruction, some 800 to a token; the places 10), where the sort took 22 besides the choice; 5 tokens to 4 of 32, in one block, 2.5 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -171,12 +171,15 @@ __device__ __forceinline__ int before_expert(Pairs &s, int own, int carried, int
     }
     if (lane == 31) s.scan[warp] = run;
     __syncthreads();
-    int past = carried;
-    all = carried;
-    for (int w = 0; w < kRouteThreads / 32; ++w) {
-        if (w < warp) past += s.scan[w];
-        all += s.scan[w];
+    static_assert(kRouteThreads == 32 * 32, "a lane to each warp");
+    int warps = s.scan[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int x = __shfl_up_sync(~0u, warps, d);
+        if (lane >= d) warps += x;
     }
+    const int earlier = __shfl_sync(~0u, warps, max(warp - 1, 0)), past = carried + (warp > 0 ? earlier : 0);
+    all = carried + __shfl_sync(~0u, warps, 31);
     __syncthreads();
     return past + run - own;
 }
