@@ -110,8 +110,8 @@ AR_API size_t ar_route_experts_workspace(const ar_route_experts_args *args);
 /*
  * ar_silu_mul_fp8 -- the gated activation, rounded to 8 bits.  Row r of x holds dim gates and dim factors after them:
  *   y_c = g_c / (1 + exp(-g_c)) * x[r][dim + c],   g_c = x[r][c]   (binary32)
- * per group of `group` channels (0: the row; the last group may be short): scale = max|y| / 448 (1 if that is 0),
- * out = e4m3(y / scale).  (A NaN is the largest: it is its group's scale, and out is NaN.)
+ * per group of `group` channels (0: the row; the last group may be short): scale = max|y| / 448 (1 where that is 0, as binary32
+ * makes it for max|y| up to 224 * 2^-149), out = e4m3(y / scale).  (A NaN is the largest: it is its group's scale, and out is NaN.)
  * out [rows][dim] and scales [rows][ceil(dim / group)] are contiguous.
  * Errors: AR_EINVAL, AR_ETOOBIG (rows > 2^30, dim > 2^20), AR_ECUDA.
  */

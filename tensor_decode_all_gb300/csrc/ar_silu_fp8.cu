@@ -50,11 +50,16 @@ __device__ __forceinline__ float2 quick_silu_mul(float2 g, float2 u) {
     return floats_of(mul2(mul2(gates, pair_of_floats(r.x, r.y)), pair_of_floats(u.x, u.y)));
 }
 
-// A group's scale, and what its values are multiplied by, from its largest value.
+// A group's scale from its largest value.  (A top up to 224 * 2^-149 rounds to 0 as well: what it leaves is 0 by the scale 1.)
+__device__ __forceinline__ float divided_scale(float top) {
+    const float scale = __fdiv_rn(top, 448.0f);
+    return scale == 0 ? 1.0f : scale;
+}
+
+// The same, and what its values are multiplied by (0: they are divided).
 __device__ __forceinline__ float2 scale_of(float top) {
     if (top > 0x1p-60f && top < 0x1p100f) return make_float2(top * (1.0f / 448.0f), __fdividef(448.0f, top));   // within 2 units of the last place of 1 / scale
-    const float scale = top == 0 ? 1.0f : __fdiv_rn(top, 448.0f);
-    return make_float2(scale, 0);
+    return make_float2(divided_scale(top), 0);
 }
 
 union Vec {
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(128) any_group_kernel(const ar_silu_mul_fp8_ar
         if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
         __syncthreads();
         for (int i = 0; i < 4; ++i) top = top_of(top, tops[i]);
-        const float scale = top == 0 ? 1.0f : __fdiv_rn(top, 448.0f);
+        const float scale = divided_scale(top);
         if (threadIdx.x == 0) a.scales[at] = scale;
         uint8_t *out = static_cast<uint8_t *>(a.out) + row * a.dim;
         for (int i = begin + threadIdx.x; i < end; i += 128)

@@ -498,6 +498,42 @@ def test_silu_of_special_rows(group):
     assert (f[4] * s[4].cpu().repeat_interleave(d // s.shape[1])).abs().max() < 1e-40
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,group,at", [(256, 128, 0), (256, 0, 0), (8200, 0, 0), (256, 128, 1), (256, 0, 1), (100, 0, 0)])
+def test_silu_of_groups_near_zero(dtype, d, group, at):
+    """Groups whose largest value is a few steps of the subnormal numbers, zeros among them, in each kernel.
+
+    A scale that rounds to 0 is 1.  Another is off by half a step, 2^-150, so that 448 of it are short of the largest value by up to 224 steps,
+    at which out is cut off; out is rounded by 2^-4 of itself, or by 2^-10 where it is small, and y by two steps.
+    """
+    steps = [1, 2, 5, 40, 100, 223, 224, 225, 230, 300, 448, 640, 672, 1000, 2000]
+    wide = torch.zeros(len(steps), 2 * d + at + 7, dtype=H.DT[dtype])
+    x = wide[:, at:at + 2 * d]
+    for i, n in enumerate(steps):
+        for c, part in ((3, 1.0), (90, -0.5)):
+            # y: bfloat16 n 2^-149 exactly, float16 22 2^-149 times whole numbers
+            x[i, c], x[i, d + c] = (2.0 ** -100, part * n * 2.0 ** -48) if dtype == "bf16" else (-88.0, -part * max(1, round(n / 22)) * 2.0 ** -24)
+    if group:
+        x[:, group + 5], x[:, d + group + 5] = 2.0, 3.0
+    view = wide.cuda()[:, at:at + 2 * d]
+    out, s = _tda().silu_mul_fp8(view, group=group)
+    f, s = out.double().cpu(), s.double().cpu()
+    y = H.silu_mul(x)
+    first = slice(0, group or d)
+    top = y[:, first].abs().amax(1)
+    assert f.isfinite().all() and (f[y == 0] == 0).all() and s.isfinite().all() and (s > 0).all()
+    step = 2.0 ** -149
+    sure = top < 223 * step                    # (y itself may be off by a step)
+    assert (s[sure, 0] == 1).all() and sure.sum() > 3
+    big = top > 226 * step
+    assert ((s[big, 0] - top[big] / 448).abs() <= step * (0.5 + 1 / 448)).all() and big.sum() > 3
+    off = (f * s[:, :1] - y)[:, first].abs()
+    back = torch.where(s[:, :1] < 1, s[:, :1], 0.0)
+    assert (off <= y[:, first].abs() * 2.0 ** -4 + back * 2.0 ** -10 + (224 + 2) * step).all()
+    if group:
+        assert (f[:, group + 5] == 448).all()
+
+
 def test_empty_silu():
     x = torch.randn(4, 256, device="cuda").half()
     out, s = _tda().silu_mul_fp8(x[:0])
