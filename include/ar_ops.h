@@ -182,7 +182,8 @@ AR_API int ar_kv4_status(const void *workspace);
  * ar_add_norm_fp8 -- residual, RMS norm and rounding to 8 bits in one pass.
  * Per row: h = x + residual (binary32; residual NULL: h = x), y = h / sqrt(mean(h^2) +
  * eps) * weight; per group of `group` channels (0: the row; the last group may
- * be short): scale = max|y| / 448 (1 if that is 0), out = e4m3(y / scale).
+ * be short): scale = max|y| / 448 (1 where that is 0, as binary32 makes it for max|y| up to 224 * 2^-149),
+ * out = e4m3(y / scale).
  * (A NaN is the largest: it is its group's scale, and out is NaN.)
  * A row whose sum of squares passes binary32 has y = 0 but where h is not finite; there y is NaN, and so are its
  * group's scale and out.

@@ -49,6 +49,17 @@ __device__ __forceinline__ float top_of(float a, float b, float c) {
     return r;
 }
 
+// A group's scale from its largest |y|.  (Up to 224 * 2^-149 it rounds to 0 as well: what it leaves is 0 by the scale 1.)
+__device__ __forceinline__ float divided_scale(float top) {
+    const float scale = __fdiv_rn(top, 448.0f);
+    return scale == 0 ? 1.0f : scale;
+}
+
+// y / scale, by the scale's reciprocal where that is finite.
+__device__ __forceinline__ float quotient(float y, float scale, float reciprocal) {
+    return scale < 0x1p-100f ? __fdiv_rn(y, scale) : y * reciprocal;
+}
+
 // Vectors of 8 channels, V to a thread: vector i * blockDim.x + threadIdx.x.  Lanes: threads that share a
 // group (a power of two up to 32; 0: the row is one group).
 template <typename T, int V>
@@ -139,9 +150,11 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) norm_rows_kernel(const ar
         const float m = lanes ? top[i] : most;
         float scale = m * inv * (1.0f / 448.0f), q = __fdividef(448.0f, m);       // h * q: within 2 units of the last place of y / scale
         if (!(m > 0x1p-60f && m < 0x1p100f && inv > 0)) {
-            // zeros, the ends of the range, infinities; rows whose sum of squares is infinite: y = 0
-            scale = m * inv == 0 ? 1.0f : __fdiv_rn(m * inv, 448.0f);
-            q = __fdiv_rn(inv, scale);
+            // zeros, the ends of the range (inv / scale may be past it), infinities; rows whose sum of squares is infinite: y = 0
+            scale = divided_scale(m * inv);
+            q = 1;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[i][e] = __fdiv_rn(h[i][e] * inv, scale);
         }
         if (!(inv == inv)) scale = q = inv;
         if (at < vecs) {
@@ -189,9 +202,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const ar_add_norm_fp
         if (lane == 0) buf[warp] = top;
         __syncthreads();
         for (int i = 0; i < kNormThreads / 32; ++i) top = top_of(top, buf[i]);
-        const float scale = top == 0 ? 1.0f : __fdiv_rn(top, 448.0f), q = __fdiv_rn(1.0f, scale);
+        const float scale = divided_scale(top), q = __fdiv_rn(1.0f, scale);
         if (threadIdx.x == 0) a.scales[row] = scale;
-        for (int i = threadIdx.x; i < a.dim; i += kNormThreads) out[i] = __nv_cvt_float_to_fp8(h[i] * q, __NV_SATFINITE, __NV_E4M3);
+        for (int i = threadIdx.x; i < a.dim; i += kNormThreads) out[i] = __nv_cvt_float_to_fp8(quotient(h[i], scale, q), __NV_SATFINITE, __NV_E4M3);
     } else {
         for (int g = warp; g < groups; g += kNormThreads / 32) {
             const int end = min(a.dim, (g + 1) * group);
@@ -202,9 +215,9 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const ar_add_norm_fp
             }
 #pragma unroll
             for (int d = 16; d; d /= 2) top = top_of(top, __shfl_xor_sync(~0u, top, d));
-            const float scale = top == 0 ? 1.0f : __fdiv_rn(top, 448.0f), q = __fdiv_rn(1.0f, scale);
+            const float scale = divided_scale(top), q = __fdiv_rn(1.0f, scale);
             if (lane == 0) a.scales[row * groups + g] = scale;
-            for (int i = g * group + lane; i < end; i += 32) out[i] = __nv_cvt_float_to_fp8(h[i] * q, __NV_SATFINITE, __NV_E4M3);
+            for (int i = g * group + lane; i < end; i += 32) out[i] = __nv_cvt_float_to_fp8(quotient(h[i], scale, q), __NV_SATFINITE, __NV_E4M3);
         }
     }
 }

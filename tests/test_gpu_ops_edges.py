@@ -358,6 +358,40 @@ def test_norm_with_a_nan_in_the_weight(d, group, shift):
     assert torch.equal(scales.cpu().isnan(), bad.view(1, -1, n)[..., 0].expand(3, -1))
 
 
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("group", [0, 128])
+def test_norm_of_groups_near_zero(group, shift):
+    """Groups whose largest |y| is a few steps of the subnormal numbers, or whose scale has no finite reciprocal, zeros among them.
+
+    A scale that rounds to 0 is 1.  Another is off by half a step, 2^-150 (and 2^-20 for the root and products), so that 448 of it are short of the
+    largest |y| by up to 224 steps, at which out is cut off; out is rounded by 2^-4 of itself, or by 2^-10 where it is small, and y by two steps.
+    """
+    d, step = 256, 2.0 ** -149
+    steps = [1, 2, 5, 40, 100, 222, 224, 228, 230, 300, 448, 640, 672, 1000, 2000, 2.0 ** 17, 2.0 ** 22, 2.0 ** 26, 2.0 ** 31, 2.0 ** 47]
+    x = torch.zeros(len(steps), d, dtype=torch.bfloat16)
+    w = torch.ones(d, dtype=torch.bfloat16)
+    x[:, 200] = 2.0 ** 57                      # the root of the mean is 2^53
+    for i, n in enumerate(steps):
+        x[i, 3], x[i, 90], x[i, 91] = n * 2.0 ** -96, -n * 2.0 ** -97, n * 2.0 ** -107
+    if not group:
+        w[200] = 0
+    out, scales, _ = _tda().add_norm_fp8(_shifted(x, shift), w.cuda(), eps=0.0, group=group)
+    f, s = out.double().cpu(), scales.double().cpu()[:, :1]
+    xd = x.double()
+    y = xd / (xd * xd).mean(1, keepdim=True).sqrt() * w.double()
+    first = slice(0, group or d)
+    top = y[:, first].abs().amax(1)
+    assert f.isfinite().all() and (f[y == 0] == 0).all() and scales.isfinite().all() and (scales > 0).all()
+    sure, big = top < 223 * step, top > 227 * step
+    assert sure.sum() > 3 and (s[sure] == 1).all()
+    assert ((s[big, 0] - top[big] / 448).abs() <= step * (0.5 + 1 / 448) + top[big] / 448 * 2.0 ** -20).all()
+    off, mag = (f * s - y)[:, first].abs(), y[:, first].abs()
+    back = torch.where(s < 1, s, 0.0)
+    assert (off <= mag * (2.0 ** -4 + 2.0 ** -19) + back * 2.0 ** -10 + (224 + 2) * step).all()
+    if group:
+        assert (f[:, 200] == 448).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_norm_of_rows_without_channels(dtype):
     """Their scale is 1, as of any row whose largest |y| is 0; it is written."""
