@@ -112,6 +112,8 @@ AR_API size_t ar_route_experts_workspace(const ar_route_experts_args *args);
  *   y_c = g_c / (1 + exp(-g_c)) * x[r][dim + c],   g_c = x[r][c]   (binary32)
  * per group of `group` channels (0: the row; the last group may be short): scale = max|y| / 448 (1 where that is 0, as binary32
  * makes it for max|y| up to 224 * 2^-149), out = e4m3(y / scale).  (A NaN is the largest: it is its group's scale, and out is NaN.)
+ * y is off by less than 2^-19.9 of itself (exp and the quotient by the hardware's approximations), scale by 2^-19.7: where y / scale lies
+ * that near to the middle of two e4m3 numbers, out may be either.  A row's output does not depend on where the row lies.
  * out [rows][dim] and scales [rows][ceil(dim / group)] are contiguous.
  * Errors: AR_EINVAL, AR_ETOOBIG (rows > 2^30, dim > 2^20), AR_ECUDA.
  */

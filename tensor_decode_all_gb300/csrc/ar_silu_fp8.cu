@@ -33,6 +33,7 @@ __device__ __forceinline__ float top_of(float a, float b, float c) {
     return r;
 }
 
+// For gates below -8.
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdiv_rn(g, 1.0f + expf(-g)) * u; }
 
 // Two at a time (the adds and products are instructions of two), for gates from -8 on, by the hardware's power of two and reciprocal.  The
@@ -48,6 +49,12 @@ __device__ __forceinline__ float2 quick_silu_mul(float2 g, float2 u) {
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r.x));
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r.y));
     return floats_of(mul2(mul2(gates, pair_of_floats(r.x, r.y)), pair_of_floats(u.x, u.y)));
+}
+
+// One value, the same bits as of two.  (Which form a value takes is its own gate's matter, so that a row has the same output wherever it lies.)
+template <typename T> __device__ __forceinline__ float one_silu_mul(T gate, T factor) {
+    const float g = Elem<T>::to_float(gate), u = Elem<T>::to_float(factor);
+    return g < -8.0f ? silu_mul(g, u) : quick_silu_mul(make_float2(g, g), make_float2(u, u)).x;
 }
 
 // A group's scale from its largest value.  (A top up to 224 * 2^-149 rounds to 0 as well: what it leaves is 0 by the scale 1.)
@@ -81,8 +88,8 @@ template <typename T> __device__ __forceinline__ float values(const Vec &g, cons
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float2 a = pair_of<T>(g.u[e]), b = pair_of<T>(u.u[e]);
-            y[2 * e] = silu_mul(a.x, b.x);
-            y[2 * e + 1] = silu_mul(a.y, b.y);
+            if (a.x < -8.0f) y[2 * e] = silu_mul(a.x, b.x);
+            if (a.y < -8.0f) y[2 * e + 1] = silu_mul(a.y, b.y);
         }
     }
 #pragma unroll
@@ -201,17 +208,19 @@ __global__ void __launch_bounds__(128) any_group_kernel(const ar_silu_mul_fp8_ar
         const int begin = (int)(at - row * groups) * group, end = min(a.dim, begin + group);
         const T *x = static_cast<const T *>(a.x) + row * a.x_stride;
         float top = 0;
-        for (int i = begin + threadIdx.x; i < end; i += 128) top = top_of(top, silu_mul(Elem<T>::to_float(x[i]), Elem<T>::to_float(x[a.dim + i])));
+        for (int i = begin + threadIdx.x; i < end; i += 128) top = top_of(top, one_silu_mul(x[i], x[a.dim + i]));
 #pragma unroll
         for (int d = 16; d; d /= 2) top = top_of(top, __shfl_xor_sync(~0u, top, d));
         if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
         __syncthreads();
         for (int i = 0; i < 4; ++i) top = top_of(top, tops[i]);
-        const float scale = divided_scale(top);
-        if (threadIdx.x == 0) a.scales[at] = scale;
+        const float2 s = scale_of(top);
+        if (threadIdx.x == 0) a.scales[at] = s.x;
         uint8_t *out = static_cast<uint8_t *>(a.out) + row * a.dim;
-        for (int i = begin + threadIdx.x; i < end; i += 128)
-            out[i] = __nv_cvt_float_to_fp8(__fdiv_rn(silu_mul(Elem<T>::to_float(x[i]), Elem<T>::to_float(x[a.dim + i])), scale), __NV_SATFINITE, __NV_E4M3);
+        for (int i = begin + threadIdx.x; i < end; i += 128) {
+            const float y = one_silu_mul(x[i], x[a.dim + i]);
+            out[i] = __nv_cvt_float_to_fp8(s.y != 0 ? y * s.y : __fdiv_rn(y, s.x), __NV_SATFINITE, __NV_E4M3);
+        }
         __syncthreads();
     }
 }

@@ -534,6 +534,25 @@ def test_silu_of_groups_near_zero(dtype, d, group, at):
         assert (f[:, group + 5] == 448).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d,group", [(512, 128), (512, 0), (264, 32), (1024, 256), (9000, 0)])
+def test_silu_is_the_same_wherever_a_row_lies(dtype, d, group):
+    """Rows on 16 bytes and off them take other kernels: the same bits, gates below -8 and special values among them."""
+    x = torch.randn(40, 2 * d, generator=H.gen(d)).to(H.DT[dtype])
+    x[1, :d] *= 6
+    x[2, :d:9] = -20.0
+    x[3, 5], x[4, d + 5], x[5, 7], x[6, 7] = math.nan, math.nan, math.inf, -math.inf
+    x[7, :d], x[8, d:], x[9] = -80.0, x[8, d:] * 1e-3, 0
+    got = []
+    for at in (0, 1, 3):
+        wide = torch.zeros(40, 2 * d + 8, dtype=H.DT[dtype], device="cuda")
+        wide[:, at:at + 2 * d] = x.cuda()
+        got.append(_tda().silu_mul_fp8(wide[:, at:at + 2 * d], group=group))
+    for out, s in got[1:]:
+        assert torch.equal(s.view(torch.int32), got[0][1].view(torch.int32)) and torch.equal(out.view(torch.uint8), got[0][0].view(torch.uint8))
+    H.check_silu(got[0][0][10:], got[0][1][10:], x[10:], group)
+
+
 def test_empty_silu():
     x = torch.randn(4, 256, device="cuda").half()
     out, s = _tda().silu_mul_fp8(x[:0])
