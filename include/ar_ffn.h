@@ -27,7 +27,7 @@ extern "C" {
  * ar_matmul_fp8 -- product of e4m3 rows with e4m3 weights, a scale to each block of 128.
  * With x's row m and the weight's row n cut into groups g of 128 channels (the last may be short):
  *   out[m][n] = sum_g xs[m][g] * ws[n / 128][g] * sum_(k in g) x[m][k] * w[n][k]
- * Products are exact, sums binary32, scales multiply each group's sum in binary32, out is rounded once.
+ * Products are exact, sums binary32; the product of the two scales is rounded to binary32 and multiplies each group's sum, out is rounded once.
  * With x_row_scales, x has one scale a row (what ar_add_norm_fp8 gives with group 0); else one to 128
  * channels (its group 128).
  * offsets NULL: one weight for all rows; row m of out belongs to row m of x, and x_rows = rows.
@@ -35,12 +35,13 @@ extern "C" {
  *   before offsets[0] and from offsets[experts] on are not written.
  * row_of [rows] (with or without offsets): row i of out belongs to row row_of[i] of x, any number of times each; a
  *   number outside x gives a row of zeros.  NULL: to row i.
- * Offsets outside 0 .. rows are taken as the nearest of these; where they decrease, an expert has no rows or
- * two share some, which are then undefined (the call stays inside the buffers).
+ * Offsets outside 0 .. rows are taken as the nearest of these.  Where they decrease, the call stays inside the buffers, and what
+ * it writes to out is undefined.
  * Results do not depend on the order in which blocks run; whether the groups are summed one after another or in
  * up to 16 parts, added in order, goes by the call's sizes.
  * Weights, x and out whose rows all begin on 16 bytes take the fast kernels (x_stride, weight_stride and expert_stride
- * multiples of 16 bytes; out is free), others a slower one.
+ * multiples of 16 bytes; out is free), others a slower one.  Which of the fast ones goes by the sizes alone, the host cannot see the offsets: few
+ * rows an expert on average take the one that reads an expert's weight for every 16 to 128 rows, which is slow where one expert has nearly all.
  * out must not overlap an input.
  * Logical ranks on one GPU: a product of many rows needs whole multiprocessors.  An exchange that is launched rank by rank
  * (ar_allreduce) and has a block on each of them, waiting for a rank whose product has not begun, keeps it from beginning

@@ -212,6 +212,86 @@ def test_offsets_that_are_wrong_stay_inside():
     _tda().matmul_fp8_check()
 
 
+@pytest.mark.parametrize("n", [50, 600])
+@pytest.mark.parametrize("K", [1024, 250])
+@pytest.mark.parametrize("gather", [False, True])
+def test_wrong_offsets_in_every_kernel(n, K, gather):
+    """Few rows, many, and rows off 16 bytes, in place and picked: the call stays inside its buffers, and offsets that are good where they are
+    brought inside 0 .. rows give the right rows."""
+    N, E = 600, 4
+    x, xs, w, ws = _operands(n + K, 40 if gather else n, N, K, E)
+    rows = torch.randint(0, 40, (n,), generator=H.gen(n)).tolist() if gather else None
+    dev = [t.cuda() for t in (x, xs, w, ws)]
+    big = 2 ** 31 - 1
+    room = torch.empty(n + 20, N, dtype=torch.bfloat16, device="cuda")
+    for offsets in ([-9, n // 5, n // 2, n - 7, big], [-big, -1, 0, n + 1, big], [0, big, 20, 30, n], [0, n, 0, n, 0], [0, n - 10, 10, 30, n], [n, 40, 30, 20, 10],
+                    [n // 2, n, 0, 5, n // 3], [-5] * 5, [n + 99] * 5):
+        room.fill_(5.0)
+        out = _tda().experts_matmul_fp8(*dev, _i32(offsets), rows=_i32(rows) if gather else None, out=room[10:n + 10])
+        torch.cuda.synchronize()
+        assert (room[:10] == 5).all() and (room[n + 10:] == 5).all()
+        inside = [min(max(o, 0), n) for o in offsets]
+        if inside == sorted(inside):
+            _check_experts(out, x, xs, w, ws, inside, rows)
+            assert (out[:inside[0]] == 5).all() and (out[inside[-1]:] == 5).all()
+    _tda().matmul_fp8_check()
+
+
+@pytest.mark.parametrize("K,row_scale", [(2560, False), (2672, False), (2560, True)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_experts_with_an_odd_output_and_many_rows(K, row_scale, gather):
+    """Results that leave by twos of bytes from whole and short tiles, experts' ends among them."""
+    N, counts = 2301, [300, 100, 512, 0, 1, 700, 129, 306]
+    offsets = [0]
+    for c in counts:
+        offsets.append(offsets[-1] + c)
+    R = offsets[-1]
+    T = R // 3 if gather else R
+    x, xs, w, ws = _operands(K, T, N, K, len(counts), row_scale)
+    rows = torch.randint(0, T, (R,), generator=H.gen(K)).tolist() if gather else None
+    out = _tda().experts_matmul_fp8(x.cuda(), xs.cuda(), w.cuda(), ws.cuda(), _i32(offsets), rows=_i32(rows) if gather else None, dtype=torch.float16)
+    _check_experts(out, x, xs, w, ws, offsets, rows)
+
+
+@pytest.mark.parametrize("counts", [[3], [0, 5, 70, 0, 1], [200, 64, 65, 0, 300]])
+@pytest.mark.parametrize("N,K", [(130, 129), (65, 1001), (64, 7)])
+@pytest.mark.parametrize("gather", [False, True])
+def test_experts_of_odd_rows(counts, N, K, gather):
+    """Rows that do not begin on 16 bytes."""
+    offsets = [0]
+    for c in counts:
+        offsets.append(offsets[-1] + c)
+    R = offsets[-1]
+    T = max(1, R // 2) if gather else R
+    x, xs, w, ws = _operands(R + K, T, N, K, len(counts))
+    rows = torch.randint(0, T, (R,), generator=H.gen(R)).tolist() if gather else None
+    out = _tda().experts_matmul_fp8(x.cuda(), xs.cuda(), w.cuda(), ws.cuda(), _i32(offsets), rows=_i32(rows) if gather else None)
+    _check_experts(out, x, xs, w, ws, offsets, rows)
+
+
+@pytest.mark.parametrize("layout", ["wider", "no whole rows between", "odd", "side by side", "one for all"])
+@pytest.mark.parametrize("R", [20, 1500])
+@pytest.mark.parametrize("gather", [False, True])
+def test_experts_of_strided_weights(layout, R, gather):
+    """Weights inside wider ones; whose experts lie 16 bytes times any number apart, or an odd number; with the experts' rows taking turns; all
+    experts the same one.  What lies between them is NaN."""
+    E, N, K = 5, 600, 1024
+    T = 40 if gather else R
+    x, xs, w, ws = _operands(R, T, N, K, E)
+    if layout == "one for all":
+        w = w.view(torch.uint8)[:1].expand(E, -1, -1).view(F8)
+    room = torch.full((E * (N + 16) * (K + 32) + 64,), 0x7f, dtype=torch.uint8, device="cuda").view(F8)
+    strides = {"wider": ((N + 16) * (K + 32), K + 32), "no whole rows between": (N * (K + 32) + 48, K + 32), "odd": (N * (K + 32) + 49, K + 32),
+               "side by side": (K, E * K), "one for all": (0, K)}[layout]
+    wd = room[16:].as_strided((E, N, K), (*strides, 1))
+    for e in range(1 if layout == "one for all" else E):
+        wd[e].view(torch.uint8).copy_(w[e].view(torch.uint8))
+    offsets = [0, R // 7, R // 2, R // 2, R - 3, R]
+    rows = torch.randint(0, T, (R,), generator=H.gen(R)).tolist() if gather else None
+    out = _tda().experts_matmul_fp8(x.cuda(), xs.cuda(), wd, ws.cuda(), _i32(offsets), rows=_i32(rows) if gather else None)
+    _check_experts(out, x, xs, w, ws, offsets, rows)
+
+
 def test_weights_past_32_bits():
     """Over 4 GiB of weights: the last expert's product, whose parts may be added otherwise than a single weight's."""
     tda = _tda()
