@@ -158,8 +158,16 @@ Encode encoder() {
 bool encode(CUtensorMap *m, const void *at, int rank, const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box) {
     static const cuuint32_t ones[3] = {1, 1, 1};
     const Encode f = encoder();
-    return f && f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(at), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    auto call = [&] {
+        return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(at), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    if (!f) return false;
+    CUresult r = call();
+    // (a host thread that has made no call yet that needs a context has none: unlike the runtime's, the driver's function does not make it current)
+    int dev = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = call();
+    return r == CUDA_SUCCESS;
 }
 
 // Whether the copy engine can take these rows: on 16 bytes, one after another.

@@ -4,6 +4,7 @@ import math
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
@@ -290,6 +291,75 @@ def test_experts_of_strided_weights(layout, R, gather):
     rows = torch.randint(0, T, (R,), generator=H.gen(R)).tolist() if gather else None
     out = _tda().experts_matmul_fp8(x.cuda(), xs.cuda(), wd, ws.cuda(), _i32(offsets), rows=_i32(rows) if gather else None)
     _check_experts(out, x, xs, w, ws, offsets, rows)
+
+
+def test_host_threads_at_once():
+    """Threads that call the library at the same time (ctypes lets go of the interpreter's lock), each on its own stream, the first calls of their
+    sizes among them."""
+    from tensor_decode_all_gb300 import ffn
+    lib, jobs = ffn._ffn(), []
+    for seed, (M, N, K) in enumerate(((9, 384, 4096), (50, 640, 2048), (128, 768, 1024), (1600, 768, 1024), (3, 130, 129), (20, 1152, 2048))):
+        ops = _operands(seed, M, N, K)
+        dev = [t.cuda() for t in ops]
+        jobs.append((ops, dev, [torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(12)], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    gate, codes = threading.Barrier(len(jobs)), []
+
+    def work(dev, outs, stream):
+        gate.wait()
+        for out in outs:
+            x, xs, w, ws = dev
+            args = ffn.MatmulFp8Args(x=x.data_ptr(), x_scales=xs.data_ptr(), weight=w.data_ptr(), weight_scales=ws.data_ptr(), out=out.data_ptr(), x_stride=x.stride(0),
+                                     x_scales_stride=xs.stride(0), weight_stride=w.stride(0), out_stride=out.stride(0), rows=len(x), x_rows=len(x), dtype=2,
+                                     out_dim=w.shape[0], dim=x.shape[1], experts=1)
+            codes.append(lib.ar_matmul_fp8(ctypes.addressof(args), stream.cuda_stream))
+
+    threads = [threading.Thread(target=work, args=j[1:]) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [0] * (12 * len(jobs))
+    for ops, _, outs, _ in jobs:
+        H.check_product(outs[0], *ops)
+        assert all(torch.equal(o, outs[0]) for o in outs[1:])
+    _tda().matmul_fp8_check()
+
+
+def test_the_first_call_of_a_host_thread():
+    """A thread that has made no CUDA call before, as a server's worker: each operator, also under a capture."""
+    tda = _tda()
+    small, large = ([t.cuda() for t in _operands(seed, M, 600, 1024)] for seed, M in ((1, 9), (2, 2000)))
+    x, logits, place = torch.randn(9, 256, device="cuda").half(), torch.randn(9, 8, device="cuda"), torch.zeros(9, 2, dtype=torch.int32, device="cuda")
+    weights = torch.ones(9, 2, device="cuda")
+    calls = [lambda: tda.matmul_fp8(*small), lambda: tda.matmul_fp8(*large), lambda: tda.route_experts(logits, 2)[1], lambda: tda.silu_mul_fp8(x)[1],
+             lambda: tda.experts_sum(x, weights, place)]
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+
+    def captured(f):
+        graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=s, capture_error_mode="thread_local"):
+            out = f()
+        graph.replay()
+        return out
+
+    for f, w in zip(calls, want):
+        for run in (f, lambda: captured(f)):
+            got = []
+
+            def work():
+                try:
+                    got.append(run())
+                except Exception as e:          # (an exception does not leave the thread)
+                    got.append(e)
+            t = threading.Thread(target=work)
+            t.start()
+            t.join()
+            torch.cuda.synchronize()
+            assert torch.is_tensor(got[0]), got[0]
+            assert torch.equal(got[0], w)
 
 
 def test_weights_past_32_bits():
