@@ -160,8 +160,8 @@ __device__ __forceinline__ int pairs_of(const Pairs &s, int expert, int words) {
     return n;
 }
 
-// Running sums over the experts of `own` (one expert to a thread): what earlier experts have.
-__device__ __forceinline__ int before_expert(Pairs &s, int own, int carried, int &all) {
+// Running sums over the experts of `own` (one expert to a thread): what earlier experts have, and all.
+__device__ __forceinline__ int before_expert(Pairs &s, int own, int &all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int run = own;
 #pragma unroll
@@ -171,17 +171,16 @@ __device__ __forceinline__ int before_expert(Pairs &s, int own, int carried, int
     }
     if (lane == 31) s.scan[warp] = run;
     __syncthreads();
-    static_assert(kRouteThreads == 32 * 32, "a lane to each warp");
+    static_assert(kRouteThreads == 32 * 32 && kMostExperts <= kRouteThreads, "a lane to each warp, a thread to each expert");
     int warps = s.scan[lane];
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
         const int x = __shfl_up_sync(~0u, warps, d);
         if (lane >= d) warps += x;
     }
-    const int earlier = __shfl_sync(~0u, warps, max(warp - 1, 0)), past = carried + (warp > 0 ? earlier : 0);
-    all = carried + __shfl_sync(~0u, warps, 31);
-    __syncthreads();
-    return past + run - own;
+    const int earlier = __shfl_sync(~0u, warps, max(warp - 1, 0));
+    all = __shfl_sync(~0u, warps, 31);
+    return (warp > 0 ? earlier : 0) + run - own;
 }
 
 // Places and rows of the block's pairs, first .. first + n - 1 of the call.
@@ -227,17 +226,14 @@ __global__ void __launch_bounds__(kRouteThreads) choose_kernel(const ar_route_ex
     if (blocks == 0) return;
     __syncthreads();
     if (blocks > 1) {
-        for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) a.workspace[(int64_t)blockIdx.x * a.experts + e] = pairs_of(s, e, words);
+        if (threadIdx.x < a.experts) a.workspace[(int64_t)blockIdx.x * a.experts + threadIdx.x] = pairs_of(s, threadIdx.x, words);
         return;
     }
-    int all = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += kRouteThreads) {
-        const int e = e0 + threadIdx.x, own = e < a.experts ? pairs_of(s, e, words) : 0;
-        const int begin = before_expert(s, own, all, all);
-        if (e < a.experts) {
-            s.before[e] = begin;
-            a.offsets[e] = begin;
-        }
+    int all;
+    const int begin = before_expert(s, threadIdx.x < a.experts ? pairs_of(s, threadIdx.x, words) : 0, all);
+    if (threadIdx.x < a.experts) {
+        s.before[threadIdx.x] = begin;
+        a.offsets[threadIdx.x] = begin;
     }
     if (threadIdx.x == 0) a.offsets[a.experts] = all;
     __syncthreads();
@@ -260,32 +256,29 @@ __global__ void __launch_bounds__(kRouteThreads) place_kernel(const ar_route_exp
         s.ids[i] = (int16_t)id;
         note_pair(s, id, i / a.chosen, words);
     }
-    int all = 0;
-    for (int e0 = 0; e0 < a.experts; e0 += kRouteThreads) {
-        // as many threads to an expert as there are, each with some of the blocks
-        const int wide = min(a.experts - e0, kRouteThreads), each = kRouteThreads / wide, e = threadIdx.x % wide, part = threadIdx.x / wide;
-        const int b0 = blocks * part / each, b1 = part < each ? blocks * (part + 1) / each : b0;
-        int sum = 0, past = 0;
+    // as many threads to an expert as there are, each with some of the blocks
+    const int wide = a.experts, each = kRouteThreads / wide, e = threadIdx.x % wide, part = threadIdx.x / wide;
+    const int b0 = blocks * part / each, b1 = part < each ? blocks * (part + 1) / each : b0;
+    int sum = 0, past = 0, all;
 #pragma unroll 32
-        for (int b = b0; b < b1; ++b) {
-            const int c = a.workspace[(int64_t)b * a.experts + e0 + e];
-            sum += c;
-            if (b < blockIdx.x) past += c;
+    for (int b = b0; b < b1; ++b) {
+        const int c = a.workspace[(int64_t)b * wide + e];
+        sum += c;
+        if (b < blockIdx.x) past += c;
+    }
+    parts[0][threadIdx.x] = sum;
+    parts[1][threadIdx.x] = past;
+    __syncthreads();
+    sum = past = 0;
+    if (threadIdx.x < wide)
+        for (int q = 0; q < each; ++q) {
+            sum += parts[0][q * wide + threadIdx.x];
+            past += parts[1][q * wide + threadIdx.x];
         }
-        parts[0][threadIdx.x] = sum;
-        parts[1][threadIdx.x] = past;
-        __syncthreads();
-        sum = past = 0;
-        if (threadIdx.x < wide)
-            for (int q = 0; q < each; ++q) {
-                sum += parts[0][q * wide + threadIdx.x];
-                past += parts[1][q * wide + threadIdx.x];
-            }
-        const int begin = before_expert(s, sum, all, all);
-        if (threadIdx.x < wide) {
-            s.before[e0 + threadIdx.x] = begin + past;
-            if (blockIdx.x == 0) a.offsets[e0 + threadIdx.x] = begin;
-        }
+    const int begin = before_expert(s, sum, all);
+    if (threadIdx.x < wide) {
+        s.before[threadIdx.x] = begin + past;
+        if (blockIdx.x == 0) a.offsets[threadIdx.x] = begin;
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) a.offsets[a.experts] = all;
     __syncthreads();
