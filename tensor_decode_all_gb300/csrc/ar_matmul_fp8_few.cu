@@ -29,7 +29,8 @@ template <int TOK> struct Few {
     static constexpr int Buffers = TOK <= 64 ? 4 : 2;                 // of sums in tensor memory
     static constexpr int Columns = TOK * Buffers;
     static constexpr int StageBytes = WeightBytes + RowBytes;
-    // Two blocks to a multiprocessor; with 128 rows one, whose sums are eight warps' (with four they would not fit their registers).
+    // Two blocks to a multiprocessor; with 128 rows one, whose sums are eight warps' (with four they would not fit their registers; with
+    // eight 44 to 48 bytes of a thread still do not).
     static constexpr int Blocks = TOK <= 64 ? 2 : 1, Halves = TOK <= 64 ? 1 : 2, Own = TOK / Halves;
     static constexpr int Threads = 64 + 128 * Halves;               // copies, instructions, warps that add up
     static constexpr int Stages = (224 * 1024 / Blocks - 4 * ScaleBytes) / (StageBytes + ScaleBytes);
@@ -333,7 +334,7 @@ cudaError_t start_few_of(const Product &p, cudaStream_t s, int multiprocessors) 
     CUtensorMap weight, x;
     if (!map_weight(&weight, p.a, kBlock) || !map_rows(&x, p.a, TOK)) return cudaErrorInvalidValue;
     const int64_t room = (int64_t)F::Blocks * multiprocessors;
-    // Blocks to share a tile's channels, as long as all tiles' run at the same time and each has four groups or more.
+    // Blocks to share a tile's channels, as long as all tiles' run at the same time and each has two groups or more.
     int cluster = 1;
     while (cluster < 16 && units * cluster * 2 <= room && p.groups >= cluster * 4) {
         int most = 0;
