@@ -438,7 +438,13 @@ bool may_share(const Tensor &a, const Tensor &b) {
     };
     if (a.numel() == 0 || b.numel() == 0) return false;
     const auto x = range(a), y = range(b);
-    return x.first < y.second && y.first < x.second;
+    if (!(x.first < y.second && y.first < x.second)) return false;
+    // columns of the same rows, side by side: where b's begin after a's in a row, and whether they end before a's next
+    if (a.dim() != 2 || b.dim() != 2 || a.size(0) < 2 || b.size(0) < 2) return true;
+    const int64_t row = a.stride(0) * (int64_t)a.element_size(), wide_a = a.size(1) * (int64_t)a.element_size(), wide_b = b.size(1) * (int64_t)b.element_size();
+    if (row <= 0 || row != b.stride(0) * (int64_t)b.element_size()) return true;
+    const int64_t at = (((y.first - x.first) % row) + row) % row;
+    return at < wide_a || at + wide_b > row;
 }
 
 // matmul(x, x_scales, weight, weight_scales, offsets | None, rows | None, out | None, dtype | None) -> out

@@ -844,6 +844,32 @@ def test_a_stream_of_the_callers():
         H.check_product(out, x, xs, w, ws)
 
 
+def test_outputs_beside_their_inputs():
+    """Columns of one buffer's rows are no overlap; columns that they share are one."""
+    tda = _tda()
+    x = torch.randn(30, 64, generator=H.gen(1)).to(torch.bfloat16)
+    w, place = torch.rand(20, 3, generator=H.gen(2)), torch.randint(0, 30, (20, 3), generator=H.gen(3)).int()
+    for at, first in ((0, 64), (64, 0), (72, 0), (0, 72), (72, 8)):
+        room = torch.zeros(30, 136, dtype=torch.bfloat16, device="cuda")
+        view = room[:, first:first + 64]
+        view.copy_(x)
+        out = room[4:24, at:at + 64]
+        assert tda.experts_sum(view, w.cuda(), place.cuda(), out=out) is out
+        H.check_weighted(out, x, w, place)
+        assert torch.equal(view.cpu(), x)
+        for a in (1, 63):
+            near = room[4:24, abs(first - a):abs(first - a) + 64]
+            with pytest.raises(ValueError, match="overlaps"):
+                tda.experts_sum(view, w.cuda(), place.cuda(), out=near)
+    wide = torch.zeros(40, 512, dtype=torch.uint8, device="cuda")
+    x, xs, wt, ws = _operands(4, 40, 64, 256)
+    x8 = wide[:, :256].view(F8)
+    wide[:, :256].copy_(x.view(torch.uint8))
+    out = wide[:, 256:384].view(torch.bfloat16)
+    tda.matmul_fp8(x8, xs.cuda(), wt.cuda(), ws.cuda(), out=out)
+    H.check_product(out, x, xs, wt, ws)
+
+
 def test_refusals_on_the_gpu():
     tda = _tda()
     x, xs, w, ws = (t.cuda() for t in _operands(1, 4, 128, 256))
