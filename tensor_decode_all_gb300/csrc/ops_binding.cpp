@@ -495,10 +495,11 @@ PyObject *matmul(PyObject *const *o) {
         if (may_share(out, x) || may_share(out, xs) || may_share(out, w) || may_share(out, ws)) refuse("out", "overlaps an input");
     }
     if (K > kInt || F > kInt) refuse("weight", "too large");
+    // (no rows: an empty tensor has no address by which the call would see that rows are picked)
     a.x = x.data_ptr(); a.x_scales = static_cast<float *>(xs.data_ptr()); a.weight = w.data_ptr();
     a.weight_scales = static_cast<float *>(ws.data_ptr()); a.out = out.data_ptr();
     a.x_stride = x.stride(0); a.x_scales_stride = xs.stride(0); a.weight_stride = w.stride(lead); a.expert_stride = experts ? w.stride(0) : 0;
-    a.out_stride = out.stride(0); a.rows = rows; a.x_rows = N; a.dtype = code_16("out", out); a.out_dim = (int32_t)F; a.dim = (int32_t)K;
+    a.out_stride = out.stride(0); a.rows = rows; a.x_rows = rows ? N : 0; a.dtype = code_16("out", out); a.out_dim = (int32_t)F; a.dim = (int32_t)K;
     a.experts = (int32_t)std::min(E, kInt); a.x_row_scales = row_scales;
     Tensor room;
     if (const size_t bytes = ar_matmul_fp8_workspace(&a)) {

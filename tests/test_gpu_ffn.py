@@ -430,6 +430,18 @@ def test_picked_rows_without_a_workspace():
     H.check_product(tda.matmul_fp8(*dev[:4], rows=dev[4]), x.view(torch.uint8)[rows.long()].view(F8), xs[rows.long()], w, ws)
 
 
+def test_no_rows_picked():
+    """An empty `rows`: an empty result, as of a step in which no request needs its logits."""
+    tda = _tda()
+    x, xs, w, ws = (t.cuda() for t in _operands(1, 7, 64, 256, 3))
+    none = _i32([])
+    assert tda.matmul_fp8(x, xs, w[0], ws[0], rows=none).shape == (0, 64)
+    out = torch.empty(0, 64, dtype=torch.float16, device="cuda")
+    assert tda.matmul_fp8(x, xs, w[0], ws[0], rows=none, out=out) is out
+    assert tda.experts_matmul_fp8(x, xs, w, ws, _i32([0] * 4), rows=none).shape == (0, 64)
+    assert tda.matmul_fp8(x[:0], xs[:0], w[0], ws[0], rows=none).shape == (0, 64)
+
+
 @pytest.mark.parametrize("n", [1, 20, 100, 900])
 @pytest.mark.parametrize("K", [512, 130 * 16, 250])
 def test_products_of_picked_rows(n, K):
