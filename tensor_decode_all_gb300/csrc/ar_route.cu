@@ -13,8 +13,8 @@
 // blocks, each with a run of the pairs, each warp of it with a part of that run: count by warp and expert, add up over warps
 // and blocks (through the cluster's shared memory), then go over the pairs again.
 //
-// 8191 tokens to 8 of 256 experts take 18 to 19 us in GB300 graph replays (the choice 13 us by itself, two thirds of the cycles issue an
-// instruction, some 800 to a token; the places 10), where the sort took 22 besides the choice; 5 tokens to 4 of 32, in one block, 2.5 us.
+// 8191 tokens to 8 of 256 experts take 17.1 us in GB300 graph replays (the choice 13 us by itself, two thirds of the cycles issue an
+// instruction, some 800 to a token; the places 10), where the sort took 22 besides the choice; 5 tokens to 4 of 32, in one block, 2.2 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
