@@ -295,12 +295,12 @@ __global__ void __launch_bounds__(Few<TOK>::Threads, Few<TOK>::Blocks) few_kerne
 // of them (15 of 8 blocks, not 19, with a block to a multiprocessor; the runtime counts one to a multiprocessor).
 template <int TOK, bool kPicked> cudaError_t clusters_at_once(int cluster, int *most) {
     using F = Few<TOK>;
-    static int known[64][5] = {};
+    static int known[64][5] = {};          // (one more: 0 is not known, and none can be the answer)
     int dev = 0, log = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     while (1 << log < cluster) ++log;
-    if (dev < 64 && (*most = *(volatile int *)&known[dev][log]) > 0) return cudaSuccess;
+    if (dev < 64 && (*most = *(volatile int *)&known[dev][log] - 1) >= 0) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)cluster);
     cfg.blockDim = dim3(F::Threads);
@@ -313,7 +313,7 @@ template <int TOK, bool kPicked> cudaError_t clusters_at_once(int cluster, int *
     cfg.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(most, few_kernel<TOK, kPicked>, &cfg);
     *most *= F::Blocks;
-    if (e == cudaSuccess && dev < 64) *(volatile int *)&known[dev][log] = std::max(*most, 1);
+    if (e == cudaSuccess && dev < 64) *(volatile int *)&known[dev][log] = *most + 1;
     return e;
 }
 
